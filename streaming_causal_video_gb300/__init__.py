@@ -34,4 +34,17 @@ from ._binding import (  # noqa: F401
     workspace_bytes,
     workspace_init,
 )
+from ._block import (  # noqa: F401
+    BF16,
+    F32,
+    CrossConfig,
+    NormConfig,
+    cross_attention,
+    cross_attention_backward,
+    cross_workspace_bytes,
+    cross_workspace_init,
+    layer_norm,
+    layer_norm_backward,
+    norm_workspace_bytes,
+)
 from .layer import LayerCache, StreamSession  # noqa: F401

@@ -216,6 +216,7 @@ uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 int64_t debug_drop_tile() { return g_drop_tile.load(); }
 int debug_force_splits() { return g_force_splits.load(); }
 void set_last_kv_splits(int splits) { g_last_splits = splits; }
+sdv2_status require_device() { return check_device(); }
 }  // namespace sdv2
 
 extern "C" {

@@ -184,6 +184,9 @@ int64_t debug_drop_tile();
 int debug_force_splits();
 void set_last_kv_splits(int splits);
 
+// SDV2_OK if the current device is an sm_103 (looked up once per device), else the status with its message.
+sdv2_status require_device();
+
 // Largest chunk index the entry points accept (frame numbers c*F stay far inside int64).
 constexpr int64_t kMaxChunkIndex = int64_t(1) << 40;
 
