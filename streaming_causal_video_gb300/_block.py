@@ -1,6 +1,8 @@
 """ctypes binding of the operators in include/sdv2_block.h (argument marshalling only)."""
 import ctypes
 
+import torch
+
 from . import _binding as _b
 
 BF16, F32 = 0, 1               # sdv2_dtype
@@ -60,34 +62,49 @@ def _lib():
     return L
 
 
+# The current device and its current stream as integers.  torch's own accessors build a Python object
+# per call, which costs more than a small kernel; its raw ones are used where the build has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_current_device())
+    return _b._stream(stream)
+
+
 class _Operands:
     """Pointers of one call's tensors, each checked for its type, its extent and its device: one CUDA
     device, the current one.  Raw integer pointers and None pass through unchecked."""
+    __slots__ = ("device",)
 
     def __init__(self):
-        self.device = None
+        self.device = -1
 
     def __call__(self, t, name, dtype, nbytes, dense=False):
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             return t
-        p = _b._dev(t, name, nbytes)
-        kind = str(t.dtype)
-        if kind != dtype:
-            raise ValueError("%s must be %s, got %s" % (name, dtype, kind))
-        if dense and not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        if self.device is None:
-            import torch
-            self.device = t.device.index
-            if self.device != torch.cuda.current_device():
-                raise ValueError("%s is on device %d, the current device is %d" %
-                                 (name, self.device, torch.cuda.current_device()))
-        elif t.device.index != self.device:
-            raise ValueError("%s is on device %d, not on device %d" % (name, t.device.index, self.device))
-        return p
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        device = t.get_device()
+        if device != self.device:
+            if self.device >= 0:
+                raise ValueError("%s is on device %d, not on device %d" % (name, device, self.device))
+            if device != _current_device():
+                raise ValueError("%s is on device %d, the current device is %d" % (name, device, _current_device()))
+            self.device = device
+        if not t.is_contiguous():
+            if dense:
+                raise ValueError("%s must be contiguous" % name)
+        elif t.nbytes >= nbytes:
+            return t.data_ptr()
+        return _b._dev(t, name, nbytes)
 
 
-_BF, _FP, _U8 = "torch.bfloat16", "torch.float32", "torch.uint8"
+_BF, _FP, _U8 = torch.bfloat16, torch.float32, torch.uint8
 _TYPE = {BF16: (_BF, 2), F32: (_FP, 4)}
 
 
@@ -100,7 +117,7 @@ def norm_workspace_bytes(cfg: NormConfig) -> int:
 
 
 def cross_workspace_init(cfg, ws, stream=None):
-    _b._check(_lib().sdv2_cross_workspace_init(ctypes.byref(cfg), _Operands()(ws, "ws", _U8, 256), _b._stream(stream)),
+    _b._check(_lib().sdv2_cross_workspace_init(ctypes.byref(cfg), _Operands()(ws, "ws", _U8, 256), _stream(stream)),
               "sdv2_cross_workspace_init")
 
 
@@ -120,13 +137,12 @@ def _span(batch, length, heads, st):
 def _cross_operand(op, t, name, batch, length, heads, st):
     """A [B][length][heads][128] view must have the configuration's strides; a tensor of another rank is
     a buffer that they are applied to."""
-    if t is not None and not isinstance(t, int) and t.dim() == 4:
-        if tuple(t.shape) != (batch, length, heads, 128):
+    if t is not None and type(t) is not int and t.dim() == 4:
+        if t.shape != (batch, length, heads, 128):
             raise ValueError("%s is %s, the configuration says %s" % (name, tuple(t.shape), (batch, length, heads, 128)))
-        want = (st[2], st[0], st[1], 1)
-        for size, have, need in zip(t.shape, t.stride(), want):
-            if size > 1 and have != need:
-                raise ValueError("%s has strides %s, the configuration says %s" % (name, tuple(t.stride()), want))
+        want, have = (st[2], st[0], st[1], 1), t.stride()
+        if want != have and any(n > 1 and w != h for n, w, h in zip(t.shape, want, have)):
+            raise ValueError("%s has strides %s, the configuration says %s" % (name, have, want))
     return op(t, name, _BF, _span(batch, length, heads, st))
 
 
@@ -150,7 +166,7 @@ def cross_attention(cfg, q, k, v, out, ws, kv_lens=None, lse=None, scale=0.0, st
     _b._check(_lib().sdv2_cross_attention(ctypes.byref(cfg), _lens(cfg, kv_lens), *_cross_inputs(cfg, op, q, k, v),
                                           float(scale), op(out, "out", _BF, rows * 256, True),
                                           op(lse, "lse", _FP, rows * 4, True),
-                                          op(ws, "ws", _U8, 256), _b._stream(stream)), "sdv2_cross_attention")
+                                          op(ws, "ws", _U8, 256), _stream(stream)), "sdv2_cross_attention")
 
 
 def cross_attention_backward(cfg, q, k, v, out, lse, dout, dq, dk, dv, ws, kv_lens=None, scale=0.0, stream=None):
@@ -164,15 +180,15 @@ def cross_attention_backward(cfg, q, k, v, out, lse, dout, dq, dk, dv, ws, kv_le
         op(lse, "lse", _FP, rows * 4, True), op(dout, "dout", _BF, rows * 256, True), float(scale),
         op(dq, "dq", _BF, rows * 256, True), op(dk, "dk", _BF, kv_rows * 256, True),
         op(dv, "dv", _BF, kv_rows * 256, True), op(ws, "ws", _U8, cross_workspace_bytes(cfg, True)),
-        _b._stream(stream)), "sdv2_cross_attention_backward")
+        _stream(stream)), "sdv2_cross_attention_backward")
 
 
 def _rows(cfg, op, t, name, dtype, stride):
     """Rows of x or y: a 2-D tensor must be [rows][cols] with the configuration's row stride."""
     kind, size = _TYPE.get(dtype, (None, 4))
     stride = stride or cfg.cols
-    if t is not None and not isinstance(t, int) and t.dim() == 2:
-        if tuple(t.shape) != (cfg.rows, cfg.cols) or (cfg.cols > 1 and t.stride(1) != 1) or \
+    if t is not None and type(t) is not int and t.dim() == 2:
+        if t.shape != (cfg.rows, cfg.cols) or (cfg.cols > 1 and t.stride(1) != 1) or \
                 (cfg.rows > 1 and t.stride(0) != stride):
             raise ValueError("%s is %s with strides %s, the configuration says %s and row stride %d" %
                              (name, tuple(t.shape), tuple(t.stride()), (cfg.rows, cfg.cols), stride))
@@ -193,7 +209,7 @@ def layer_norm(cfg, x, y, weight=None, bias=None, mean=None, rstd=None, stream=N
                                      op(weight, "weight", _FP, par), op(bias, "bias", _FP, par),
                                      _rows(cfg, op, y, "y", cfg.y_dtype, cfg.y_row_stride),
                                      op(mean, "mean", _FP, cfg.rows * 4, True), op(rstd, "rstd", _FP, cfg.rows * 4, True),
-                                     _b._stream(stream)), "sdv2_layer_norm")
+                                     _stream(stream)), "sdv2_layer_norm")
 
 
 def layer_norm_backward(cfg, dy, x, mean, rstd, dx, ws, weight=None, dweight=None, dbias=None, stream=None):
@@ -209,4 +225,4 @@ def layer_norm_backward(cfg, dy, x, mean, rstd, dx, ws, weight=None, dweight=Non
         _rows(cfg, op, dx, "dx", cfg.x_dtype, cfg.x_row_stride), op(dweight, "dweight", _FP, grads, True),
         op(dbias, "dbias", _FP, grads, True),
         op(ws, "ws", _U8, norm_workspace_bytes(cfg) if (dweight is not None or dbias is not None) else 0),
-        _b._stream(stream)), "sdv2_layer_norm_backward")
+        _stream(stream)), "sdv2_layer_norm_backward")

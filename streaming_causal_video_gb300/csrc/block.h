@@ -47,6 +47,12 @@ struct CrossBackward {
     float* delta;              // [B][H][Nq] scratch
 };
 
+// Heads that share a key head and a 128-row query tile: the largest divisor of `group` up to 128.
+int cross_pack(int group);
+
+// Query tiles of 128 rows on the tensor cores.
+cudaError_t launch_cross_attention(const CrossForward& p, cudaStream_t s);
+
 // Query rows on the CUDA cores (any size; fast for a few queries).
 cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s);
 cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s);

@@ -204,7 +204,9 @@ sdv2_status sdv2_cross_attention(const sdv2_cross_cfg* c, const int64_t* kv_lens
         const int64_t rows = static_cast<int64_t>(b0) * c->heads * c->q_len;
         p.out = static_cast<uint16_t*>(out) + rows * 128;
         p.lse = lse ? lse + rows : nullptr;
-        const cudaError_t e = launch_cross_rows(p, static_cast<cudaStream_t>(stream));
+        const bool few = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq <= 4;
+        const cudaError_t e = few ? launch_cross_rows(p, static_cast<cudaStream_t>(stream))
+                                  : launch_cross_attention(p, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return done(e, "cross attention launch");
     }
     return done(cudaSuccess, "");

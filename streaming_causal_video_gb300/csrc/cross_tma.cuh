@@ -1,0 +1,42 @@
+// Tensor maps and loads of the cross attention kernels: operands with token, head and batch strides.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "block.h"
+#include "ptx.cuh"
+
+namespace sdv2 {
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Bring a box to L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2, int32_t c3)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
+// Writes of generic stores to shared memory become visible to the async proxy (TMA, tensor cores).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Queries (or their gradient): (D, heads, tokens, batch), boxes of 64 dims x `heads_box` heads x
+// `tokens_box` tokens, whose rows arrive token-major.  Tokens past the end arrive as zeros.
+bool encode_query_map(CUtensorMap* map, const void* base, int heads, int64_t tokens, int batch, const CrossStrides& st,
+                      int heads_box, int tokens_box);
+
+// Keys or values of one stream: (D, heads, rows), boxes of 64 dims x 1 head x 128 rows.  Rows past
+// `rows` arrive as zeros, so what lies behind a stream's last row is never read.
+bool encode_key_map(CUtensorMap* map, const void* base, int heads, int64_t rows, const CrossStrides& st);
+
+}  // namespace sdv2

@@ -146,14 +146,14 @@ class FakeTensor:
             need = sum((n - 1) * s for n, s in zip(shape, strides)) + 1
             self._t = torch.empty(need, dtype=dtype).as_strided(shape, strides)
         self.dtype, self.shape, self.is_cuda = dtype, self._t.shape, True
-        self.device = torch.device("cuda", device)
+        self.get_device = lambda: device
 
     def __getattr__(self, name):
         return getattr(self._t, name)
 
 
 def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_block, "_current_device", lambda: 0)
     c = cross()
     q, k, v, out = (FakeTensor(s) for s in ((2, 5, 4, 128), (2, 7, 2, 128), (2, 7, 2, 128), (2, 5, 4, 128)))
     ws = FakeTensor((256,), torch.uint8)
@@ -174,10 +174,10 @@ def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
                      (dict(q=torch.empty((2, 5, 4, 128), dtype=torch.bfloat16)), "q must be a CUDA tensor")):
         with pytest.raises(ValueError, match=match):
             call(**o)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(_block, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="the current device is 1"):
         call()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_block, "_current_device", lambda: 0)
     n = norm(rows_per_group=4)
     x, y = FakeTensor((6, 40)), FakeTensor((6, 40))
     w = FakeTensor((2, 40), torch.float32)

@@ -279,6 +279,26 @@ def test_two_streams_with_their_own_workspaces():
         c.check_backward()
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The copy of one key tile is left out: the waits for it run out, the kernel returns, the error word says
+    so, and the workspace serves the next call."""
+    c = Cross(2, 3, 3, 300, 500, [500, 400], seed=8)
+    few = Cross(1, 2, 2, 20, 900, [900], seed=8)          # key ranges shared by a cluster
+    for case in (c, few):
+        try:
+            sd.set_wait_timeout_ns(50_000_000)
+            sd.debug_drop_kv_tile(1)
+            case.forward()
+            with pytest.raises(sd.SDV2Error) as e:
+                sd.check_device_error(case.ws)
+            assert e.value.status == 4
+        finally:
+            sd.debug_drop_kv_tile(-1)
+            sd.set_wait_timeout_ns(2_000_000_000)
+        case.forward()
+        case.check_forward()
+
+
 def test_cross_gradients_against_differences():
     """<gradient, direction> against central differences of the 64-bit forward."""
     c = Cross(1, 2, 1, 150, 200, [200], seed=31)
