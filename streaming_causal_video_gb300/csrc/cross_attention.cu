@@ -20,7 +20,7 @@
 //
 // Roles in a CTA (12 warps):
 //   warps 0-3, 4-7: softmax of lane 0, 1; thread = query row.  Then the row's epilogue.
-//   warp 8: K tiles (3 slots); 10: V tiles (2 slots); 11: Q tiles (1 slot per lane).
+//   warp 8: K tiles (2 slots); 10: V tiles (2 slots); 11: Q tiles (1 slot per lane).
 //   warp 9: issues S_t = Q_t K^T and O_t += P_t V.
 // Nothing is drained between items: a lane's next Q is loaded when its last S is done, its next S
 // is issued behind its last PV, and the tensor cores run the other lane meanwhile.
@@ -39,7 +39,7 @@ namespace sdv2 {
 namespace {
 
 constexpr int BM = 128, BN = 128, HD = 128;
-constexpr int KST = 3, VST = 2;
+constexpr int KST = 2, VST = 2;
 constexpr uint32_t TILE = 128 * HD * 2;
 constexpr uint32_t HALF = TILE / 2;           // 64 dims of 128 rows
 constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10, Q_WARP = 11;
@@ -47,11 +47,13 @@ constexpr int NTHREADS = 12 * 32;
 constexpr uint32_t TMEM_COLS = 512;           // S_0 | S_1 | O_0 | O_1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxCtas = 160;
 
 enum Bar { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = KFULL + KST, VFULL = KEMPTY + KST, VEMPTY = VFULL + VST,
-           SFULL = VEMPTY + VST, PFULL = SFULL + 2, OFULL = PFULL + 2, MMADONE = OFULL + 2, NBARS = MMADONE + 1 };
+           SFULL = VEMPTY + VST, PFULL = SFULL + 2, OFULL = PFULL + 2,
+           MMADONE = OFULL + 2, NBARS = MMADONE + 1 };
 
-constexpr uint32_t SMEM_TILES = (2 + KST + VST) * TILE;
+constexpr uint32_t SMEM_TILES = (2 + KST + VST + 1) * TILE;   // Q, K, V, and half an output tile per lane
 constexpr uint32_t SMEM_STATS = 2 * BM * 8;   // (max, sum) of every row and lane
 constexpr uint32_t SMEM_USED = SMEM_TILES + SMEM_STATS + 256;
 constexpr uint32_t SMEM_BYTES = 232448;       // all of it: 768 bytes are left to align the tiles with
@@ -59,7 +61,7 @@ static_assert(SMEM_USED + 768 <= SMEM_BYTES && NBARS * 8 + 8 <= 256, "shared mem
 
 template <int CAP>
 struct Params {
-    CUtensorMap qmap;
+    CUtensorMap qmap, omap;
     CUtensorMap kmap[CAP], vmap[CAP];
     int32_t n[CAP];
     uint16_t* out;
@@ -69,8 +71,11 @@ struct Params {
     int64_t drop_tile;
     int32_t B, H, Hk, Nq;
     int32_t pack, tokens;                     // heads and tokens of a tile
+    int32_t packs;                            // packs of heads of a stream
+    int32_t group;                            // query heads of a key head
     int32_t tiles;                            // query tiles of one (stream, pack of heads)
-    int32_t splits;                           // CTAs of a cluster that share a tile
+    int32_t split_shift;                      // log2 of the CTAs of a cluster that share a tile's keys
+    int32_t start[kMaxCtas + 1];              // first query tile of every CTA (not of clusters)
     float scale_log2;
 };
 
@@ -81,63 +86,60 @@ struct Item {
     int keys, k0;                             // key tiles of the item, the first one
     __device__ int steps(int t) const { return pair ? keys : (t == 0 ? (keys + 1) / 2 : keys / 2); }
     __device__ int first(int t) const { return pair || t == 0 ? k0 : k0 + (keys + 1) / 2; }
-    __device__ bool owns(int t) const { return pair || t == 0; }
 };
 
+// Key tiles of stream b.
 template <int CAP>
 __device__ __forceinline__ int key_tiles(const Params<CAP>& p, int b) { return (p.n[b] + BN - 1) / BN; }
 
-// First query tile at or past `x` units of cost.
-template <int CAP>
-__device__ __forceinline__ int tile_at(const Params<CAP>& p, int64_t x)
-{
-    const int per_stream = p.tiles * (p.H / p.pack);
-    int64_t cost = 0;
-    for (int b = 0; b < p.B; ++b) {
-        const int64_t w = key_tiles(p, b) + 1;
-        if (x <= cost + w * per_stream) return b * per_stream + static_cast<int>((x - cost + w - 1) / w);
-        cost += w * per_stream;
-    }
-    return p.B * per_stream;
-}
-
-template <int CAP>
+// The CTA's items.  The start is decoded once; from then on the walk only counts, because a division
+// by a launch parameter in every role and item cost more than the key tiles of a short prompt.
 struct Walk {
-    int cur, end;
+    int b, h0, tile, left;                    // next query tile, tiles left
+    template <int CAP>
     __device__ explicit Walk(const Params<CAP>& p)
     {
-        if (p.splits > 1) {
-            cur = blockIdx.x / p.splits;
-            end = cur + 1;
-            return;
-        }
-        int64_t total = 0;
-        for (int b = 0; b < p.B; ++b) total += static_cast<int64_t>(key_tiles(p, b) + 1) * p.tiles * (p.H / p.pack);
-        cur = tile_at(p, total * blockIdx.x / gridDim.x);
-        end = tile_at(p, total * (blockIdx.x + 1) / gridDim.x);
+        const uint32_t cta = p.split_shift ? blockIdx.x >> p.split_shift : blockIdx.x;
+        const uint32_t cur = p.split_shift ? cta : static_cast<uint32_t>(p.start[cta]);
+        left = p.split_shift ? 1 : p.start[cta + 1] - static_cast<int>(cur);
+        const uint32_t group = cur / static_cast<uint32_t>(p.tiles);
+        tile = static_cast<int>(cur - group * p.tiles);
+        const uint32_t bb = group / static_cast<uint32_t>(p.packs);
+        b = static_cast<int>(bb);
+        h0 = static_cast<int>(group - bb * p.packs) * p.pack;
     }
-    __device__ bool next(const Params<CAP>& p, Item& it)
-    {
-        if (cur >= end) return false;
-        peek(p, it);
-        cur += it.pair ? 2 : 1;
-        return true;
-    }
+    template <int CAP>
     __device__ void peek(const Params<CAP>& p, Item& it) const
     {
-        const int group = cur / p.tiles;      // (stream, pack of heads)
-        const int packs = p.H / p.pack;
-        it.tile = cur - group * p.tiles;
-        it.b = group / packs;
-        it.h0 = (group - it.b * packs) * p.pack;
-        it.keys = key_tiles(p, it.b);
+        it.b = b;
+        it.h0 = h0;
+        it.tile = tile;
+        it.keys = key_tiles(p, b);
         it.k0 = 0;
-        it.pair = p.splits == 1 && cur + 1 < end && it.tile + 1 < p.tiles;
-        if (p.splits > 1) {
-            const int r = blockIdx.x % p.splits, all = it.keys;
-            it.k0 = all * r / p.splits;
-            it.keys = all * (r + 1) / p.splits - it.k0;
+        it.pair = left > 1 && tile + 1 < p.tiles;
+        if (p.split_shift) {
+            const int r = blockIdx.x & ((1 << p.split_shift) - 1), all = it.keys;
+            it.k0 = (all * r) >> p.split_shift;
+            it.keys = ((all * (r + 1)) >> p.split_shift) - it.k0;
         }
+    }
+    template <int CAP>
+    __device__ bool next(const Params<CAP>& p, Item& it)
+    {
+        if (left <= 0) return false;
+        peek(p, it);
+        const int k = it.pair ? 2 : 1;
+        left -= k;
+        tile += k;
+        if (tile == p.tiles) {
+            tile = 0;
+            h0 += p.pack;
+            if (h0 == p.H) {
+                h0 = 0;
+                ++b;
+            }
+        }
+        return true;
     }
 };
 
@@ -147,6 +149,10 @@ __device__ __forceinline__ void give_up(volatile int* abort_flag, uint32_t* err)
     atomicOr(err, kErrTimeout);
 }
 
+// Barrier of lane t's softmax warpgroup.
+__device__ __forceinline__ void lane_barrier(int t) { asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory"); }
+
+// Barrier of both.
 __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
         if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
         return;
     }
-    const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * TILE, sV = sK + KST * TILE;
+    const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * TILE, sV = sK + KST * TILE, sO = sV + VST * TILE;
     float2* stats = reinterpret_cast<float2*>(smem + SMEM_TILES);               // [2][128]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SMEM_TILES + SMEM_STATS);
     const uint32_t bar0 = smem_u32(bars);
@@ -186,29 +192,38 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
+    const int splits = 1 << p.split_shift;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i >= PFULL && i < PFULL + 2 ? 128 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    // rows of a Q tile that no load writes (the pack does not divide 128): zero, so that they stay finite
+    // The load warps only need the barriers: they start while the rest of the block is still setting up.
     const int used_rows = p.pack * p.tokens;
-    for (int i = threadIdx.x; i < (BM - used_rows) * 32; i += NTHREADS) {
-        const int part = i & 31, row = used_rows + (i >> 5);                   // 2 tiles x 2 halves x 8 vectors
-        *reinterpret_cast<uint4*>(smem + (part >> 4) * TILE + ((part >> 3) & 1) * HALF + row * 128 + (part & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+    if (warp >= K_WARP) {
+        if (threadIdx.x == K_WARP * 32) {
+            for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i >= PFULL && i < PFULL + 2 ? 128 : 1);
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        asm volatile("bar.sync 4, 128;" ::: "memory");
+    } else {
+        // rows of a Q tile that no load writes (the pack does not divide 128): zero, so that they stay finite
+        for (int i = threadIdx.x; i < (BM - used_rows) * 32; i += K_WARP * 32) {
+            const int part = i & 31, row = used_rows + (i >> 5);               // 2 tiles x 2 halves x 8 vectors
+            *reinterpret_cast<uint4*>(smem + (part >> 4) * TILE + ((part >> 3) & 1) * HALF + row * 128 + (part & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
     }
-    fence_proxy_async();
-    if (warp == MMA_WARP) {
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
+    uint32_t tmem = 0;
+    if (warp <= MMA_WARP && warp != K_WARP) {
+        if (warp == MMA_WARP) {
+            tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 5, 288;" ::: "memory");         // softmax warps and the MMA warp
+        tc_fence_after();
+        tmem = *tmem_slot;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    Walk<CAP> walk(p);
+    Walk walk(p);
     Item it;
     bool ok = true;
 
@@ -223,7 +238,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
             uint32_t phase = 0, pending = 0;
             while (ok && walk.next(p, it)) {
                 const CUtensorMap* map = is_k ? &p.kmap[it.b] : &p.vmap[it.b];
-                const int hk = it.h0 / (p.H / p.Hk);
+                const int hk = p.group == 1 ? it.h0 : it.h0 / p.group;
                 for (int i = 0; i < it.keys; ++i) {
                     // a single's lanes alternate
                     const int j = it.pair ? it.k0 + i : it.first(i & 1) + (i >> 1);
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
                         tma_load_4d(sQ + t * TILE + hf * HALF, &p.qmap, bar(QFULL + t), hf * 64, it.h0, tok, it.b);
                     ++loads[t];
                 }
-                Walk<CAP> ahead = walk;        // the next item's queries reach L2 while this one runs
+                Walk ahead = walk;        // the next item's queries reach L2 while this one runs
                 Item nx;
                 if (ok && ahead.next(p, nx) && nx.keys > 0)
                     for (int t = 0; t < (nx.pair ? 2 : 1); ++t)
@@ -285,11 +300,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
         };
         int kslot = 0, vslot = 0;             // slots of the tile that the next S, PV uses
         uint32_t kph = 0, vph = 0;
+        bool knew = true, vnew = true;        // a wait costs 100 cycles even when the tile is there: once a slot
         uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
         // S_t of the lane's next step; `release`: no other lane uses the key tile after it
         auto issue_s = [&](int t, bool first, bool last, bool release) {
             if (first && !wait(QFULL + t, qn[t] & 1u)) return;
-            if (!wait(KFULL + kslot, kph)) return;
+            if (knew && !wait(KFULL + kslot, kph)) return;
+            knew = false;
             tc_fence_after();
             const uint64_t a0 = dQ + static_cast<uint64_t>(t) * kTileStep, b0 = dK + static_cast<uint64_t>(kslot) * kTileStep;
 #pragma unroll
@@ -304,6 +321,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
             }
             if (release) {
                 mma_commit_warp(bar(KEMPTY + kslot));
+                knew = true;
                 if (++kslot == KST) {
                     kslot = 0;
                     kph ^= 1u;
@@ -323,7 +341,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
                 for (int t = 0; ok && t < 2; ++t) {
                     const int nt = t ? n1 : n0;
                     if (j >= nt) continue;
-                    if (!wait(VFULL + vslot, vph) || !wait(PFULL + t, pn[t] & 1u)) break;
+                    if (vnew && !wait(VFULL + vslot, vph)) break;
+                    vnew = false;
+                    if (!wait(PFULL + t, pn[t] & 1u)) break;
                     ++pn[t];
                     tc_fence_after();
                     const uint64_t b0 = dV + static_cast<uint64_t>(vslot) * kTileStep;
@@ -334,6 +354,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
                     if (j + 1 == nt) mma_commit_warp(bar(OFULL + t));
                     if (!it.pair || t == 1) {
                         mma_commit_warp(bar(VEMPTY + vslot));
+                        vnew = true;
                         if (++vslot == VST) {
                             vslot = 0;
                             vph ^= 1u;
@@ -359,85 +380,113 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax, thread = row
+        // Beside the 128 scores a thread has few registers left: what the read-out needs of the item and
+        // of the thread's place is worked out again there, and the barriers' phases are bits of one word.
         const int t = warp >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + t * 128;
-        const uint32_t tO = tmem + lane_base + 256;
-        uint32_t sn = 0, on[2] = {0, 0};
+        uint32_t phases = 0;                   // 1: SFULL of the lane; 2, 4: OFULL of lanes 0, 1
         // a warp whose wait ran out still meets the others at every barrier of the items that are left
-        while (walk.cur < walk.end) {
+        while (walk.left > 0) {
             float m = -INFINITY, l = 0.f;
             {
                 walk.peek(p, it);
                 int left = p.n[it.b] - it.first(t) * BN;       // valid keys from the lane's next tile on
                 int steps = it.steps(t);
+                const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 128;
                 for (bool first = true; ok && steps > 0; --steps, left -= BN, first = false) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(SFULL + t), sn & 1u, tmo, abort_flag));
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(SFULL + t), phases & 1u, tmo, abort_flag));
                     if (!ok) break;
-                    ++sn;
+                    phases ^= 1u;
                     tc_fence_after();
-                    softmax_step(tS, tO + t * 128, p.scale_log2, left, first, m, l);
+                    softmax_step(tS, tS + 256, p.scale_log2, left, first, m, l);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(bar(PFULL + t));
                 }
             }
-            // the item is decoded again, so that none of it lives in registers beside the score tile
-            asm volatile("" : "+r"(walk.cur));
+            asm volatile("" : "+r"(walk.b), "+r"(walk.h0), "+r"(walk.tile), "+r"(walk.left));
             walk.next(p, it);
             const int n = p.n[it.b];
+            int tid;
+            asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+            const int row = tid & 127;
+            const bool leader = row == 0;
+            const int row_tok = p.pack == 1 ? row : row / p.pack;
+            const uint32_t tO = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256;
+            // Half a tile's output (64 dims) goes through shared memory: rows are written by their threads in
+            // the swizzled layout (8 rows hit 8 different bank groups), and one TMA store writes whole sectors.
+            // Writing rows of 256 bytes straight from their threads took 4500 cycles a tile pair.
+            const uint32_t stage = sO + static_cast<uint32_t>(t) * HALF;
+            auto stage_begin = [&]() {
+                if (leader) tma_store_wait_read();
+                lane_barrier(t);
+            };
+            auto stage_put = [&](int c, const uint32_t (&w)[16]) {     // 32 dims
+                uint8_t* dst = smem + (stage - sQ) + row * 128;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    *reinterpret_cast<uint4*>(dst + (((c * 4 + v) ^ (row & 7)) << 4)) =
+                        make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+            };
+            auto stage_end = [&](int hf, int tok0) {
+                fence_proxy_async();
+                lane_barrier(t);
+                if (leader) tma_store_4d(&p.omap, stage, hf * 64, it.h0, tok0, it.b);
+            };
             // both accumulators of a single are read by both warpgroups
             for (int u = 0; u < 2; ++u) {
                 if (it.steps(u) == 0) continue;
-                if (ok && (u == t || !it.pair) && !mbar_wait_bounded(bar(OFULL + u), on[u] & 1u, tmo, abort_flag)) ok = false;
-                ++on[u];
+                if (ok && (u == t || !it.pair) && !mbar_wait_bounded(bar(OFULL + u), (phases >> (1 + u)) & 1u, tmo, abort_flag)) ok = false;
+                phases ^= 2u << u;
             }
             // warp-uniform from here on: tensor-memory loads are warp-collective
             ok = __all_sync(0xffffffffu, ok);
+            const int tok0 = (it.pair ? it.tile + t : it.tile) * p.tokens;
+            const bool whole = it.pair || (n == 0 && t == 0);   // this warpgroup writes out a whole tile
             if (!ok) {
                 give_up(abort_flag, p.err);
-                if (n > 0 && !it.pair) {
+                if (whole) {
+                    for (int i = 0; i < 4; ++i) lane_barrier(t);
+                } else if (n > 0) {
                     softmax_barrier();
+                    if (splits == 1) {
+                        lane_barrier(t);
+                        lane_barrier(t);
+                    }
                     softmax_barrier();
                 }
                 continue;
             }
             tc_fence_after();
-            const int row_tok = row / p.pack, row_head = row - row_tok * p.pack;
-            const int64_t tok = static_cast<int64_t>(it.pair ? it.tile + t : it.tile) * p.tokens + row_tok;
+            const int64_t tok = static_cast<int64_t>(tok0) + row_tok;
             const bool live = row < used_rows && tok < p.Nq;
-            const int64_t stat = (static_cast<int64_t>(it.b) * p.H + it.h0 + row_head) * p.Nq + tok;
-            uint16_t* dst = p.out + ((static_cast<int64_t>(it.b) * p.Nq + tok) * p.H + it.h0 + row_head) * HD;
-            if (n == 0) {                      // no keys at all
-                if (live && it.owns(t) && (p.splits == 1 || blockIdx.x % p.splits == 0)) {
-#pragma unroll 1
-                    for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
-                    if (p.lse) p.lse[stat] = -INFINITY;
+            const int64_t stat = (static_cast<int64_t>(it.b) * p.H + it.h0 + row - row_tok * p.pack) * p.Nq + tok;
+            if (whole) {
+                if (splits > 1 && (blockIdx.x & (splits - 1)) != 0) {   // a tile without keys: the cluster's first CTA writes it
+                    for (int i = 0; i < 4; ++i) lane_barrier(t);
+                    continue;
                 }
-                continue;
-            }
-            if (it.pair) {
                 const float inv = 1.0f / l;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_x32_sync(tO + t * 128 + c * 32, o);
-                    if (live) {
+                for (int hf = 0; hf < 2; ++hf) {
+                    // 64 dims are converted before the staging space is waited for
+                    uint32_t out[2][16];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint4 w;
-                            w.x = bf16_pair(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
-                            w.y = bf16_pair(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
-                            w.z = bf16_pair(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
-                            w.w = bf16_pair(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
-                            reinterpret_cast<uint4*>(dst)[c * 4 + v] = w;
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_x32_sync(tO + t * 128 + hf * 64 + c * 32, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            out[c][i] = n > 0 ? bf16_pair(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
                     }
+                    stage_begin();
+                    stage_put(0, out[0]);
+                    stage_put(1, out[1]);
+                    stage_end(hf, tok0);
                 }
-                if (p.lse && live) p.lse[stat] = (m + __log2f(l)) * kLn2;
+                if (p.lse && live) p.lse[stat] = n > 0 ? (m + __log2f(l)) * kLn2 : -INFINITY;
                 continue;
             }
+            if (n == 0) continue;
             // single: warpgroup t reads out dims [64t, 64t + 64) of both accumulators
             stats[t * BM + row] = make_float2(m, l);
             softmax_barrier();
@@ -446,7 +495,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
             const float wa = weight_of(a, M), wb = weight_of(b, M);
             const float L = a.y * wa + b.y * wb;
             const bool two = it.steps(1) > 0, one = it.steps(0) > 0;   // a cluster's CTA may have no keys
-            const float inv = p.splits > 1 ? 1.0f : 1.0f / L;
+            const float inv = splits > 1 ? 1.0f : 1.0f / L;
+            if (splits == 1) stage_begin();
 #pragma unroll 1
             for (int c = 2 * t; c < 2 * t + 2; ++c) {
                 // a part without keys has whatever its columns held before, and counts as 0
@@ -458,61 +508,74 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
                 tmem_ld_x32_sync(tO + 128 + c * 32, o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) f[i] = (two ? fmaf(__uint_as_float(o[i]), wb, f[i]) : f[i]) * inv;
-                if (p.splits > 1) {            // [dims / 4][row] so that a warp writes 512 contiguous bytes
+                if (splits > 1) {            // [dims / 4][row] so that a warp writes 512 contiguous bytes
                     float4* part = reinterpret_cast<float4*>(smem);
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         part[(c * 8 + v) * BM + row] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
-                } else if (live) {
+                } else {
+                    uint32_t out[16];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        reinterpret_cast<uint4*>(dst)[c * 4 + v] =
-                            make_uint4(bf16_pair(f[8 * v], f[8 * v + 1]), bf16_pair(f[8 * v + 2], f[8 * v + 3]),
-                                       bf16_pair(f[8 * v + 4], f[8 * v + 5]), bf16_pair(f[8 * v + 6], f[8 * v + 7]));
+                    for (int i = 0; i < 16; ++i) out[i] = bf16_pair(f[2 * i], f[2 * i + 1]);
+                    stage_put(c & 1, out);
                 }
             }
+            if (splits == 1) stage_end(t, tok0);
             tc_fence_before();
             softmax_barrier();                 // both accumulators and the statistics have been read
-            if (p.splits > 1) {
+            if (splits > 1) {
                 if (t == 0) stats[row] = make_float2(M, L);
             } else if (t == 0 && live && p.lse) {
                 p.lse[stat] = (M + __log2f(L)) * kLn2;
             }
         }
+        if ((threadIdx.x & 127) == 0) tma_store_wait();
+        __syncwarp();
     }
-    if (p.splits > 1) {
-        // join the parts of the cluster's CTAs: thread = (4 dims, row), the CTAs share the tile
+    if (splits > 1) {
+        // join the parts of the cluster's CTAs: a thread keeps its row, the CTAs share the dims
         cluster_sync_all();
-        Walk<CAP> again(p);
+        Walk again(p);
         again.next(p, it);
-        const int rank = blockIdx.x % p.splits;
-        const int n = p.n[it.b];
-        for (int i = rank * NTHREADS + threadIdx.x; n > 0 && i < used_rows * (HD / 4); i += p.splits * NTHREADS) {
-            const int d4 = i / used_rows, row = i - d4 * used_rows;
-            const int64_t tok = static_cast<int64_t>(it.tile) * p.tokens + row / p.pack;
-            if (tok >= p.Nq) continue;
+        const int row = threadIdx.x & 127;
+        const int64_t tok = static_cast<int64_t>(it.tile) * p.tokens + (p.pack == 1 ? row : row / p.pack);
+        if (p.n[it.b] > 0 && row < used_rows && tok < p.Nq) {
             float2 ml[kMaxCluster];
-            float M = -INFINITY;
-            for (int c = 0; c < p.splits; ++c) {
-                ml[c] = ld_cluster_f32x2(map_to_rank(smem_u32(&stats[row]), c));
-                if (ml[c].y != 0.f) M = fmaxf(M, ml[c].x);
-            }
-            float L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < p.splits; ++c) {
-                const float w = weight_of(ml[c], M);
-                L = fmaf(ml[c].y, w, L);
-                const float4 o = ld_cluster_f32x4(map_to_rank(sQ + static_cast<uint32_t>(d4 * BM + row) * 16u, c));
-                acc.x = fmaf(o.x, w, acc.x);
-                acc.y = fmaf(o.y, w, acc.y);
-                acc.z = fmaf(o.z, w, acc.z);
-                acc.w = fmaf(o.w, w, acc.w);
-            }
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                if (c < splits) {
+                    ml[c] = ld_cluster_f32x2(map_to_rank(smem_u32(&stats[row]), c));
+                    if (ml[c].y != 0.f) M = fmaxf(M, ml[c].x);
+                }
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                if (c < splits) {
+                    const float w = weight_of(ml[c], M);
+                    L = fmaf(ml[c].y, w, L);
+                    ml[c].x = w;
+                }
             const float inv = 1.0f / L;
-            const int h = it.h0 + row % p.pack;
-            uint16_t* dst = p.out + ((static_cast<int64_t>(it.b) * p.Nq + tok) * p.H + h) * HD + d4 * 4;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(acc.x * inv, acc.y * inv), bf16_pair(acc.z * inv, acc.w * inv));
-            if (d4 == 0 && p.lse)
+            const int rank = blockIdx.x & (splits - 1);
+            const int h = it.h0 + (p.pack == 1 ? 0 : row % p.pack);
+            uint16_t* dst = p.out + ((static_cast<int64_t>(it.b) * p.Nq + tok) * p.H + h) * HD;
+#pragma unroll 1
+            for (int d4 = rank * (NTHREADS / 128) + (threadIdx.x >> 7); d4 < HD / 4; d4 += splits * (NTHREADS / 128)) {
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < splits) {
+                        const float4 o = ld_cluster_f32x4(map_to_rank(sQ + static_cast<uint32_t>(d4 * BM + row) * 16u, c));
+                        const float w = ml[c].x;
+                        acc.x = fmaf(o.x, w, acc.x);
+                        acc.y = fmaf(o.y, w, acc.y);
+                        acc.z = fmaf(o.z, w, acc.z);
+                        acc.w = fmaf(o.w, w, acc.w);
+                    }
+                *reinterpret_cast<uint2*>(dst + d4 * 4) =
+                    make_uint2(bf16_pair(acc.x * inv, acc.y * inv), bf16_pair(acc.z * inv, acc.w * inv));
+            }
+            if (rank == 0 && threadIdx.x < 128 && p.lse)
                 p.lse[(static_cast<int64_t>(it.b) * p.H + h) * p.Nq + tok] = (M + __log2f(L)) * kLn2;
         }
         cluster_sync_all();                    // no CTA leaves while others read its memory
@@ -561,7 +624,12 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
     p.pack = cross_pack(c.H / c.Hk);
     p.tokens = BM / p.pack;
     p.tiles = (c.Nq + p.tokens - 1) / p.tokens;
-    if (!encode_query_map(&p.qmap, c.q, c.H, c.Nq, c.B, c.qs, p.pack, p.tokens)) return cudaErrorInvalidValue;
+    p.packs = c.H / p.pack;
+    p.group = c.H / c.Hk;
+    const CrossStrides dense = {int64_t(c.H) * HD, HD, int64_t(c.H) * HD * c.Nq};
+    if (!encode_query_map(&p.qmap, c.q, c.H, c.Nq, c.B, c.qs, p.pack, p.tokens) ||
+        !encode_query_map(&p.omap, f.out, c.H, c.Nq, c.B, dense, p.pack, p.tokens))
+        return cudaErrorInvalidValue;
     int least = 1 << 30;                       // key tiles of the shortest stream that has any
     for (int b = 0; b < c.B; ++b) {
         p.n[b] = c.n[b];
@@ -584,8 +652,30 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
     const int64_t tiles = static_cast<int64_t>(p.tiles) * (c.H / p.pack) * c.B;
     if (tiles > INT32_MAX / kMaxCluster) return cudaErrorInvalidConfiguration;
     // clusters share a tile's keys while that leaves SMs idle and gives every lane a key tile
-    p.splits = 1;
-    while (p.splits < kMaxCluster && tiles * p.splits * 2 <= sms && least >= p.splits * 4 && least != 1 << 30) p.splits *= 2;
+    int splits = 1;
+    while (splits < kMaxCluster && tiles * splits * 2 <= sms && least >= splits * 4 && least != 1 << 30) {
+        splits *= 2;
+        ++p.split_shift;
+    }
+    const int ctas = static_cast<int>(std::min<int64_t>(tiles, std::min(sms, kMaxCtas)));
+    if (splits == 1) {
+        // ranges of equal cost; a query tile costs its key tiles, and one for its start and end
+        const int64_t per_stream = static_cast<int64_t>(p.tiles) * p.packs;
+        int64_t total = 0;
+        for (int b = 0; b < c.B; ++b) total += ((c.n[b] + BN - 1) / BN + 1) * per_stream;
+        int b = 0;
+        int64_t before = 0;                    // cost of the streams before b
+        for (int i = 0; i <= ctas; ++i) {
+            const int64_t x = total * i / ctas;
+            int64_t w = (c.n[b] + BN - 1) / BN + 1;
+            while (x > before + w * per_stream && b + 1 < c.B) {
+                before += w * per_stream;
+                ++b;
+                w = (c.n[b] + BN - 1) / BN + 1;
+            }
+            p.start[i] = static_cast<int32_t>(b * per_stream + (x - before + w - 1) / w);
+        }
+    }
 
     auto kernel = cross_attention_kernel<CAP>;
     int dev = 0;
@@ -597,16 +687,16 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
         attr_set.fetch_or(uint64_t(1) << (dev & 63));
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.splits > 1 ? tiles * p.splits : std::min<int64_t>(tiles, sms)));
+    cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? tiles * splits : ctas));
     cfg.blockDim = dim3(NTHREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr.val.clusterDim.x = static_cast<unsigned>(splits);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
