@@ -367,14 +367,21 @@ cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, cross_rows_kernel, p, splits, static_cast<int>(row_blocks));
 }
 
-cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s)
+cudaError_t launch_cross_delta(const CrossBackward& p, cudaStream_t s)
 {
     const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Nq * p.c.H;
+    if ((rows + 15) / 16 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cross_delta_kernel<<<static_cast<unsigned>((rows + 15) / 16), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s)
+{
     const int64_t qb = (static_cast<int64_t>(p.c.Nq) + 15) / 16, kb = (static_cast<int64_t>(p.c.Nk) + 15) / 16;
     const int64_t dq_blocks = qb * p.c.B * p.c.H, dkv_blocks = kb * p.c.B * p.c.Hk;
-    if ((rows + 15) / 16 > INT32_MAX || dq_blocks > INT32_MAX || dkv_blocks > INT32_MAX)
-        return cudaErrorInvalidConfiguration;
-    cross_delta_kernel<<<static_cast<unsigned>((rows + 15) / 16), 256, 0, s>>>(p);
+    if (dq_blocks > INT32_MAX || dkv_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_cross_delta(p, s);
+    if (e != cudaSuccess) return e;
     cross_rows_dq_kernel<<<static_cast<unsigned>(dq_blocks), 256, 0, s>>>(p, static_cast<int>(qb));
     if (dkv_blocks > 0) cross_rows_dkv_kernel<<<static_cast<unsigned>(dkv_blocks), 256, 0, s>>>(p, static_cast<int>(kb));
     return cudaGetLastError();
