@@ -44,8 +44,8 @@ struct CrossBackward {
     uint16_t* dq;
     uint16_t* dk;              // [B][Nk][Hk][D]
     uint16_t* dv;
-    float* delta;              // [B][H][Nq] scratch
-    float* part;               // cross_backward_part_bytes of scratch
+    float* stats;              // scratch: delta [B][H][Nq], or cross_backward_stats_bytes
+    float* part;               // scratch: cross_backward_part_bytes
 };
 
 // Heads that share a key head and a 128-row query tile: the largest divisor of `group` up to 128.
@@ -54,12 +54,11 @@ int cross_pack(int group);
 // Query tiles of 128 rows on the tensor cores.
 cudaError_t launch_cross_attention(const CrossForward& p, cudaStream_t s);
 
-// Gradients on the tensor cores, and the bytes of the key tiles' partial sums for a batch of B streams.
+// Gradients on the tensor cores, and the bytes of scratch for a batch of B streams: lse and delta by query
+// tile, and the key tiles' partial sums.
 cudaError_t launch_cross_backward(const CrossBackward& p, cudaStream_t s);
+size_t cross_backward_stats_bytes(int B, int H, int Hk, int64_t Nq);
 size_t cross_backward_part_bytes(int B, int H, int Hk, int64_t Nq, int64_t Nk);
-
-// delta[b][h][i] = sum_d dout * out.
-cudaError_t launch_cross_delta(const CrossBackward& p, cudaStream_t s);
 
 // Query rows on the CUDA cores (any size; fast for a few queries).
 cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s);

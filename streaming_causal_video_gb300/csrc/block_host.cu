@@ -121,9 +121,10 @@ CrossProblem slice_of(const sdv2_cross_cfg* c, const int64_t* kv_lens, const Cro
     return p;
 }
 
-size_t delta_bytes(const sdv2_cross_cfg* c)
+// Scratch of the backward pass for one launch's streams: statistics, then partial sums.
+size_t stats_bytes(const sdv2_cross_cfg* c)
 {
-    return (static_cast<size_t>(c->batch) * c->heads * c->q_len * sizeof(float) + 255) / 256 * 256;
+    return (cross_backward_stats_bytes(std::min(c->batch, kCrossStreams), c->heads, kv_heads_of(c), c->q_len) + 255) / 256 * 256;
 }
 
 int64_t rows_of(const sdv2_norm_cfg* c) { return c->rows_per_group ? c->rows_per_group : c->rows; }
@@ -179,7 +180,7 @@ size_t sdv2_cross_workspace_bytes(const sdv2_cross_cfg* c, int32_t backward)
     if (check_cross(c, &qs, &kvs) != SDV2_OK) return 0;
     size_t bytes = kHeaderBytes;
     if (backward)
-        bytes += delta_bytes(c) + cross_backward_part_bytes(std::min(c->batch, kCrossStreams), c->heads, kv_heads_of(c), c->q_len,
+        bytes += stats_bytes(c) + cross_backward_part_bytes(std::min(c->batch, kCrossStreams), c->heads, kv_heads_of(c), c->q_len,
                                                             c->kv_len);
     return bytes;
 }
@@ -245,8 +246,8 @@ sdv2_status sdv2_cross_attention_backward(const sdv2_cross_cfg* c, const int64_t
         p.dq = static_cast<uint16_t*>(dq) + rows * 128;
         p.dk = static_cast<uint16_t*>(dk) + (dk ? kv_rows * 128 : 0);
         p.dv = static_cast<uint16_t*>(dv) + (dv ? kv_rows * 128 : 0);
-        p.delta = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes) + rows;
-        p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes + delta_bytes(c));
+        p.stats = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes);
+        p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes + stats_bytes(c));
         const bool few = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq <= 4;
         const cudaError_t e = few ? launch_cross_rows_backward(p, static_cast<cudaStream_t>(stream))
                                   : launch_cross_backward(p, static_cast<cudaStream_t>(stream));

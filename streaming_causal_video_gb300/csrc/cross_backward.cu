@@ -16,11 +16,17 @@
 //   S = R0 T0^T,  dP = R1 T1^T,  acc0 += dS T0,  and for dKV also  acc1 += P T1,
 // rows being queries (dQ) or keys (dKV): lse and delta belong to the rows or to the columns.
 //
-// A CTA walks a contiguous range of units, cut by cost.  Roles (12 warps):
-//   warps 0-7 : thread = row and half of the 128 columns.  S is read out and turned into P as soon as
-//               it is there, which frees it for the next step's S while dP is still computed; P and dS
-//               then take dP's place as packed bf16, the A operands of the accumulating products.
-//   warp 8: T tiles (2 stages); 10: R tiles (loaded while the unit before is read out); 9: MMA.
+// A CTA walks a contiguous range of units, cut by cost.  Roles (20 warps):
+//   warps 0-15: thread = row and 32 of the 128 columns.  S is turned into P, which takes its place as packed
+//               bf16, the A operand of dV += P^T dO; then dP into dS in its place.  A step's chain is
+//               dS(i) -> acc0 -> dP(i+1) -> dS(i+1); dV, the next S and its exponentials fit beside it.
+//   warps 16, 18: T0 tiles (3 slots), T1 tiles (dKV 2, dQ 1); 19: R tiles; 17: MMA.
+// Both T tiles of a step are read to its end, and a slot that is filled only then comes too late for
+// the next step's S: with two slots of each, a dKV step waited about 1500 cycles for its load.  Seven
+// tiles fit; the third T0 slot takes the place of an output tile in dKV (its read-out goes through R0
+// and R1, once for many steps), and of the second T1 slot in dQ (V is only needed for dP).
+// A first kernel leaves -lse (log2 units) and -delta of every query tile's 128 rows side by side in the
+// workspace, so that dKV copies them with the tiles.
 // Tensor memory: acc0 | acc1 | S | dP, 128 columns each.
 #include <algorithm>
 #include <atomic>
@@ -33,24 +39,26 @@ namespace sdv2 {
 namespace {
 
 constexpr int HD = 128, BM = 128;
-constexpr int TST = 2;
+constexpr int T0ST = 3;
 constexpr uint32_t TILE = 128 * HD * 2;
 constexpr uint32_t HALF = TILE / 2;
-constexpr int T_WARP = 8, MMA_WARP = 9, R_WARP = 10;
-constexpr int NTHREADS = 12 * 32;
+constexpr int COMPUTE = 512;                   // threads of the compute warps
+constexpr int T0_WARP = 16, MMA_WARP = 17, T1_WARP = 18, R_WARP = 19;
+constexpr int NTHREADS = 20 * 32;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC0 = 0, ACC1 = 128, SCOL = 256, XCOL = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 8;
 
-enum Bar { RFULL, REMPTY, TFULL, TEMPTY = TFULL + TST, SFULL = TEMPTY + TST, SREAD, DPFULL, DSFULL, ACCFULL, MMADONE, NBARS };
+enum Bar { RFULL, REMPTY, T0FULL, T0EMPTY = T0FULL + T0ST, T1FULL = T0EMPTY + T0ST, T1EMPTY = T1FULL + 2, SFULL = T1EMPTY + 2,
+           SREAD, DPFULL, DSFULL, ACCFULL, MMADONE, NBARS };
 
-constexpr uint32_t SMEM_TILES = (2 + 2 * TST + 1) * TILE;      // R0 R1, (T0 T1) per stage, an output tile
-constexpr uint32_t SMEM_STATS = 2 * 2 * BM * 4;                // dKV: lse and delta of a query tile, two steps
+constexpr uint32_t SMEM_TILES = 7 * TILE;                      // R0 R1, T0 slots, T1 slots, dQ: an output tile
+constexpr uint32_t SMEM_STATS = (T0ST + 2) * BM * 4;           // dKV: -lse per T0 slot, -delta per T1 slot
 constexpr uint32_t SMEM_USED = SMEM_TILES + SMEM_STATS + 256;
-constexpr uint32_t SMEM_BYTES = 232448;
-static_assert(SMEM_USED + 768 <= SMEM_BYTES && NBARS * 8 + 8 <= 256, "shared memory layout");
+constexpr uint32_t SMEM_BYTES = 232448;                        // 256 bytes to spare: the base has to be 1024-byte aligned
+static_assert(SMEM_USED <= SMEM_BYTES && NBARS * 8 + 8 <= 256, "shared memory layout");
 
 template <int CAP>
 struct Params {
@@ -58,8 +66,8 @@ struct Params {
     CUtensorMap kmap[CAP], vmap[CAP];          // per stream: valid rows
     CUtensorMap dkmap, dvmap;                  // (D, Hk, Nk, B): boxes of 64 dims x 1 x 128 rows
     int32_t n[CAP];
-    const float* lse;                          // [B][H][Nq]
-    const float* delta;
+    const float* stats;                        // [query tile][-lse (log2 units), -delta][128]
+    uint16_t *dk, *dv;                         // [B][Nk][Hk][D]
     float* part;                               // dKV: [split][unit][2][D/4][128][4]
     uint32_t* err;
     uint64_t timeout_ns;
@@ -122,7 +130,7 @@ __device__ __forceinline__ void give_up(volatile int* abort_flag, uint32_t* err)
     atomicOr(err, kErrTimeout);
 }
 
-__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 template <bool DKV, int CAP>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __grid_constant__ Params<CAP> p)
@@ -133,8 +141,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
         return;
     }
-    const uint32_t sR = smem_u32(smem), sT = sR + 2 * TILE, sO = sT + 2 * TST * TILE;
-    float* colstat = reinterpret_cast<float*>(smem + SMEM_TILES);           // [2][2][128]
+    constexpr int T1ST = DKV ? 2 : 1;
+    const uint32_t sR = smem_u32(smem), sT0 = sR + 2 * TILE, sT1 = sT0 + T0ST * TILE;
+    const uint32_t sO = DKV ? sR : sR + 6 * TILE;                          // read-out: R0 and R1, or the seventh tile
+    const uint32_t sL = sR + SMEM_TILES, sD = sL + T0ST * BM * 4;          // dKV: statistics of the T slots
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SMEM_TILES + SMEM_STATS);
     const uint32_t bar0 = smem_u32(bars);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
@@ -147,13 +157,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
     const int used_rows = p.pack * p.tokens;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == SREAD || i == DSFULL ? 256 : 1);
+        for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == SREAD || i == DSFULL ? COMPUTE : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     // Rows of a query tile that no load writes (the pack does not divide 128) are zero: as streamed tiles
     // they are summed over, with probability 0.
-    for (int i = threadIdx.x; i < (BM - used_rows) * 16 * (2 + 2 * TST); i += NTHREADS) {
+    for (int i = threadIdx.x; i < (BM - used_rows) * 16 * 7; i += NTHREADS) {
         const int part = i & 15, r = i >> 4, tile = r / (BM - used_rows), row = used_rows + r - tile * (BM - used_rows);
         *reinterpret_cast<uint4*>(smem + tile * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -201,40 +211,52 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             if (units) mbar_wait_bounded(bar(RFULL), (units - 1) & 1u, tmo, &never);
         }
         __syncwarp();
-    } else if (warp == T_WARP) {
+    } else if (warp == T0_WARP || warp == T1_WARP) {
         if (lane == 0) {
-            uint32_t count = 0;
+            const bool t0 = warp == T0_WARP;
+            const int nst = t0 ? T0ST : T1ST;
+            const int full = t0 ? T0FULL : T1FULL, empty = t0 ? T0EMPTY : T1EMPTY;
+            const uint32_t ring = t0 ? sT0 : sT1, stat_ring = t0 ? sL : sD;
+            int slot = 0;
+            uint32_t phase = 0, pending = 0;
             while (ok && walk.next(p, u)) {
                 int tile = 0, h0 = 0;          // dKV: query tile and first head of its pack
+                const float* stat = nullptr;
                 if constexpr (DKV) {
                     const int pk = u.s0 / p.qtiles;
                     tile = u.s0 - pk * p.qtiles;
                     h0 = u.head * p.group + pk * p.pack;
+                    const int64_t q = (static_cast<int64_t>(u.b) * p.packs + u.head * (p.group / p.pack) + pk) * p.qtiles + tile;
+                    stat = p.stats + q * 2 * BM + (t0 ? 0 : BM);
                 }
                 const int hk = DKV ? 0 : u.head / p.group;
-                for (int i = 0; i < u.steps; ++i, ++count) {
-                    const int st = count & (TST - 1);
-                    if (!mbar_wait_bounded(bar(TEMPTY + st), ((count / TST) & 1u) ^ 1u, tmo, abort_flag)) { ok = false; break; }
-                    const uint32_t dst = sT + st * 2 * TILE;
+                for (int i = 0; i < u.steps; ++i) {
+                    if (!mbar_wait_bounded(bar(empty + slot), phase ^ 1u, tmo, abort_flag)) { ok = false; break; }
+                    const uint32_t dst = ring + slot * TILE;
                     if constexpr (DKV) {
-                        mbar_arrive_expect_tx(bar(TFULL + st), 2 * query_bytes);
-                        load_queries(&p.qmap, dst, TFULL + st, h0, tile * p.tokens, u.b);
-                        load_queries(&p.domap, dst + TILE, TFULL + st, h0, tile * p.tokens, u.b);
+                        mbar_arrive_expect_tx(bar(full + slot), query_bytes + BM * 4);
+                        load_queries(t0 ? &p.qmap : &p.domap, dst, full + slot, h0, tile * p.tokens, u.b);
+                        bulk_load(stat_ring + slot * BM * 4, stat, BM * 4, bar(full + slot));
+                        stat += 2 * BM;        // the packs of a key head follow one another
                         if (++tile == p.qtiles) {
                             tile = 0;
                             h0 += p.pack;
                         }
                     } else {
-                        mbar_arrive_expect_tx(bar(TFULL + st), 2 * TILE);
-                        load_keys(&p.kmap[u.b], dst, TFULL + st, hk, i * BM);
-                        load_keys(&p.vmap[u.b], dst + TILE, TFULL + st, hk, i * BM);
+                        mbar_arrive_expect_tx(bar(full + slot), TILE);
+                        load_keys(t0 ? &p.kmap[u.b] : &p.vmap[u.b], dst, full + slot, hk, i * BM);
+                    }
+                    pending = (pending & ~(17u << slot)) | (1u << slot) | (phase << (slot + 4));
+                    if (++slot == nst) {
+                        slot = 0;
+                        phase ^= 1u;
                     }
                 }
             }
             if (!ok) give_up(abort_flag, p.err);
-            volatile int never = 0;
-            for (uint32_t k = 1; k <= TST && k <= count; ++k)
-                mbar_wait_bounded(bar(TFULL + ((count - k) & (TST - 1))), ((count - k) / TST) & 1u, tmo, &never);
+            volatile int never = 0;            // every copy lands before the CTA may exit
+            for (int i = 0; i < nst; ++i)
+                if (pending >> i & 1u) mbar_wait_bounded(bar(full + i), pending >> (i + 4) & 1u, tmo, &never);
         }
         __syncwarp();
     } else if (warp == MMA_WARP) {
@@ -254,48 +276,71 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 mma_ss_warp(tmem + d, desc(a + o, 16), desc(b + o, 16), idKK, k > 0 ? 1u : 0u);
             }
         };
-        // D += A B with A = 128 packed columns written by the two column halves: their parts `a_off` into each half
-        auto accumulate = [&](uint32_t d, uint32_t a_off, uint32_t b, bool add) {
+        // D += A B with A = 128 columns packed to bf16, each quarter of them at the start of its 32
+        auto accumulate = [&](uint32_t d, uint32_t a, uint32_t b, bool add) {
 #pragma unroll
             for (int k = 0; k < BM / 16; ++k)
-                mma_ts_warp(tmem + d, tmem + XCOL + (k >> 2) * 64 + a_off + (k & 3) * 8, desc(b + k * 2048u, HALF), idKM,
+                mma_ts_warp(tmem + d, tmem + a + (k >> 1) * 32 + (k & 1) * 8, desc(b + k * 2048u, HALF), idKM,
                             (add || k > 0) ? 1u : 0u);
         };
         uint32_t count = 0, units = 0;         // steps, units begun
-        auto stage = [&](uint32_t c) { return sT + (c & (TST - 1)) * 2 * TILE; };
-        auto begin_s = [&](uint32_t c) {       // S of step c
-            if (!wait(TFULL + (c & (TST - 1)), (c / TST) & 1u)) return;
+        // T slots and phases of the next S, the next dP and the step being finished
+        int s_slot = 0, p_slot = 0, a_slot0 = 0, a_slot1 = 0;
+        uint32_t s_ph = 0, p_ph = 0;
+        auto begin_s = [&]() {
+            if (!wait(T0FULL + s_slot, s_ph)) return;
             tc_fence_after();
-            product(SCOL, sR, stage(c));
+            product(SCOL, sR, sT0 + s_slot * TILE);
             mma_commit_warp(bar(SFULL));
+            if (++s_slot == T0ST) {
+                s_slot = 0;
+                s_ph ^= 1u;
+            }
         };
-        auto begin_dp = [&](uint32_t c, bool last) {
-            product(XCOL, sR + TILE, stage(c) + TILE);
+        auto begin_dp = [&](bool last) {
+            if (!wait(T1FULL + p_slot, p_ph)) return;
+            tc_fence_after();
+            product(XCOL, sR + TILE, sT1 + p_slot * TILE);
             mma_commit_warp(bar(DPFULL));
-            if (last) mma_commit_warp(bar(REMPTY));
+            if (!DKV) {
+                mma_commit_warp(bar(T1EMPTY + p_slot));                  // V has done its part
+                if (last) mma_commit_warp(bar(REMPTY));
+            }
+            if (++p_slot == T1ST) {
+                p_slot = 0;
+                p_ph ^= 1u;
+            }
         };
         while (ok && walk.next(p, u)) {
             if (u.steps == 0) continue;
             // the unit before has read its last S and written its last dS, so both score tiles are free
             if (!wait(RFULL, units & 1u)) break;
             ++units;
-            begin_s(count);
+            begin_s();
             if (!ok) break;
-            begin_dp(count, u.steps == 1);
+            begin_dp(u.steps == 1);
             for (int i = 0; ok && i < u.steps; ++i, ++count) {
                 const bool more = i + 1 < u.steps;
-                if (more) {
+                if (DKV || more) {
                     if (!wait(SREAD, count & 1u)) break;
-                    begin_s(count + 1);
+                    tc_fence_after();
+                }
+                if constexpr (DKV) {
+                    accumulate(ACC1, SCOL, sT1 + a_slot1 * TILE, i > 0);         // dV += P^T dO
+                    mma_commit_warp(bar(T1EMPTY + a_slot1));
+                    if (++a_slot1 == T1ST) a_slot1 = 0;
+                }
+                if (more) {
+                    begin_s();
                     if (!ok) break;
                 }
                 if (!wait(DSFULL, count & 1u)) break;
                 tc_fence_after();
-                if constexpr (DKV) accumulate(ACC1, 0, stage(count) + TILE, i > 0);      // dV += P^T dO
-                accumulate(ACC0, 32, stage(count), i > 0);                               // dQ += dS K, dK += dS^T Q
-                mma_commit_warp(bar(TEMPTY + (count & (TST - 1))));
+                accumulate(ACC0, XCOL, sT0 + a_slot0 * TILE, i > 0);             // dQ += dS K, dK += dS^T Q
+                mma_commit_warp(bar(T0EMPTY + a_slot0));
+                if (++a_slot0 == T0ST) a_slot0 = 0;
                 if (!more) mma_commit_warp(bar(ACCFULL));
-                else begin_dp(count + 1, i + 2 == u.steps);
+                else begin_dp(i + 2 == u.steps);
             }
         }
         if (!ok && lane == 0) give_up(abort_flag, p.err);
@@ -305,99 +350,97 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             mbar_wait_bounded(bar(MMADONE), 0, tmo, &never);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- P and dS, thread = (row, column half)
-        const int half = warp >> 2;
+    } else {
+        // ---------------------------------------------------------------- P and dS, thread = (row, 32 columns)
+        const int quarter = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t tL = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const bool leader = threadIdx.x == 0;
         uint32_t count = 0, units = 0;
-        // lse (log2 units, so that padding rows have probability 0) and delta of row `r` of a query tile
-        auto stat_index = [&](int b, int h0, int tok0, int r) {
-            const int rt = p.pack == 1 ? r : r / p.pack;
-            const int64_t tok = static_cast<int64_t>(tok0) + rt;
-            return r < used_rows && tok < p.Nq ? (static_cast<int64_t>(b) * p.H + h0 + (r - rt * p.pack)) * p.Nq + tok : int64_t(-1);
-        };
-        while (walk.next(p, u)) {
-            float lse2 = 0.f, delta = 0.f;     // dQ: of the thread's row
-            int tile = 0, h0 = 0;              // dKV: query tile whose statistics come next
-            float next_stat = 0.f;             // dKV: this thread's entry of the next step's statistics
-            auto fetch = [&]() {
-                const int64_t i = stat_index(u.b, h0, tile * p.tokens, threadIdx.x & 127);
-                if (half == 0) next_stat = i >= 0 ? p.lse[i] * kLog2e : INFINITY;
-                else next_stat = i >= 0 ? p.delta[i] : 0.f;
-                if (++tile == p.qtiles) {
-                    tile = 0;
-                    h0 += p.pack;
-                }
-            };
-            if (u.steps > 0) {
-                if constexpr (DKV) {
-                    const int pk = u.s0 / p.qtiles;
-                    tile = u.s0 - pk * p.qtiles;
-                    h0 = u.head * p.group + pk * p.pack;
-                    fetch();
-                } else {
-                    const int64_t i = stat_index(u.b, u.head, u.tile * p.tokens, row);
-                    lse2 = i >= 0 ? p.lse[i] * kLog2e : INFINITY;
-                    delta = i >= 0 ? p.delta[i] : 0.f;
-                }
+        float row_lse = 0.f, row_delta = 0.f;  // dQ: of the thread's row, negated, and of the unit that comes next
+        auto fetch_unit = [&](const Unit& v) {
+            if constexpr (!DKV) {
+                if (v.steps == 0) return;
+                row_lse = p.stats[static_cast<int64_t>(v.index) * 2 * BM + row];
+                row_delta = p.stats[static_cast<int64_t>(v.index) * 2 * BM + BM + row];
             }
+        };
+        int slot0 = 0, slot1 = 0;              // dKV: T slots of the step
+        uint32_t phase0 = 0, phase1 = 0;
+        bool has = walk.next(p, u);
+        if (has) fetch_unit(u);
+        while (has) {
             const bool constant = DKV && p.n[u.b] == 1;           // a softmax over one key has no gradient
+            const uint64_t lse2 = f32x2_pack(row_lse, row_lse), delta2 = f32x2_pack(row_delta, row_delta);
             // a thread whose wait ran out still runs through all steps, to meet the others at every barrier
+#pragma unroll 1
             for (int i = 0; i < u.steps; ++i, ++count) {
-                const float* cl = colstat + (count & 1u) * 2 * BM + half * 64;
-                if constexpr (DKV) {
-                    colstat[(count & 1u) * 2 * BM + half * BM + (threadIdx.x & 127)] = next_stat;
-                    if (i + 1 < u.steps) fetch();
-                    compute_barrier();
-                }
+                const float* cl = reinterpret_cast<const float*>(smem + SMEM_TILES) + slot0 * BM + quarter * 32;
+                const float* cd = reinterpret_cast<const float*>(smem + SMEM_TILES) + (T0ST + slot1) * BM + quarter * 32;
+                if constexpr (DKV) ok = ok && mbar_wait_bounded(bar(T0FULL + slot0), phase0, tmo, abort_flag);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(SFULL), count & 1u, tmo, abort_flag));
                 tc_fence_after();
-                float pr[64];
+                const uint64_t sl2x2 = f32x2_pack(p.scale_log2, p.scale_log2);
+                uint64_t pr[16];                                   // P, two columns each
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t s[32];
-                    tmem_ld_x32_sync(tL + SCOL + half * 64 + c * 32, s);
+                    uint32_t x[16], w[8];
+                    tmem_ld_x16_sync(tL + SCOL + quarter * 32 + c * 16, x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        pr[c * 32 + e] = ex2_approx(fmaf(__uint_as_float(s[e]), p.scale_log2, DKV ? -cl[c * 32 + e] : -lse2));
+                    for (int e = 0; e < 8; ++e) {
+                        uint64_t m2;
+                        if constexpr (DKV) m2 = reinterpret_cast<const uint64_t*>(cl)[c * 8 + e];
+                        else m2 = lse2;
+                        float a, b;
+                        f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2x2, m2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        pr[c * 8 + e] = f32x2_pack(a, b);
+                        w[e] = bf16_pair(a, b);
+                    }
+                    // the first 16 columns have been read, the second are not written over
+                    if constexpr (DKV) tmem_st_x8(tL + SCOL + quarter * 32 + c * 8, w);
                 }
+                if constexpr (DKV) tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(SREAD));
+                if constexpr (DKV) ok = ok && mbar_wait_bounded(bar(T1FULL + slot1), phase1, tmo, abort_flag);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(DPFULL), count & 1u, tmo, abort_flag));
                 if (!ok) give_up(abort_flag, p.err);
                 tc_fence_after();
-                uint32_t ds[2][16];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t d[32];
-                    tmem_ld_x32_sync(tL + XCOL + half * 64 + c * 32, d);
+                    uint32_t x[16], w[8];
+                    tmem_ld_x16_sync(tL + XCOL + quarter * 32 + c * 16, x);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float a = __uint_as_float(d[2 * e]) - (DKV ? cl[BM + c * 32 + 2 * e] : delta);
-                        float b = __uint_as_float(d[2 * e + 1]) - (DKV ? cl[BM + c * 32 + 2 * e + 1] : delta);
-                        a *= pr[c * 32 + 2 * e];
-                        b *= pr[c * 32 + 2 * e + 1];
-                        if (DKV && constant) a = b = 0.f;
-                        ds[c][e] = bf16_pair(a, b);
+                    for (int e = 0; e < 8; ++e) {
+                        uint64_t m2;
+                        if constexpr (DKV) m2 = reinterpret_cast<const uint64_t*>(cd)[c * 8 + e];
+                        else m2 = delta2;
+                        float a, b;
+                        f32x2_unpack(fmul2(fadd2(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), m2), pr[c * 8 + e]), a, b);
+                        w[e] = constant ? 0u : bf16_pair(a, b);
                     }
+                    tmem_st_x8(tL + XCOL + quarter * 32 + c * 8, w);
                 }
-                if constexpr (DKV) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = bf16_pair(pr[c * 32 + 2 * e], pr[c * 32 + 2 * e + 1]);
-                        tmem_st_x16(tL + XCOL + half * 64 + c * 16, w);
-                    }
-                }
-                tmem_st_x16(tL + XCOL + half * 64 + 32, ds[0]);
-                tmem_st_x16(tL + XCOL + half * 64 + 48, ds[1]);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(DSFULL));
+                if constexpr (DKV) {
+                    if (++slot0 == T0ST) {
+                        slot0 = 0;
+                        phase0 ^= 1u;
+                    }
+                    if (++slot1 == T1ST) {
+                        slot1 = 0;
+                        phase1 ^= 1u;
+                    }
+                }
             }
+            // the next unit's statistics are on their way while the accumulators are read out
+            Unit nx;
+            has = walk.next(p, nx);
+            if (has) fetch_unit(nx);
             // ------------------------------------------------------------ read out the accumulators
             if (u.steps > 0) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(ACCFULL), units & 1u, tmo, abort_flag));
@@ -406,54 +449,57 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             }
             if (!ok) give_up(abort_flag, p.err);                   // and on, past every barrier, with whatever is there
             const bool zero = u.steps == 0 || (DKV && u.tile * BM + row >= p.n[u.b]);
-            if (DKV && p.splits > 1) {
-                float4* part = reinterpret_cast<float4*>(p.part) +
-                               (u.split * p.units + u.index) * 2 * (HD / 4) * BM + row;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {                      // acc0 and acc1, this thread's 64 dims of each
-                    uint32_t o[32];
-                    tmem_ld_x32_sync(tL + (c >> 1) * 128 + half * 64 + (c & 1) * 32, o);
-                    float4* dst = part + ((c >> 1) * (HD / 4) + half * 16 + (c & 1) * 8) * BM;
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        dst[v * BM] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                           : make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                                         __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
-                }
-                tc_fence_before();
-                continue;
-            }
 #pragma unroll 1
             for (int acc = 0; acc < (DKV ? 2 : 1); ++acc) {
-                const float f = acc == 0 ? p.scale : 1.0f;
-                uint32_t w[2][16];
+                uint32_t o[32];
+                tmem_ld_x32_sync(tL + acc * 128 + quarter * 32, o);
+                if (DKV && p.splits > 1) {
+                    float4* part = reinterpret_cast<float4*>(p.part) +
+                                   ((u.split * p.units + u.index) * 2 + acc) * (HD / 4) * BM + quarter * 8 * BM + row;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_x32_sync(tL + acc * 128 + half * 64 + c * 32, o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[c][e] = zero ? 0u : bf16_pair(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+                    for (int v = 0; v < 8; ++v)
+                        part[v * BM] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                            : make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                          __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                    continue;
                 }
-                if (leader) tma_store_wait_read();                 // the staging tile is free
-                compute_barrier();
-                uint8_t* dst = smem + (sO - sR) + half * HALF + row * 128;
+                const float f = acc == 0 ? p.scale : 1.0f;
+                uint32_t w[16];
 #pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    *reinterpret_cast<uint4*>(dst + ((v ^ (row & 7)) << 4)) =
-                        make_uint4(w[v >> 2][4 * (v & 3)], w[v >> 2][4 * (v & 3) + 1], w[v >> 2][4 * (v & 3) + 2],
-                                   w[v >> 2][4 * (v & 3) + 3]);
+                for (int e = 0; e < 16; ++e)
+                    w[e] = zero ? 0u : bf16_pair(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+                if (DKV && u.steps == 0) {                         // rows behind the stream's last: R may hold the next unit
+                    uint16_t* dst = (acc == 0 ? p.dk : p.dv) + ((static_cast<int64_t>(u.b) * p.Nk + u.tile * BM + row) * p.Hk + u.head) * HD + quarter * 32;
+                    if (u.tile * BM + row < p.Nk)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                if (!DKV) {
+                    if (leader) tma_store_wait_read();             // the output tile is free
+                    compute_barrier();
+                }
+                uint8_t* dst = smem + (sO - sR) + acc * TILE + (quarter >> 1) * HALF + row * 128;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    *reinterpret_cast<uint4*>(dst + ((((quarter & 1) * 4 + v) ^ (row & 7)) << 4)) =
+                        make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
                 fence_proxy_async();
                 compute_barrier();
                 if (leader)
                     for (int hf = 0; hf < 2; ++hf) {
                         if constexpr (DKV)
-                            tma_store_4d(acc == 0 ? &p.dkmap : &p.dvmap, sO + hf * HALF, hf * 64, u.head, u.tile * BM, u.b);
+                            tma_store_4d(acc == 0 ? &p.dkmap : &p.dvmap, sO + acc * TILE + hf * HALF, hf * 64, u.head, u.tile * BM, u.b);
                         else
                             tma_store_4d(&p.dqmap, sO + hf * HALF, hf * 64, u.head, u.tile * p.tokens, u.b);
                     }
             }
+            if (DKV && u.steps > 0 && leader) {                    // R0 and R1 are free for the next unit's tiles
+                tma_store_wait_read();
+                mbar_arrive(bar(REMPTY));
+            }
             tc_fence_before();
+            u = nx;
         }
         if (leader) tma_store_wait();
         __syncwarp();
@@ -466,38 +512,93 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
     }
 }
 
-// Adds the splits of a key tile's dK or dV in order.  grid: (units, 2); the tile is turned around in shared
-// memory, because its parts lie [dims / 4][row].
+// Adds the splits of a key tile's dK or dV in order.  grid: (units, 2, 4): a block adds 32 dims of 128 rows, turned
+// around in shared memory because the parts lie [dims / 4][row].
 __global__ void __launch_bounds__(256) cross_fold_kernel(const float4* __restrict__ part, int splits, int64_t units, int ktiles,
                                                          int Hk, int Nk, float scale, uint16_t* __restrict__ dk,
                                                          uint16_t* __restrict__ dv)
 {
-    __shared__ __align__(16) uint16_t tile[BM][HD + 8];
+    __shared__ __align__(16) uint16_t tile[BM][32 + 8];
     const int64_t unit = blockIdx.x;
     const int which = blockIdx.y;
-    for (int i = threadIdx.x; i < BM * (HD / 4); i += 256) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < splits; ++k) {
-            const float4 x = part[((k * units + unit) * 2 + which) * (BM * (HD / 4)) + i];
-            s.x += x.x;
-            s.y += x.y;
-            s.z += x.z;
-            s.w += x.w;
+    const int64_t step = units * 2 * (BM * (HD / 4));
+    const float4* src = part + (unit * 2 + which) * (BM * (HD / 4)) + blockIdx.z * 8 * BM + threadIdx.x;
+    float4 s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = src[i * 256];
+#pragma unroll 1
+    for (int k = 1; k < splits; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = src[k * step + i * 256];
+            s[i].x += x.x;
+            s[i].y += x.y;
+            s[i].z += x.z;
+            s[i].w += x.w;
         }
-        const float f = which == 0 ? scale : 1.0f;
-        *reinterpret_cast<uint2*>(&tile[i & 127][(i >> 7) * 4]) = make_uint2(bf16_pair(s.x * f, s.y * f), bf16_pair(s.z * f, s.w * f));
-    }
+    const float f = which == 0 ? scale : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(&tile[threadIdx.x & 127][(2 * i + (threadIdx.x >> 7)) * 4]) =
+            make_uint2(bf16_pair(s[i].x * f, s[i].y * f), bf16_pair(s[i].z * f, s[i].w * f));
     __syncthreads();
     const int64_t bh = unit / ktiles;
     const int kt = static_cast<int>(unit - bh * ktiles);
     const int64_t b = bh / Hk;
     const int hk = static_cast<int>(bh - b * Hk);
     uint16_t* out = which == 0 ? dk : dv;
-    for (int i = threadIdx.x; i < BM * 16; i += 256) {
-        const int r = i >> 4, v = i & 15;
+#pragma unroll
+    for (int i = threadIdx.x; i < BM * 4; i += 256) {
+        const int r = i >> 2, v = i & 3;
         const int64_t j = static_cast<int64_t>(kt) * BM + r;
         if (j < Nk)
-            *reinterpret_cast<uint4*>(out + ((b * Nk + j) * Hk + hk) * HD + v * 8) = *reinterpret_cast<const uint4*>(&tile[r][v * 8]);
+            *reinterpret_cast<uint4*>(out + ((b * Nk + j) * Hk + hk) * HD + blockIdx.z * 32 + v * 8) =
+                *reinterpret_cast<const uint4*>(&tile[r][v * 8]);
+    }
+}
+
+// -lse (log2 units) and -delta = -rowsum(dO * O) of a query tile's rows; rows that are none get lse = infinity, so
+// that their probabilities are 0.  One block per query tile, a half-warp per row, eight rows in flight.
+__global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* __restrict__ out, const uint16_t* __restrict__ dout,
+                                                          const float* __restrict__ lse, float* __restrict__ stats, int H,
+                                                          int Nq, int pack, int tokens, int qtiles, int packs)
+{
+    const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
+    const uint32_t bp = blockIdx.x / static_cast<uint32_t>(qtiles);
+    const int tile = static_cast<int>(blockIdx.x - bp * qtiles);
+    const int b = static_cast<int>(bp / static_cast<uint32_t>(packs));
+    const int h0 = static_cast<int>(bp - b * packs) * pack;
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = half + 16 * i;
+        const int rt = pack == 1 ? r : r / pack;
+        const int64_t tok = static_cast<int64_t>(tile) * tokens + rt;
+        sum[i] = 0.f;
+        if (rt < tokens && tok < Nq) {
+            const int64_t o = ((static_cast<int64_t>(b) * Nq + tok) * H + h0 + (r - rt * pack)) * HD + sub * 8;
+            const uint4 x = *reinterpret_cast<const uint4*>(out + o), y = *reinterpret_cast<const uint4*>(dout + o);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sum[i] = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum[i]);
+                sum[i] = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        const int r = half + 16 * i;
+        const int rt = pack == 1 ? r : r / pack;
+        const int64_t tok = static_cast<int64_t>(tile) * tokens + rt;
+        if (sub == 0) {
+            const bool live = rt < tokens && tok < Nq;
+            float* dst = stats + static_cast<int64_t>(blockIdx.x) * 2 * BM + r;
+            dst[0] = live ? -lse[(static_cast<int64_t>(b) * H + h0 + (r - rt * pack)) * Nq + tok] * kLog2e : -INFINITY;
+            dst[BM] = live ? -sum[i] : 0.f;
+        }
     }
 }
 
@@ -578,9 +679,10 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
         if (!encode_query_map(&p.dkmap, f.dk, c.Hk, c.Nk, c.B, kd, 1, BM) || !encode_query_map(&p.dvmap, f.dv, c.Hk, c.Nk, c.B, kd, 1, BM))
             return cudaErrorInvalidValue;
     }
-    p.lse = f.lse;
-    p.delta = f.delta;
+    p.stats = f.stats;
     p.part = f.part;
+    p.dk = f.dk;
+    p.dv = f.dv;
     p.err = c.err;
     p.timeout_ns = c.timeout_ns;
     p.B = c.B;
@@ -600,7 +702,9 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     const int64_t qunits = static_cast<int64_t>(c.B) * sh.packs * sh.qtiles;
     if (qunits > INT32_MAX || sh.kunits * sh.splits > INT32_MAX) return cudaErrorInvalidConfiguration;
 
-    cudaError_t e = launch_cross_delta(f, s);
+    cross_stats_kernel<<<dim3(static_cast<unsigned>(qunits)), 256, 0, s>>>(f.out, f.dout, f.lse, f.stats, c.H, c.Nq, sh.pack,
+                                                                           sh.tokens, sh.qtiles, sh.packs);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     static std::atomic<uint64_t> dq_set{0}, dkv_set{0};
     auto dq_kernel = cross_backward_kernel<false, CAP>;
@@ -621,13 +725,19 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     p.units = sh.kunits;
     dkv_kernel<<<dim3(static_cast<unsigned>(ctas)), NTHREADS, SMEM_BYTES, s>>>(p);
     if (sh.splits > 1)
-        cross_fold_kernel<<<dim3(static_cast<unsigned>(sh.kunits), 2), 256, 0, s>>>(reinterpret_cast<const float4*>(f.part), sh.splits,
+        cross_fold_kernel<<<dim3(static_cast<unsigned>(sh.kunits), 2, 4), 256, 0, s>>>(reinterpret_cast<const float4*>(f.part), sh.splits,
                                                                                     sh.kunits, sh.ktiles, c.Hk, c.Nk, c.scale,
                                                                                     f.dk, f.dv);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+size_t cross_backward_stats_bytes(int B, int H, int Hk, int64_t Nq)
+{
+    const Shape s = shape_of(B, H, Hk, Nq, 0);
+    return static_cast<size_t>(B) * s.packs * s.qtiles * 2 * BM * sizeof(float);
+}
 
 size_t cross_backward_part_bytes(int B, int H, int Hk, int64_t Nq, int64_t Nk)
 {

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant_
         const int64_t bi = row / p.c.H;
         const int h = static_cast<int>(row - bi * p.c.H);
         const int64_t b = bi / p.c.Nq;
-        p.delta[(b * p.c.H + h) * p.c.Nq + (bi - b * p.c.Nq)] = s;
+        p.stats[(b * p.c.H + h) * p.c.Nq + (bi - b * p.c.Nq)] = s;
     }
 }
 
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) cross_rows_dq_kernel(const __grid_constan
     const int64_t o = ((static_cast<int64_t>(b) * p.c.Nq + safe) * p.c.H + h) * HD + sub * 8;
     const Vec8 q = unpack8(load_vec(p.c.q + b * p.c.qs.batch + safe * p.c.qs.tok + h * p.c.qs.hd + sub * 8));
     const Vec8 dout = unpack8(load_vec(p.dout + o));
-    const float lse2 = p.lse[bh * p.c.Nq + safe] * kLog2e, delta = p.delta[bh * p.c.Nq + safe];
+    const float lse2 = p.lse[bh * p.c.Nq + safe] * kLog2e, delta = p.stats[bh * p.c.Nq + safe];
     const uint16_t* kb = p.c.k + b * p.c.kvs.batch + hk * p.c.kvs.hd + sub * 8;
     const uint16_t* vb = p.c.v + b * p.c.kvs.batch + hk * p.c.kvs.hd + sub * 8;
     float acc[8] = {};
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(256) cross_rows_dkv_kernel(const __grid_consta
                     unpack8(load_vec(p.dout + ((static_cast<int64_t>(b) * p.c.Nq + i) * p.c.H + h) * HD + sub * 8));
                 const float s = half_sum(dot8(q, k)), dp = half_sum(dot8(dout, v));
                 const float pr = exp2f(fmaf(s, sl2, -p.lse[stat + i] * kLog2e));
-                const float ds = n > 1 ? pr * (dp - p.delta[stat + i]) : 0.f;
+                const float ds = n > 1 ? pr * (dp - p.stats[stat + i]) : 0.f;
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
                     dk[d] = fmaf(ds, q.x[d], dk[d]);
@@ -367,21 +367,14 @@ cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, cross_rows_kernel, p, splits, static_cast<int>(row_blocks));
 }
 
-cudaError_t launch_cross_delta(const CrossBackward& p, cudaStream_t s)
-{
-    const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Nq * p.c.H;
-    if ((rows + 15) / 16 > INT32_MAX) return cudaErrorInvalidConfiguration;
-    cross_delta_kernel<<<static_cast<unsigned>((rows + 15) / 16), 256, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
 cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s)
 {
+    const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Nq * p.c.H;
     const int64_t qb = (static_cast<int64_t>(p.c.Nq) + 15) / 16, kb = (static_cast<int64_t>(p.c.Nk) + 15) / 16;
     const int64_t dq_blocks = qb * p.c.B * p.c.H, dkv_blocks = kb * p.c.B * p.c.Hk;
-    if (dq_blocks > INT32_MAX || dkv_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_cross_delta(p, s);
-    if (e != cudaSuccess) return e;
+    if ((rows + 15) / 16 > INT32_MAX || dq_blocks > INT32_MAX || dkv_blocks > INT32_MAX)
+        return cudaErrorInvalidConfiguration;
+    cross_delta_kernel<<<static_cast<unsigned>((rows + 15) / 16), 256, 0, s>>>(p);
     cross_rows_dq_kernel<<<static_cast<unsigned>(dq_blocks), 256, 0, s>>>(p, static_cast<int>(qb));
     if (dkv_blocks > 0) cross_rows_dkv_kernel<<<static_cast<unsigned>(dkv_blocks), 256, 0, s>>>(p, static_cast<int>(kb));
     return cudaGetLastError();

@@ -17,6 +17,14 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// (a.lo*b.lo, a.hi*b.hi), each rounded once.
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Columns at and past `valid` become -infinity.
 __device__ __forceinline__ void mask_columns(uint32_t (&r)[32], int valid)
 {
