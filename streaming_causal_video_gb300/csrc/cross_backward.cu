@@ -203,6 +203,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                     mbar_arrive_expect_tx(bar(RFULL), 2 * query_bytes);
                     load_queries(&p.qmap, sR, RFULL, u.head, u.tile * p.tokens, u.b);
                     load_queries(&p.domap, sR + TILE, RFULL, u.head, u.tile * p.tokens, u.b);
+                    // the next unit's tiles reach L2 while this one runs: its load is on the way between units
+                    Walk<DKV, CAP> ahead = walk;
+                    Unit nx;
+                    if (ahead.next(p, nx) && nx.steps > 0)
+                        for (int hf = 0; hf < 2; ++hf) {
+                            tma_prefetch_4d(&p.qmap, hf * 64, nx.head, nx.tile * p.tokens, nx.b);
+                            tma_prefetch_4d(&p.domap, hf * 64, nx.head, nx.tile * p.tokens, nx.b);
+                        }
                 }
                 ++units;
             }
@@ -386,11 +394,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 for (int c = 0; c < 2; ++c) {
                     uint32_t x[16], w[8];
                     tmem_ld_x16_sync(tL + SCOL + quarter * 32 + c * 16, x);
+                    ulonglong2 st[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[e] = DKV ? reinterpret_cast<const ulonglong2*>(cl)[c * 4 + e] : ulonglong2{lse2, lse2};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        uint64_t m2;
-                        if constexpr (DKV) m2 = reinterpret_cast<const uint64_t*>(cl)[c * 8 + e];
-                        else m2 = lse2;
+                        const uint64_t m2 = e & 1 ? st[e >> 1].y : st[e >> 1].x;
                         float a, b;
                         f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2x2, m2), a, b);
                         a = ex2_approx(a);
@@ -412,11 +421,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 for (int c = 0; c < 2; ++c) {
                     uint32_t x[16], w[8];
                     tmem_ld_x16_sync(tL + XCOL + quarter * 32 + c * 16, x);
+                    ulonglong2 st[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[e] = DKV ? reinterpret_cast<const ulonglong2*>(cd)[c * 4 + e] : ulonglong2{delta2, delta2};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        uint64_t m2;
-                        if constexpr (DKV) m2 = reinterpret_cast<const uint64_t*>(cd)[c * 8 + e];
-                        else m2 = delta2;
+                        const uint64_t m2 = e & 1 ? st[e >> 1].y : st[e >> 1].x;
                         float a, b;
                         f32x2_unpack(fmul2(fadd2(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), m2), pr[c * 8 + e]), a, b);
                         w[e] = constant ? 0u : bf16_pair(a, b);
@@ -558,7 +568,7 @@ __global__ void __launch_bounds__(256) cross_fold_kernel(const float4* __restric
 }
 
 // -lse (log2 units) and -delta = -rowsum(dO * O) of a query tile's rows; rows that are none get lse = infinity, so
-// that their probabilities are 0.  One block per query tile, a half-warp per row, eight rows in flight.
+// that their probabilities are 0.  grid: (query tiles, 4): a half-warp per row, two rows each.
 __global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* __restrict__ out, const uint16_t* __restrict__ dout,
                                                           const float* __restrict__ lse, float* __restrict__ stats, int H,
                                                           int Nq, int pack, int tokens, int qtiles, int packs)
@@ -568,36 +578,40 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* __rest
     const int tile = static_cast<int>(blockIdx.x - bp * qtiles);
     const int b = static_cast<int>(bp / static_cast<uint32_t>(packs));
     const int h0 = static_cast<int>(bp - b * packs) * pack;
-    float sum[8];
+    uint4 x[2], y[2];
+    float l[2];
+    bool live[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = half + 16 * i;
+    for (int i = 0; i < 2; ++i) {
+        const int r = blockIdx.y * 32 + half + 16 * i;
         const int rt = pack == 1 ? r : r / pack;
         const int64_t tok = static_cast<int64_t>(tile) * tokens + rt;
-        sum[i] = 0.f;
-        if (rt < tokens && tok < Nq) {
-            const int64_t o = ((static_cast<int64_t>(b) * Nq + tok) * H + h0 + (r - rt * pack)) * HD + sub * 8;
-            const uint4 x = *reinterpret_cast<const uint4*>(out + o), y = *reinterpret_cast<const uint4*>(dout + o);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sum[i] = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum[i]);
-                sum[i] = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum[i]);
-            }
+        live[i] = rt < tokens && tok < Nq;
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        l[i] = INFINITY;
+        if (live[i]) {
+            const int h = h0 + (r - rt * pack);
+            const int64_t o = ((static_cast<int64_t>(b) * Nq + tok) * H + h) * HD + sub * 8;
+            x[i] = *reinterpret_cast<const uint4*>(out + o);
+            y[i] = *reinterpret_cast<const uint4*>(dout + o);
+            l[i] = lse[(static_cast<int64_t>(b) * H + h) * Nq + tok];
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+        float sum = 0.f;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        const int r = half + 16 * i;
-        const int rt = pack == 1 ? r : r / pack;
-        const int64_t tok = static_cast<int64_t>(tile) * tokens + rt;
+        for (int k = 0; k < 4; ++k) {
+            sum = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum);
+            sum = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (sub == 0) {
-            const bool live = rt < tokens && tok < Nq;
-            float* dst = stats + static_cast<int64_t>(blockIdx.x) * 2 * BM + r;
-            dst[0] = live ? -lse[(static_cast<int64_t>(b) * H + h0 + (r - rt * pack)) * Nq + tok] * kLog2e : -INFINITY;
-            dst[BM] = live ? -sum[i] : 0.f;
+            float* dst = stats + static_cast<int64_t>(blockIdx.x) * 2 * BM + blockIdx.y * 32 + half + 16 * i;
+            dst[0] = -l[i] * kLog2e;
+            dst[BM] = live[i] ? -sum : 0.f;
         }
     }
 }
@@ -702,7 +716,7 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     const int64_t qunits = static_cast<int64_t>(c.B) * sh.packs * sh.qtiles;
     if (qunits > INT32_MAX || sh.kunits * sh.splits > INT32_MAX) return cudaErrorInvalidConfiguration;
 
-    cross_stats_kernel<<<dim3(static_cast<unsigned>(qunits)), 256, 0, s>>>(f.out, f.dout, f.lse, f.stats, c.H, c.Nq, sh.pack,
+    cross_stats_kernel<<<dim3(static_cast<unsigned>(qunits), 4), 256, 0, s>>>(f.out, f.dout, f.lse, f.stats, c.H, c.Nq, sh.pack,
                                                                            sh.tokens, sh.qtiles, sh.packs);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
