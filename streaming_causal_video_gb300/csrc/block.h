@@ -85,7 +85,7 @@ struct NormParams {
 
 // Blocks that share the rows of one group in the backward pass; the workspace holds one row of
 // partial sums of dweight and dbias for each.
-int norm_backward_slices(int64_t rows, int64_t rows_per_group, int cols);
+int norm_backward_slices(int64_t rows, int64_t rows_per_group, int cols, bool aligned);
 
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const NormParams& p, cudaStream_t s);

@@ -278,7 +278,7 @@ size_t sdv2_norm_workspace_bytes(const sdv2_norm_cfg* c)
 {
     if (check_norm(c) != SDV2_OK) return 0;
     const int64_t per = std::min(rows_of(c), c->rows);
-    const int slices = norm_backward_slices(c->rows, per, c->cols);
+    const int slices = norm_backward_slices(c->rows, per, c->cols, norm_params(c, nullptr, nullptr).aligned);
     const size_t groups = static_cast<size_t>((c->rows + per - 1) / per);
     return slices > 1 ? (groups * slices * 2 * c->cols * sizeof(float) + 255) / 256 * 256 : 256;
 }
@@ -304,7 +304,7 @@ sdv2_status sdv2_layer_norm_backward(const sdv2_norm_cfg* c, const void* dy, con
     p.dweight = dweight;
     p.dbias = dbias;
     p.partial = static_cast<float*>(ws);
-    p.slices = norm_backward_slices(p.rows, p.rows_per_group, p.cols);
+    p.slices = norm_backward_slices(p.rows, p.rows_per_group, p.cols, p.aligned);
     return done(launch_layer_norm_backward(p, static_cast<cudaStream_t>(stream)), "layer norm backward launch");
 }
 

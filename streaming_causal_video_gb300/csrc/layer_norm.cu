@@ -10,71 +10,121 @@
 //             dx = rstd * (g - mean(g) - xhat * mean(g * xhat));
 //             dgain = sum over rows of dy * xhat, dbias = sum of dy.
 // Both are bound by memory: each row is read once and written once and stays in registers in
-// between.  The parameter sums of a group are split over `slices` blocks, each of which keeps its
-// columns' sums in registers over all of its rows and writes them once; a second kernel adds the
-// slices in index order, so the result does not depend on the order in which blocks run.
-#include <cuda_bf16.h>
-
+// between.  What decides the rate is how many rows are on their way while a row's sums are exchanged
+// between threads, so a team of threads walks over rows that it copies ahead into its own part of
+// shared memory (cp.async; every thread reads back only what it copied, so no barrier is needed for
+// it).  A row at a time without that took 2 us a row: 38.7 us for the 14B forward, 18.7 us for the
+// 1.3B backward.  Rows that do not start on 16 bytes are read element by element, one row ahead in
+// registers.  A thread holds vectors of eight neighbouring columns (of four where x or y is fp32, so that a
+// warp reads whole sectors: 32 bytes a thread in two copies of 16 took 42.9 us for the 14B forward),
+// and as many of them as registers allow, with the group's gain and bias, and works on pairs of them (f32x2): with one instruction per
+// operation and column, and a test of every vector against the row's end, a row took 695
+// instructions a warp and the 14B forward 43.4 us.  Rows whose vectors fill their threads exactly need
+// no such test (kFull).
+// The parameter sums of a group are split over `slices` blocks, each of which keeps its columns' sums
+// in registers over all of its rows and writes them once; a second kernel adds the slices in index
+// order, so the result does not depend on the order in which blocks run.
 #include <algorithm>
 
 #include "block.h"
+#include "softmax_tile.cuh"
 
 namespace sdv2 {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kSms = 152;
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void* base, int64_t i)
+// How a row's elements are reached: one by one, in vectors of eight, and in vectors that fill all threads.
+enum Rows { kSingle, kVector, kFull };
+
+__device__ __forceinline__ uint64_t both(float v) { return f32x2_pack(v, v); }
+__device__ __forceinline__ float add_pair(uint64_t v)
 {
-    if constexpr (F32) return static_cast<const float*>(base)[i];
-    else return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
+    float a, b;
+    f32x2_unpack(v, a, b);
+    return a + b;
 }
 
-// Eight consecutive columns from element offset `i` (a multiple of 8, 16-byte aligned rows).
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t i, float* v)
+// Columns of a vector.
+constexpr int columns(bool x_f32, bool y_f32) { return x_f32 || y_f32 ? 4 : 8; }
+
+// The first n of C consecutive columns of a row that is not aligned, and 0 in the rest, as pairs.
+template <int C, bool F32>
+__device__ __forceinline__ void load_part(const void* base, int64_t i, int n, uint64_t* v)
 {
-    if constexpr (F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float x[C];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = __uint_as_float(u[k] << 16);
-            v[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    for (int k = 0; k < C; ++k) {
+        x[k] = 0.f;
+        if (k < n) {
+            if constexpr (F32) x[k] = static_cast<const float*>(base)[i + k];
+            else x[k] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i + k]) << 16);
         }
+    }
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) v[k] = f32x2_pack(x[2 * k], x[2 * k + 1]);
+}
+
+// Stores n of C columns; all of them at once where VECTOR.
+template <int C, bool F32, bool VECTOR>
+__device__ __forceinline__ void store_columns(void* base, int64_t i, int n, const uint64_t* v)
+{
+    float x[C];
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) f32x2_unpack(v[k], x[2 * k], x[2 * k + 1]);
+    if constexpr (!VECTOR) {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            if (k < n) {
+                if constexpr (F32) static_cast<float*>(base)[i + k] = x[k];
+                else static_cast<__nv_bfloat16*>(base)[i + k] = __float2bfloat16_rn(x[k]);
+            }
+    } else if constexpr (F32) {
+        static_assert(C == 4, "fp32 vectors have four columns");
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if constexpr (C == 4) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+            make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void store1(void* base, int64_t i, float v)
+// C parameters (fp32, which no output overlaps) as pairs.
+template <int C>
+__device__ __forceinline__ void load_param(const float* p, bool vector, int n, uint64_t* v)
 {
-    if constexpr (F32) static_cast<float*>(base)[i] = v;
-    else static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+    float x[C];
+    if (vector) {
+#pragma unroll
+        for (int k = 0; k < C; k += 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p + k));
+            x[k] = a.x; x[k + 1] = a.y; x[k + 2] = a.z; x[k + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k) x[k] = k < n ? __ldg(p + k) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) v[k] = f32x2_pack(x[2 * k], x[2 * k + 1]);
 }
 
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t i, const float* v)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
-    if constexpr (F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-            u[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = make_uint4(u[0], u[1], u[2], u[3]);
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the newest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -83,358 +133,522 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// The same over lanes 0-15, for every lane (a team has at most 16 warps).
+__device__ __forceinline__ float warp_sum16(float v)
+{
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
 __device__ __forceinline__ void team_barrier(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sum over the `warps` warps of one row's team; every thread gets the same value (the partial sums
-// are added in warp order).  `scratch` holds one float per warp; `id` is the team's barrier.
-__device__ __forceinline__ float team_sum(float v, int warps, int warp, float* scratch, int id)
+// R sums over the `warps` warps of a team; every thread gets the same values (both levels are fixed trees).
+// `scratch` holds R floats per warp; `id` is the team's barrier.
+template <int R>
+__device__ __forceinline__ void team_sums(float (&v)[R], int warps, int warp, float* scratch, int id)
 {
-    v = warp_sum(v);
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) scratch[warp] = v;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = warp_sum(v[r]);
+    if (warps == 1) return;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) scratch[r * warps + warp] = v[r];
     team_barrier(id, warps * 32);
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += scratch[w];
-    return s;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = warp_sum16(lane < warps ? scratch[r * warps + lane] : 0.f);
 }
 
-// A thread's columns: NV vectors of 8, vector i starting at column 8*(i*team + t) where the row can
-// be read in 16-byte vectors, else 8*NV single columns i*team + t (still coalesced).
-template <int NV, bool ALIGNED, typename F>
-__device__ __forceinline__ void for_columns(int team, int t, int cols, F&& f)
+// A thread's columns: N vectors of C, vector i starting at column C*(i*team + t).  f(first pair of the vector,
+// column, how many of its columns the row has).
+template <int N, int C, Rows MODE, typename F>
+__device__ __forceinline__ void for_vectors(int team, int t, int cols, F&& f)
 {
-    if constexpr (ALIGNED) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (i * team + t);
-            if (c < cols) f(i * 8, c);
+    for (int i = 0; i < N; ++i) {
+        const int c = C * (i * team + t);
+        if constexpr (MODE == kFull) f(i * (C / 2), c, C);
+        else if (c < cols) f(i * (C / 2), c, min(C, cols - c));
+    }
+}
+
+// A thread's vectors of one row of x or dy, copied ahead: vector i of slot `slot` lies at
+// base + (slot*N + i) * threads * BYTES; base is the thread's own.
+template <int N, int C, bool F32, Rows MODE>
+struct Ring {
+    static constexpr int BYTES = C * (F32 ? 4 : 2);
+    uint32_t base;
+    int threads;
+    __device__ uint32_t at(int slot, int i) const { return base + (slot * N + i) * threads * BYTES; }
+    // row: the row's first element
+    __device__ void copy(int slot, const char* row, int team, int t, int cols) const
+    {
+        const char* src = row + t * BYTES;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (MODE == kFull || C * (i * team + t) < cols) {
+                if constexpr (BYTES == 16) copy16(at(slot, i), src + i * team * BYTES);
+                else copy8(at(slot, i), src + i * team * BYTES);
+            }
+    }
+    __device__ void read(int slot, int team, int t, int cols, uint64_t* v) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t w[BYTES / 4] = {};
+            if (MODE == kFull || C * (i * team + t) < cols) {
+                if constexpr (BYTES == 16)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at(slot, i)) : "memory");
+                else asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at(slot, i)) : "memory");
+            }
+#pragma unroll
+            for (int k = 0; k < C / 2; ++k) {
+                if constexpr (F32) v[(C / 2) * i + k] = f32x2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+                else v[(C / 2) * i + k] = f32x2_pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            }
+        }
+    }
+};
+
+// Rows copied ahead: up to 192 bytes a thread.
+constexpr int stages(int bytes_per_row) { return bytes_per_row <= 32 ? 6 : bytes_per_row <= 48 ? 4 : bytes_per_row <= 64 ? 3 : 2; }
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ const char* row_of(const void* base, int64_t row, int64_t stride, bool f32)
+{
+    return static_cast<const char*>(base) + row * stride * (f32 ? 4 : 2);
+}
+
+// blockDim = (team, teams): a team takes the rows of its index, then every gridDim * teams further.
+template <int NV, Rows MODE, bool XF32, bool YF32>
+__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormParams p)
+{
+    constexpr bool VECTOR = MODE != kSingle;
+    constexpr int C = columns(XF32, YF32), N = NV * 8 / C;
+    constexpr int S = stages(NV * 16 * (XF32 ? 2 : 1));
+    extern __shared__ __align__(16) uint8_t copied[];
+    __shared__ float scratch[2][2][kMaxThreads / 32];
+    const int team = blockDim.x, t = threadIdx.x;
+    const int warps = team >> 5, warp = t >> 5;
+    const int id = 1 + threadIdx.y;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= p.rows) return;                         // whole team: its barrier is its own
+    using RingX = Ring<N, C, XF32, MODE>;
+    const RingX ring{shared_address(copied) + (threadIdx.y * team + t) * RingX::BYTES, team * static_cast<int>(blockDim.y)};
+    uint64_t next[VECTOR ? 1 : NV * 4];                // single elements: the next row
+    auto fetch = [&](int64_t r) {
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) { load_part<C, XF32>(p.x, r * p.xs + c, n, next + i); });
+    };
+    if constexpr (VECTOR) {
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            if (row + k * step < p.rows) ring.copy(k, row_of(p.x, row + k * step, p.xs, XF32), team, t, p.cols);
+            copy_commit();
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV * 8; ++i) {
-            const int c = i * team + t;
-            if (c < cols) f(i, c);
-        }
+        for (int i = 0; i < NV * 4; ++i) next[i] = 0;
+        fetch(row);
     }
-}
-
-// blockDim = (team, rows per block): one row per team of `team` threads (a multiple of 32).
-template <int NV, bool ALIGNED, bool XF32, bool YF32>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormParams p)
-{
-    constexpr int W = ALIGNED ? 8 : 1;
-    __shared__ float scratch[2][kMaxThreads / 32];
-    const int team = blockDim.x, t = threadIdx.x;
-    const int warps = team >> 5, warp = t >> 5;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (row >= p.rows) return;                         // whole team: its barrier is its own
-    float* s0 = scratch[0] + threadIdx.y * warps;
-    float* s1 = scratch[1] + threadIdx.y * warps;
-    const int id = 1 + threadIdx.y;
-
-    float v[NV * 8];
-#pragma unroll
-    for (int i = 0; i < NV * 8; ++i) v[i] = 0.f;
-    for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int c) {
-        if constexpr (ALIGNED) load8<XF32>(p.x, row * p.xs + c, v + i);
-        else v[i] = load1<XF32>(p.x, row * p.xs + c);
-    });
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV * 8; ++i) sum += v[i];
-    const float mean = team_sum(sum, warps, warp, s0, id) / static_cast<float>(p.cols);
-    float sq = 0.f;
-    for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int) {
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            v[i + k] -= mean;
-            sq = fmaf(v[i + k], v[i + k], sq);
-        }
-    });
-    const float var = team_sum(sq, warps, warp, s1, id) / static_cast<float>(p.cols);
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    if (t == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    const int64_t g = (row / p.rows_per_group) * p.gs;
-    const float base = p.plus_one ? 1.0f : 0.0f;
-    for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int c) {
-        float w[W], b[W];
-        if constexpr (ALIGNED) {
-            if (p.weight) load8<true>(p.weight, g + c, w);
-            if (p.bias) load8<true>(p.bias, g + c, b);
-        } else {
-            if (p.weight) w[0] = p.weight[g + c];
-            if (p.bias) b[0] = p.bias[g + c];
-        }
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            const float gain = p.weight ? base + w[k] : 1.0f;
-            v[i + k] = fmaf(v[i + k] * rstd, gain, p.bias ? b[k] : 0.f);
-        }
-        if constexpr (ALIGNED) store8<YF32>(p.y, row * p.ys + c, v + i);
-        else store1<YF32>(p.y, row * p.ys + c, v[i]);
-    });
-}
-
-// blockDim = (team, teams); block (group, slice) walks the group's rows slice*teams + team index,
-// then every slices*teams further.  Each thread keeps dgain and dbias of its columns.
-template <int NV, bool ALIGNED, bool XF32, bool YF32>
-__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormParams p)
-{
-    constexpr int W = ALIGNED ? 8 : 1;
-    extern __shared__ float dyn[];                     // [teams][2][cols] for the teams' sums
-    __shared__ float scratch[4][kMaxThreads / 32];
-    const int team = blockDim.x, t = threadIdx.x, teams = blockDim.y, slot = threadIdx.y;
-    const int warps = team >> 5, warp = t >> 5;
-    const int id = 1 + slot;
-    const int64_t group = blockIdx.x / p.slices;
-    const int slice = static_cast<int>(blockIdx.x - group * p.slices);
-    const int64_t row_end = min(p.rows, (group + 1) * p.rows_per_group);
-    const int64_t g = group * p.gs;
-    const float base = p.plus_one ? 1.0f : 0.0f;
     const float inv_cols = 1.0f / static_cast<float>(p.cols);
-
-    float dw[NV * 8], db[NV * 8], gain[NV * 8];
+    uint64_t gain[NV * 4], bias[NV * 4];
+    int64_t group_end = 0;
+    int slot = 0, phase = 0;
+#pragma unroll 1
+    for (; row < p.rows; row += step) {
+        if (row >= group_end) {
+            const int64_t group = row / p.rows_per_group;
+            group_end = (group + 1) * p.rows_per_group;
+            for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
 #pragma unroll
-    for (int i = 0; i < NV * 8; ++i) {
-        dw[i] = 0.f;
-        db[i] = 0.f;
-        gain[i] = 1.f;
+                for (int k = i; k < i + C / 2; ++k) {
+                    gain[k] = both(1.f);
+                    bias[k] = 0;
+                }
+                if (p.weight) {
+                    load_param<C>(p.weight + group * p.gs + c, VECTOR, n, gain + i);
+                    if (p.plus_one)
+#pragma unroll
+                        for (int k = i; k < i + C / 2; ++k) gain[k] = fadd2(gain[k], both(1.f));
+                }
+                if (p.bias) load_param<C>(p.bias + group * p.gs + c, VECTOR, n, bias + i);
+            });
+        }
+        uint64_t v[NV * 4];
+        if constexpr (VECTOR) {
+            copy_wait<S - 1>();
+            ring.read(slot, team, t, p.cols, v);
+            if (row + S * step < p.rows) ring.copy(slot, row_of(p.x, row + S * step, p.xs, XF32), team, t, p.cols);
+            copy_commit();
+            if (++slot == S) slot = 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV * 4; ++i) v[i] = next[i];
+            if (row + step < p.rows) fetch(row + step);
+        }
+        uint64_t two[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i) two[i & 1] = fadd2(two[i & 1], v[i]);
+        float mean[1] = {add_pair(fadd2(two[0], two[1]))};
+        // two sets of scratch in turn: a warp that is a row ahead does not touch what others still read
+        team_sums<1>(mean, warps, warp, scratch[phase][0] + threadIdx.y * warps, id);
+        mean[0] *= inv_cols;
+        two[0] = two[1] = 0;
+        const uint64_t minus = both(-mean[0]);
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int, int n) {
+#pragma unroll
+            for (int k = 0; k < C / 2; ++k) {
+                uint64_t d = fadd2(v[i + k], minus);
+                if constexpr (!VECTOR) {               // columns past the row's end stay 0
+                    float a, b;
+                    f32x2_unpack(d, a, b);
+                    d = f32x2_pack(2 * k < n ? a : 0.f, 2 * k + 1 < n ? b : 0.f);
+                }
+                v[i + k] = d;
+                two[k & 1] = ffma2(d, d, two[k & 1]);
+            }
+        });
+        float var[1] = {add_pair(fadd2(two[0], two[1]))};
+        team_sums<1>(var, warps, warp, scratch[phase][1] + threadIdx.y * warps, id);
+        phase ^= 1;
+        const float rstd = 1.0f / sqrtf(fmaf(var[0], inv_cols, p.eps));
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mean[0];
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        const uint64_t rstd2 = both(rstd);
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
+            uint64_t y[C / 2];
+#pragma unroll
+            for (int k = 0; k < C / 2; ++k) y[k] = ffma2(fmul2(v[i + k], rstd2), gain[i + k], bias[i + k]);
+            store_columns<C, YF32, VECTOR>(p.y, row * p.ys + c, n, y);
+        });
+    }
+}
+
+// blockDim = (team, teams); block (group, slice): its teams take the group's rows slice*teams + team, then
+// every slices*teams further.  Each thread keeps dgain and dbias of its columns.
+template <int NV, Rows MODE, bool XF32, bool YF32>
+__global__ void __launch_bounds__(kMaxThreads, NV == 1 && MODE != kSingle ? 2 : 1) norm_backward_kernel(const NormParams p)
+{
+    constexpr bool VECTOR = MODE != kSingle;
+    constexpr int C = columns(XF32, YF32), N = NV * 8 / C;
+    constexpr int S = stages(NV * 16 * ((XF32 ? 2 : 1) + (YF32 ? 2 : 1)));
+    extern __shared__ __align__(16) uint8_t copied[];  // the rows copied ahead; at the end the teams' sums [teams][2][cols]
+    float* dyn = reinterpret_cast<float*>(copied);
+    __shared__ float scratch[2][2 * kMaxThreads / 32];
+    const int team = blockDim.x, t = threadIdx.x, teams = blockDim.y, slot_id = threadIdx.y;
+    const int warps = team >> 5, warp = t >> 5;
+    const int id = 1 + slot_id;
+    const uint32_t group = blockIdx.x / static_cast<uint32_t>(p.slices);
+    const int slice = static_cast<int>(blockIdx.x - group * p.slices);
+    const int64_t row_end = min(p.rows, (group + int64_t(1)) * p.rows_per_group);
+    const int64_t step = static_cast<int64_t>(p.slices) * teams;
+    const int64_t g = group * p.gs;
+    const float inv_cols = 1.0f / static_cast<float>(p.cols);
+    const int threads = team * teams, tid = slot_id * team + t;
+    using RingX = Ring<N, C, XF32, MODE>;
+    using RingY = Ring<N, C, YF32, MODE>;
+    const RingX ring_x{shared_address(copied) + tid * RingX::BYTES, threads};
+    const RingY ring_y{shared_address(copied) + S * N * threads * RingX::BYTES + tid * RingY::BYTES, threads};
+
+    int64_t row = group * p.rows_per_group + static_cast<int64_t>(slice) * teams + slot_id;
+    uint64_t next_x[VECTOR ? 1 : NV * 4], next_y[VECTOR ? 1 : NV * 4];  // single elements: the next row
+    auto fetch = [&](int64_t r) {
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
+            load_part<C, XF32>(p.x, r * p.xs + c, n, next_x + i);
+            load_part<C, YF32>(p.dy, r * p.ys + c, n, next_y + i);
+        });
+    };
+    auto copy = [&](int slot, int64_t r) {
+        ring_x.copy(slot, row_of(p.x, r, p.xs, XF32), team, t, p.cols);
+        ring_y.copy(slot, row_of(p.dy, r, p.ys, YF32), team, t, p.cols);
+    };
+    float next_mean = 0.f, next_rstd = 0.f;
+    if (row < row_end) {
+        next_mean = p.mean[row];
+        next_rstd = p.rstd[row];
+    }
+    if constexpr (VECTOR) {
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            if (row + k * step < row_end) copy(k, row + k * step);
+            copy_commit();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV * 4; ++i) {
+            next_x[i] = 0;
+            next_y[i] = 0;
+        }
+        if (row < row_end) fetch(row);
+    }
+    uint64_t dw[NV * 4], db[NV * 4], gain[NV * 4];
+#pragma unroll
+    for (int i = 0; i < NV * 4; ++i) {
+        dw[i] = 0;
+        db[i] = 0;
+        gain[i] = both(1.f);
     }
     if (p.weight)
-        for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int c) {
-            if constexpr (ALIGNED) load8<true>(p.weight, g + c, gain + i);
-            else gain[i] = p.weight[g + c];
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
+            load_param<C>(p.weight + g + c, VECTOR, n, gain + i);
+            if (p.plus_one)
 #pragma unroll
-            for (int k = 0; k < W; ++k) gain[i + k] += base;
+                for (int k = i; k < i + C / 2; ++k) gain[k] = fadd2(gain[k], both(1.f));
         });
-    int phase = 0;
-    for (int64_t row = group * p.rows_per_group + static_cast<int64_t>(slice) * teams + slot; row < row_end;
-         row += static_cast<int64_t>(p.slices) * teams) {
-        float xh[NV * 8], gy[NV * 8];
-#pragma unroll
-        for (int i = 0; i < NV * 8; ++i) {
-            xh[i] = 0.f;
-            gy[i] = 0.f;
+    int slot = 0, phase = 0;
+#pragma unroll 1
+    for (; row < row_end; row += step) {
+        uint64_t xh[NV * 4], gy[NV * 4];
+        const uint64_t mean = both(-next_mean), rstd = both(next_rstd);
+        if (row + step < row_end) {
+            next_mean = p.mean[row + step];
+            next_rstd = p.rstd[row + step];
         }
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int c) {
-            if constexpr (ALIGNED) {
-                load8<XF32>(p.x, row * p.xs + c, xh + i);
-                load8<YF32>(p.dy, row * p.ys + c, gy + i);
-            } else {
-                xh[i] = load1<XF32>(p.x, row * p.xs + c);
-                gy[i] = load1<YF32>(p.dy, row * p.ys + c);
-            }
-        });
-        float s1 = 0.f, s2 = 0.f;
-        for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int) {
+        if constexpr (VECTOR) {
+            copy_wait<S - 1>();
+            ring_x.read(slot, team, t, p.cols, xh);
+            ring_y.read(slot, team, t, p.cols, gy);
+            if (row + S * step < row_end) copy(slot, row + S * step);
+            copy_commit();
+            if (++slot == S) slot = 0;
+        } else {
 #pragma unroll
-            for (int k = i; k < i + W; ++k) {
-                xh[k] = (xh[k] - mean) * rstd;
-                dw[k] = fmaf(gy[k], xh[k], dw[k]);
-                db[k] += gy[k];
-                gy[k] *= gain[k];
-                s1 += gy[k];
-                s2 = fmaf(gy[k], xh[k], s2);
+            for (int i = 0; i < NV * 4; ++i) {
+                xh[i] = next_x[i];
+                gy[i] = next_y[i];
             }
-        });
+            if (row + step < row_end) fetch(row + step);
+        }
+        // past the row's end dy is 0, and so is what it multiplies
+        uint64_t sum0[2] = {0, 0}, sum1[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < NV * 4; ++k) {
+            xh[k] = fmul2(fadd2(xh[k], mean), rstd);
+            dw[k] = ffma2(gy[k], xh[k], dw[k]);
+            db[k] = fadd2(db[k], gy[k]);
+            gy[k] = fmul2(gy[k], gain[k]);
+            sum0[k & 1] = fadd2(sum0[k & 1], gy[k]);
+            sum1[k & 1] = ffma2(gy[k], xh[k], sum1[k & 1]);
+        }
+        float s[2] = {add_pair(fadd2(sum0[0], sum0[1])), add_pair(fadd2(sum1[0], sum1[1]))};
         // two scratch rows in turn: a warp that is a row ahead does not touch what others still read
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (warps > 1) {
-            float* a = scratch[2 * phase] + slot * warps;
-            float* b = scratch[2 * phase + 1] + slot * warps;
-            if ((t & 31) == 0) {
-                a[warp] = s1;
-                b[warp] = s2;
-            }
-            team_barrier(id, team);
-            s1 = 0.f;
-            s2 = 0.f;
-            for (int w = 0; w < warps; ++w) {
-                s1 += a[w];
-                s2 += b[w];
-            }
-            phase ^= 1;
-        }
-        s1 *= inv_cols;
-        s2 *= inv_cols;
-        for_columns<NV, ALIGNED>(team, t, p.cols, [&](int i, int c) {
+        team_sums<2>(s, warps, warp, scratch[phase] + slot_id * warps * 2, id);
+        phase ^= 1;
+        const uint64_t minus0 = both(-s[0] * inv_cols), minus1 = both(-s[1] * inv_cols);
+        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
+            uint64_t d[C / 2];
 #pragma unroll
-            for (int k = i; k < i + W; ++k) gy[k] = (gy[k] - s1 - xh[k] * s2) * rstd;
-            if constexpr (ALIGNED) store8<XF32>(p.y, row * p.xs + c, gy + i);
-            else store1<XF32>(p.y, row * p.xs + c, gy[i]);
+            for (int k = 0; k < C / 2; ++k) d[k] = fmul2(ffma2(xh[i + k], minus1, fadd2(gy[i + k], minus0)), rstd);
+            store_columns<C, XF32, VECTOR>(p.y, row * p.xs + c, n, d);
         });
     }
     if (!p.dweight && !p.dbias) return;
     // the teams' sums, added in team order, then one row of partial sums for the block
     const int cols = p.cols;
     if (teams > 1) {
-        for_columns<NV, ALIGNED>(team, t, cols, [&](int i, int c) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                dyn[(slot * 2) * cols + c + k] = dw[i + k];
-                dyn[(slot * 2 + 1) * cols + c + k] = db[i + k];
-            }
+        if constexpr (VECTOR) copy_wait<0>();
+        __syncthreads();                               // every team is done with the rows copied ahead
+        for_vectors<N, C, MODE>(team, t, cols, [&](int i, int c, int n) {
+            store_columns<C, true, false>(dyn, (slot_id * 2) * cols + c, n, dw + i);
+            store_columns<C, true, false>(dyn, (slot_id * 2 + 1) * cols + c, n, db + i);
         });
         __syncthreads();
-        for (int c = slot * team + t; c < 2 * cols; c += team * teams) {
+        for (int c = tid; c < 2 * cols; c += threads) {
             const int which = c >= cols, cc = c - which * cols;
-            float s = 0.f;
-            for (int j = 0; j < teams; ++j) s += dyn[(2 * j + which) * cols + cc];
+            float sum = 0.f;
+            for (int j = 0; j < teams; ++j) sum += dyn[(2 * j + which) * cols + cc];
             float* out = p.slices > 1 ? p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * cols
                                       : (which ? p.dbias : p.dweight);
-            if (p.slices == 1 && out) out += group * cols;
-            if (out) out[cc] = s;
+            if (p.slices == 1 && out) out += static_cast<int64_t>(group) * cols;
+            if (out) out[cc] = sum;
         }
     } else {
-        for_columns<NV, ALIGNED>(team, t, cols, [&](int i, int c) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                if (p.slices > 1) {
-                    p.partial[(static_cast<int64_t>(blockIdx.x) * 2) * cols + c + k] = dw[i + k];
-                    p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + 1) * cols + c + k] = db[i + k];
-                } else {
-                    if (p.dweight) p.dweight[group * cols + c + k] = dw[i + k];
-                    if (p.dbias) p.dbias[group * cols + c + k] = db[i + k];
-                }
+        for_vectors<N, C, MODE>(team, t, cols, [&](int i, int c, int n) {
+            if (p.slices > 1) {
+                store_columns<C, true, false>(p.partial, (static_cast<int64_t>(blockIdx.x) * 2) * cols + c, n, dw + i);
+                store_columns<C, true, false>(p.partial, (static_cast<int64_t>(blockIdx.x) * 2 + 1) * cols + c, n, db + i);
+            } else {
+                if (p.dweight) store_columns<C, true, false>(p.dweight, static_cast<int64_t>(group) * cols + c, n, dw + i);
+                if (p.dbias) store_columns<C, true, false>(p.dbias, static_cast<int64_t>(group) * cols + c, n, db + i);
             }
         });
     }
 }
 
-// Sums the slices of 32 columns: thread (column, lane) adds slices lane, lane + 16, ..., then the
-// 16 lanes' sums are added in order.  grid: (columns / 32, groups, 2).
-constexpr int kFoldLanes = 16;
+// Sums the slices of 32 columns: thread (column, lane) adds slices lane, lane + 32, ..., then the 32 lanes'
+// sums are added in a fixed tree.  grid: (columns / 32, groups, 2).
+constexpr int kFoldLanes = 32;
 
 __global__ void __launch_bounds__(32 * kFoldLanes) norm_fold_kernel(const float* partial, int slices, int cols,
                                                                     float* dweight, float* dbias)
 {
     float* out = blockIdx.z ? dbias : dweight;
     if (!out) return;
-    __shared__ float part[kFoldLanes][32];
+    __shared__ float part[kFoldLanes][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     const int64_t group = blockIdx.y;
+    const float* src = partial + ((group * slices + threadIdx.y) * 2 + blockIdx.z) * cols + c;
+    const int64_t step = static_cast<int64_t>(kFoldLanes) * 2 * cols;
     float s = 0.f;
-    if (c < cols)
-        for (int i = threadIdx.y; i < slices; i += kFoldLanes)
-            s += partial[((group * slices + i) * 2 + blockIdx.z) * cols + c];
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = threadIdx.y; i < slices; i += kFoldLanes, src += step) s += *src;
+    }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && c < cols) {
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFoldLanes; ++i) s += part[i][threadIdx.x];
-        out[group * cols + c] = s;
-    }
+    // warp y adds column y: its lanes hold the 32 sums, added in a fixed tree
+    s = warp_sum(part[threadIdx.x][threadIdx.y]);
+    const int cc = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && cc < cols) out[group * cols + cc] = s;
 }
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-// Vectors of 8 columns per thread and threads per row.
+// Vectors of 8 columns per thread, threads per row, how its elements are reached.
 struct Team {
     int nv, threads;
+    Rows mode;
 };
 
-Team forward_team(int cols)
+Team forward_team(int cols, bool aligned)
 {
     const int vecs = (cols + 7) / 8;
-    if (vecs <= 32) return {1, 32};
-    if (vecs <= 64) return {2, 32};
-    if (vecs <= 128) return {4, 32};
-    if (vecs <= 192) return {6, 32};
-    if (vecs <= 256) return {8, 32};
-    if (vecs <= 512) return {1, round32(vecs)};
-    if (vecs <= 1024) return {2, round32((vecs + 1) / 2)};
-    return {4, round32((vecs + 3) / 4)};
+    if (!aligned) {                                    // the next row takes registers as well
+        if (vecs <= 32) return {1, 32, kSingle};
+        if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kSingle};
+        return {4, round32((vecs + 3) / 4), kSingle};
+    }
+    for (int nv = 4; nv >= 1; --nv)
+        if (vecs % (32 * nv) == 0 && vecs / nv <= kMaxThreads) return {nv, vecs / nv, kFull};
+    if (vecs <= 32) return {1, 32, kVector};
+    if (vecs <= 64) return {2, 32, kVector};
+    return {4, round32((vecs + 3) / 4), kVector};
 }
 
-Team backward_team(int cols)
+Team backward_team(int cols, bool aligned)
 {
     const int vecs = (cols + 7) / 8;
-    if (vecs <= 512) return {1, round32(vecs)};
-    if (vecs <= 1024) return {2, round32((vecs + 1) / 2)};
-    return {4, round32((vecs + 3) / 4)};
-}
-
-int backward_teams(int cols) { return std::max(1, std::min(8, kMaxThreads / backward_team(cols).threads)); }
-
-template <int NV, bool ALIGNED>
-void forward_types(const NormParams& p, dim3 grid, dim3 block, cudaStream_t s)
-{
-    if (p.x_f32) {
-        if (p.y_f32) norm_forward_kernel<NV, ALIGNED, true, true><<<grid, block, 0, s>>>(p);
-        else norm_forward_kernel<NV, ALIGNED, true, false><<<grid, block, 0, s>>>(p);
-    } else {
-        if (p.y_f32) norm_forward_kernel<NV, ALIGNED, false, true><<<grid, block, 0, s>>>(p);
-        else norm_forward_kernel<NV, ALIGNED, false, false><<<grid, block, 0, s>>>(p);
+    if (!aligned) {
+        if (vecs <= 512) return {1, round32(vecs), kSingle};
+        if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kSingle};
+        return {4, round32((vecs + 3) / 4), kSingle};
     }
+    for (int nv = 2; nv >= 1; --nv)
+        if (vecs % (32 * nv) == 0 && vecs / nv <= kMaxThreads) return {nv, vecs / nv, kFull};
+    if (vecs <= 32) return {1, 32, kVector};
+    if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kVector};
+    return {4, round32((vecs + 3) / 4), kVector};
 }
 
-template <int NV, bool ALIGNED>
-void backward_types(const NormParams& p, dim3 grid, dim3 block, size_t smem, cudaStream_t s)
+int backward_teams(int cols, bool aligned) { return std::max(1, std::min(15, kMaxThreads / backward_team(cols, aligned).threads)); }
+
+// Blocks of the backward kernel that an SM holds, by its registers.
+int backward_blocks(int cols, bool aligned) { return aligned && backward_team(cols, aligned).nv == 1 ? 2 : 1; }
+
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes)
 {
-    if (p.x_f32) {
-        if (p.y_f32) norm_backward_kernel<NV, ALIGNED, true, true><<<grid, block, smem, s>>>(p);
-        else norm_backward_kernel<NV, ALIGNED, true, false><<<grid, block, smem, s>>>(p);
-    } else {
-        if (p.y_f32) norm_backward_kernel<NV, ALIGNED, false, true><<<grid, block, smem, s>>>(p);
-        else norm_backward_kernel<NV, ALIGNED, false, false><<<grid, block, smem, s>>>(p);
-    }
+    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes))
+                             : cudaSuccess;
 }
+
+template <int NV, Rows MODE, bool XF32, bool YF32>
+cudaError_t forward(const NormParams& p, int threads, cudaStream_t s)
+{
+    constexpr int S = stages(NV * 16 * (XF32 ? 2 : 1));
+    constexpr int kBytes = MODE != kSingle ? S * NV * 16 * (XF32 ? 2 : 1) : 0;          // of shared memory per thread
+    // teams of a block: none idle while there are SMs without one
+    const int64_t spread = (p.rows + kSms - 1) / kSms;
+    const int teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(15, kMaxThreads / threads), spread)));
+    const int block = teams * threads;
+    // resident blocks: by shared memory, and by the registers of this width (an estimate: more blocks than fit wait)
+    constexpr int kRegs = MODE == kSingle ? 128 : NV == 1 ? 64 : NV == 2 ? 96 : 128;
+    const int fit = std::max(1, std::min(kBytes ? 220 * 1024 / (kBytes * block + 1024) : 8, 65536 / (kRegs * block)));
+    const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams, static_cast<int64_t>(kSms) * fit);
+    const size_t smem = static_cast<size_t>(kBytes) * block;
+    auto kernel = norm_forward_kernel<NV, MODE, XF32, YF32>;
+    const cudaError_t e = allow_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)), smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int NV, Rows MODE, bool XF32, bool YF32>
+cudaError_t backward(const NormParams& p, int threads, cudaStream_t s)
+{
+    constexpr int S = stages(NV * 16 * ((XF32 ? 2 : 1) + (YF32 ? 2 : 1)));
+    constexpr int kBytes = MODE != kSingle ? S * NV * 16 * ((XF32 ? 2 : 1) + (YF32 ? 2 : 1)) : 0;
+    const int teams = backward_teams(p.cols, MODE != kSingle);
+    const int64_t groups = (p.rows + p.rows_per_group - 1) / p.rows_per_group;
+    const size_t sums = teams > 1 ? static_cast<size_t>(teams) * 2 * p.cols * sizeof(float) : 0;
+    const size_t smem = std::max(sums, static_cast<size_t>(kBytes) * threads * teams);
+    auto kernel = norm_backward_kernel<NV, MODE, XF32, YF32>;
+    const cudaError_t e = allow_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(static_cast<unsigned>(groups * p.slices)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)),
+             smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+// Calls f<NV, MODE, XF32, YF32>(p, threads, s) for the row's width, alignment and types.
+#define SDV2_NORM_TYPES(f, NV, MODE)                                                                        \
+    (p.x_f32 ? (p.y_f32 ? f<NV, MODE, true, true>(p, tm.threads, s) : f<NV, MODE, true, false>(p, tm.threads, s)) \
+             : (p.y_f32 ? f<NV, MODE, false, true>(p, tm.threads, s) : f<NV, MODE, false, false>(p, tm.threads, s)))
+#define SDV2_NORM(f, NV)                                   \
+    (tm.mode == kFull ? SDV2_NORM_TYPES(f, NV, kFull)      \
+                      : tm.mode == kVector ? SDV2_NORM_TYPES(f, NV, kVector) : SDV2_NORM_TYPES(f, NV, kSingle))
 
 }  // namespace
 
-int norm_backward_slices(int64_t rows, int64_t rows_per_group, int cols)
+int norm_backward_slices(int64_t rows, int64_t rows_per_group, int cols, bool aligned)
 {
-    // about two blocks for each of the 152 SMs, and no block without rows
+    // the blocks that the 152 SMs hold at once, and no block without rows
     const int64_t groups = (rows + rows_per_group - 1) / rows_per_group;
-    const int64_t want = (304 + groups - 1) / groups;
-    const int64_t teams = backward_teams(cols);
+    const int64_t want = std::max<int64_t>(1, kSms * backward_blocks(cols, aligned) / groups);
+    const int64_t teams = backward_teams(cols, aligned);
     return static_cast<int>(std::max<int64_t>(1, std::min(want, (std::min(rows, rows_per_group) + teams - 1) / teams)));
 }
 
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s)
 {
-    const Team tm = forward_team(p.cols);
-    const int teams = tm.threads == 32 ? 4 : 1;
-    const dim3 block(static_cast<unsigned>(tm.threads), static_cast<unsigned>(teams));
-    const dim3 grid(static_cast<unsigned>((p.rows + teams - 1) / teams));
+    const Team tm = forward_team(p.cols, p.aligned);
     switch (tm.nv) {
-    case 1: p.aligned ? forward_types<1, true>(p, grid, block, s) : forward_types<1, false>(p, grid, block, s); break;
-    case 2: p.aligned ? forward_types<2, true>(p, grid, block, s) : forward_types<2, false>(p, grid, block, s); break;
-    case 4: p.aligned ? forward_types<4, true>(p, grid, block, s) : forward_types<4, false>(p, grid, block, s); break;
-    case 6: p.aligned ? forward_types<6, true>(p, grid, block, s) : forward_types<6, false>(p, grid, block, s); break;
-    default: p.aligned ? forward_types<8, true>(p, grid, block, s) : forward_types<8, false>(p, grid, block, s); break;
+    case 1: return SDV2_NORM(forward, 1);
+    case 2: return SDV2_NORM(forward, 2);
+    case 3: return SDV2_NORM_TYPES(forward, 3, kFull);
+    default: return SDV2_NORM(forward, 4);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_layer_norm_backward(const NormParams& p, cudaStream_t s)
 {
-    const Team tm = backward_team(p.cols);
-    const int teams = backward_teams(p.cols);
-    const int64_t groups = (p.rows + p.rows_per_group - 1) / p.rows_per_group;
-    const dim3 block(static_cast<unsigned>(tm.threads), static_cast<unsigned>(teams));
-    const dim3 grid(static_cast<unsigned>(groups * p.slices));
-    // at most 2 teams * 2 * 2048 columns * 4 bytes: a team of up to 256 threads holds 8 columns each
-    const size_t smem = teams > 1 ? static_cast<size_t>(teams) * 2 * p.cols * sizeof(float) : 0;
+    const Team tm = backward_team(p.cols, p.aligned);
+    cudaError_t e;
     switch (tm.nv) {
-    case 1: p.aligned ? backward_types<1, true>(p, grid, block, smem, s) : backward_types<1, false>(p, grid, block, smem, s); break;
-    case 2: p.aligned ? backward_types<2, true>(p, grid, block, smem, s) : backward_types<2, false>(p, grid, block, smem, s); break;
-    default: p.aligned ? backward_types<4, true>(p, grid, block, smem, s) : backward_types<4, false>(p, grid, block, smem, s); break;
+    case 1: e = SDV2_NORM(backward, 1); break;
+    case 2: e = SDV2_NORM(backward, 2); break;
+    default: e = tm.mode == kVector ? SDV2_NORM_TYPES(backward, 4, kVector) : SDV2_NORM_TYPES(backward, 4, kSingle); break;
     }
+    if (e != cudaSuccess) return e;
     if (p.slices > 1 && (p.dweight || p.dbias)) {
+        const int64_t groups = (p.rows + p.rows_per_group - 1) / p.rows_per_group;
         const dim3 fold(static_cast<unsigned>((p.cols + 31) / 32), static_cast<unsigned>(groups), 2);
         norm_fold_kernel<<<fold, dim3(32, kFoldLanes), 0, s>>>(p.partial, p.slices, p.cols, p.dweight, p.dbias);
     }
     return cudaGetLastError();
 }
+
+#undef SDV2_NORM
+#undef SDV2_NORM_TYPES
 
 }  // namespace sdv2
