@@ -44,7 +44,7 @@ struct CrossBackward {
     uint16_t* dq;
     uint16_t* dk;              // [B][Nk][Hk][D]
     uint16_t* dv;
-    float* stats;              // scratch: delta [B][H][Nq], or cross_backward_stats_bytes
+    float* stats;              // scratch: cross_backward_stats_bytes
     float* part;               // scratch: cross_backward_part_bytes
 };
 
@@ -60,9 +60,9 @@ cudaError_t launch_cross_backward(const CrossBackward& p, cudaStream_t s);
 size_t cross_backward_stats_bytes(int B, int H, int Hk, int64_t Nq);
 size_t cross_backward_part_bytes(int B, int H, int Hk, int64_t Nq, int64_t Nk);
 
-// Query rows on the CUDA cores (any size; fast for a few queries).
+// One or two rows per key head on the CUDA cores.
+constexpr int kFewRows = 2, kFewKeys = 1024;       // where it is the faster of the two
 cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s);
-cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s);
 
 struct NormParams {
     const void* x;

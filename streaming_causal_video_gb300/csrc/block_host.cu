@@ -212,7 +212,7 @@ sdv2_status sdv2_cross_attention(const sdv2_cross_cfg* c, const int64_t* kv_lens
         const int64_t rows = static_cast<int64_t>(b0) * c->heads * c->q_len;
         p.out = static_cast<uint16_t*>(out) + rows * 128;
         p.lse = lse ? lse + rows : nullptr;
-        const bool few = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq <= 4;
+        const bool few = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq <= kFewRows && *std::max_element(p.c.n, p.c.n + p.c.B) <= kFewKeys;
         const cudaError_t e = few ? launch_cross_rows(p, static_cast<cudaStream_t>(stream))
                                   : launch_cross_attention(p, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return done(e, "cross attention launch");
@@ -248,9 +248,7 @@ sdv2_status sdv2_cross_attention_backward(const sdv2_cross_cfg* c, const int64_t
         p.dv = static_cast<uint16_t*>(dv) + (dv ? kv_rows * 128 : 0);
         p.stats = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes);
         p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes + stats_bytes(c));
-        const bool few = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq <= 4;
-        const cudaError_t e = few ? launch_cross_rows_backward(p, static_cast<cudaStream_t>(stream))
-                                  : launch_cross_backward(p, static_cast<cudaStream_t>(stream));
+        const cudaError_t e = launch_cross_backward(p, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return done(e, "cross attention backward launch");
     }
     return done(cudaSuccess, "");

@@ -28,7 +28,7 @@
 // Every wait is bounded; on expiry the kernel records the timeout in the workspace's error word,
 // lets all roles finish what they have in flight and returns.
 #include <algorithm>
-#include <atomic>
+#include <mutex>
 
 #include "cross_tma.cuh"
 #include "internal.h"
@@ -46,7 +46,7 @@ constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10, Q_WARP = 11;
 constexpr int NTHREADS = 12 * 32;
 constexpr uint32_t TMEM_COLS = 512;           // S_0 | S_1 | O_0 | O_1
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxCtas = 160;
 
 enum Bar { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = KFULL + KST, VFULL = KEMPTY + KST, VEMPTY = VFULL + VST,
@@ -74,7 +74,7 @@ struct Params {
     int32_t packs;                            // packs of heads of a stream
     int32_t group;                            // query heads of a key head
     int32_t tiles;                            // query tiles of one (stream, pack of heads)
-    int32_t split_shift;                      // log2 of the CTAs of a cluster that share a tile's keys
+    int32_t splits;                           // CTAs of a cluster that share a tile's keys
     int32_t start[kMaxCtas + 1];              // first query tile of every CTA (not of clusters)
     float scale_log2;
 };
@@ -99,9 +99,14 @@ struct Walk {
     template <int CAP>
     __device__ explicit Walk(const Params<CAP>& p)
     {
-        const uint32_t cta = p.split_shift ? blockIdx.x >> p.split_shift : blockIdx.x;
-        const uint32_t cur = p.split_shift ? cta : static_cast<uint32_t>(p.start[cta]);
-        left = p.split_shift ? 1 : p.start[cta + 1] - static_cast<int>(cur);
+        uint32_t cur;
+        if (p.splits > 1) {
+            cur = blockIdx.x / static_cast<uint32_t>(p.splits);
+            left = 1;
+        } else {
+            cur = static_cast<uint32_t>(p.start[blockIdx.x]);
+            left = p.start[blockIdx.x + 1] - static_cast<int>(cur);
+        }
         const uint32_t group = cur / static_cast<uint32_t>(p.tiles);
         tile = static_cast<int>(cur - group * p.tiles);
         const uint32_t bb = group / static_cast<uint32_t>(p.packs);
@@ -117,10 +122,10 @@ struct Walk {
         it.keys = key_tiles(p, b);
         it.k0 = 0;
         it.pair = left > 1 && tile + 1 < p.tiles;
-        if (p.split_shift) {
-            const int r = blockIdx.x & ((1 << p.split_shift) - 1), all = it.keys;
-            it.k0 = (all * r) >> p.split_shift;
-            it.keys = ((all * (r + 1)) >> p.split_shift) - it.k0;
+        if (p.splits > 1) {
+            const uint32_t r = cluster_ctarank(), all = it.keys, n = p.splits;
+            it.k0 = static_cast<int>(all * r / n);
+            it.keys = static_cast<int>(all * (r + 1) / n) - it.k0;
         }
     }
     template <int CAP>
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
-    const int splits = 1 << p.split_shift;
+    const int splits = p.splits;
 
     // The load warps only need the barriers: they start while the rest of the block is still setting up.
     const int used_rows = p.pack * p.tokens;
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
             const bool live = row < used_rows && tok < p.Nq;
             const int64_t stat = (static_cast<int64_t>(it.b) * p.H + it.h0 + row - row_tok * p.pack) * p.Nq + tok;
             if (whole) {
-                if (splits > 1 && (blockIdx.x & (splits - 1)) != 0) {   // a tile without keys: the cluster's first CTA writes it
+                if (splits > 1 && cluster_ctarank() != 0) {   // a tile without keys: the cluster's first CTA writes it
                     for (int i = 0; i < 4; ++i) lane_barrier(t);
                     continue;
                 }
@@ -556,10 +561,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
                     ml[c].x = w;
                 }
             const float inv = 1.0f / L;
-            const int rank = blockIdx.x & (splits - 1);
+            const int rank = static_cast<int>(cluster_ctarank());
             const int h = it.h0 + (p.pack == 1 ? 0 : row % p.pack);
             uint16_t* dst = p.out + ((static_cast<int64_t>(it.b) * p.Nq + tok) * p.H + h) * HD;
-#pragma unroll 1
+#pragma unroll 2
             for (int d4 = rank * (NTHREADS / 128) + (threadIdx.x >> 7); d4 < HD / 4; d4 += splits * (NTHREADS / 128)) {
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -616,6 +621,38 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many clusters of each size a device holds at once (a cluster lies within one of the GPU's processing
+// clusters, whose sizes differ: 152 SMs take 36 clusters of 4, but 23 of 6 and 7 of 16).  Asked once per device.
+struct Placement {
+    std::once_flag once;
+    cudaError_t error = cudaSuccess;
+    int clusters[kMaxCluster + 1] = {};
+    template <typename K>
+    cudaError_t prepare(K kernel)
+    {
+        std::call_once(once, [&]() {
+            error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+            if (error != cudaSuccess) return;
+            const bool wide = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            for (int n = 2; n <= (wide ? kMaxCluster : 8); ++n) {
+                cudaLaunchConfig_t cfg{};
+                cfg.gridDim = dim3(static_cast<unsigned>(n));
+                cfg.blockDim = dim3(NTHREADS);
+                cfg.dynamicSmemBytes = SMEM_BYTES;
+                cudaLaunchAttribute attr{};
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = static_cast<unsigned>(n);
+                attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&clusters[n], kernel, &cfg) != cudaSuccess) clusters[n] = 0;
+            }
+            cudaGetLastError();                // a size that the device does not take is no error
+        });
+        return error;
+    }
+};
+
 template <int CAP>
 cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
 {
@@ -651,12 +688,18 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
     p.scale_log2 = c.scale * kLog2e;
     const int64_t tiles = static_cast<int64_t>(p.tiles) * (c.H / p.pack) * c.B;
     if (tiles > INT32_MAX / kMaxCluster) return cudaErrorInvalidConfiguration;
-    // clusters share a tile's keys while that leaves SMs idle and gives every lane a key tile
+    auto kernel = cross_attention_kernel<CAP>;
+    static Placement placements[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const Placement& fit = placements[dev & 63];
+    const cudaError_t prepared = placements[dev & 63].prepare(kernel);
+    if (prepared != cudaSuccess) return prepared;
+    // A cluster shares a tile's keys, as wide as all tiles' clusters fit at once and every CTA has a key tile.
     int splits = 1;
-    while (splits < kMaxCluster && tiles * splits * 2 <= sms && least >= splits * 4 && least != 1 << 30) {
-        splits *= 2;
-        ++p.split_shift;
-    }
+    for (int c = 2; least != 1 << 30 && c <= std::min(least, kMaxCluster); ++c)
+        if (tiles <= fit.clusters[c]) splits = c;
+    p.splits = splits;
     const int ctas = static_cast<int>(std::min<int64_t>(tiles, std::min(sms, kMaxCtas)));
     if (splits == 1) {
         // ranges of equal cost; a query tile costs its key tiles, and one for its start and end
@@ -677,15 +720,6 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
         }
     }
 
-    auto kernel = cross_attention_kernel<CAP>;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    static std::atomic<uint64_t> attr_set{0};  // one bit per device
-    if (!(attr_set.load() >> (dev & 63) & 1u)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-        if (e != cudaSuccess) return e;
-        attr_set.fetch_or(uint64_t(1) << (dev & 63));
-    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? tiles * splits : ctas));
     cfg.blockDim = dim3(NTHREADS);

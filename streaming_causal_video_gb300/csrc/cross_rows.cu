@@ -1,16 +1,15 @@
-// Cross attention on the CUDA cores, forward and backward: one half-warp per key or row, any size.
+// Cross attention of one or two query rows on the CUDA cores: a half-warp per key.
 //
-// Forward (a few queries, where the keys and values have to be read and there is next to nothing to
-// multiply them with): out = sum_j softmax_j(scale q.k_j) v_j in one pass over the keys.  The heads
-// that share a key head and their queries form rows r = i*g + (h mod g); a cluster of CTAs holds
-// up to kRows rows and splits the key range.  In a CTA each half-warp walks its own keys, a lane
-// holding 8 of the 128 dims (one 16-byte load of k and of v), with its own running maximum and sum
-// per row; half-warps are joined through shared memory, CTAs through the cluster's shared memory, in
-// a fixed order.
+// The keys and values have to be read and there is next to nothing to multiply them with, so what counts
+// is the time until the first product, and a tile of 128 rows is mostly empty (12 heads, 512 states: one
+// row 5.2 us, two 6.1 us, against 8.9 us on the tensor cores; at 20000 states the tensor cores' deeper
+// loads win by far, 46 against 139 us).
 //
-// Backward: delta = rowsum(dO * O); dQ with a half-warp per query row over the keys; dK and dV with
-// a half-warp per key over the queries of every head that shares it.  No atomics: each output row
-// has one owner.
+// out = sum_j softmax_j(scale q.k_j) v_j in one pass over the keys.  The heads that share a key head and their
+// queries form rows r = i*g + (h mod g); a cluster of CTAs holds the rows of one key head and splits its key
+// range.  In a CTA each half-warp walks its own keys, a lane holding 8 of the 128 dims (one 16-byte load of k and
+// of v), with its own running maximum and sum per row; half-warps are joined through shared memory, CTAs through
+// the cluster's shared memory, in a fixed order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -23,7 +22,7 @@ namespace sdv2 {
 namespace {
 
 constexpr int HD = 128;
-constexpr int kRows = 4;               // query rows per cluster
+constexpr int kMaxSplits = 8;
 constexpr int kWarps = 8;
 constexpr int kHalves = 2 * kWarps;    // half-warps per CTA
 constexpr int kKeysAtOnce = 4;         // keys a half-warp loads before it computes
@@ -44,17 +43,6 @@ __device__ __forceinline__ Vec8 unpack8(uint4 w)
         r.x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
     return r;
-}
-
-__device__ __forceinline__ uint4 pack8(const float* v)
-{
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 __device__ __forceinline__ uint4 load_vec(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -86,6 +74,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 }
 
 // grid.x = units * splits, clusters of `splits` CTAs; unit = ((b * Hk) + key head) * row blocks + block.
+template <int kRows>
 __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_constant__ CrossForward p, int splits,
                                                                  int row_blocks)
 {
@@ -94,15 +83,15 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     __shared__ float c_m[kRows], c_l[kRows], c_acc[kRows][HD];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = warp * 2 + (lane >> 4), sub = lane & 15;
-    const int64_t unit = blockIdx.x / splits;
+    // 32-bit divisions: a 64-bit one costs as much as a key
+    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(splits);
     const int split = static_cast<int>(blockIdx.x - unit * splits);
-    const int rb = static_cast<int>(unit % row_blocks);
-    const int64_t bh = unit / row_blocks;
-    const int hk = static_cast<int>(bh % p.c.Hk);
-    const int b = static_cast<int>(bh / p.c.Hk);
+    const uint32_t bh = unit / static_cast<uint32_t>(row_blocks);
+    const int b = static_cast<int>(bh / static_cast<uint32_t>(p.c.Hk));
+    const int hk = static_cast<int>(bh - b * p.c.Hk);
     const int g = p.c.H / p.c.Hk;
-    const int64_t rows = static_cast<int64_t>(g) * p.c.Nq;
-    const int64_t row0 = static_cast<int64_t>(rb) * kRows;
+    const uint32_t rows = static_cast<uint32_t>(g) * p.c.Nq;               // the host keeps it below 2^31
+    const uint32_t row0 = (unit - bh * row_blocks) * kRows;
     const int n = p.c.n[b];
     const int j0 = static_cast<int>(static_cast<int64_t>(n) * split / splits);
     const int j1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits);
@@ -111,8 +100,8 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     Vec8 q[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const int64_t row = row0 + r < rows ? row0 + r : rows - 1;       // rows past the end repeat the last
-        const int64_t i = row / g;
+        const uint32_t row = row0 + r < rows ? row0 + r : rows - 1;      // rows past the end repeat the last
+        const int64_t i = row / static_cast<uint32_t>(g);
         const int h = hk * g + static_cast<int>(row - i * g);
         q[r] = unpack8(load_vec(p.c.q + b * p.c.qs.batch + i * p.c.qs.tok + h * p.c.qs.hd + sub * 8));
     }
@@ -218,21 +207,32 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
             c_l[r] = sum;
         }
     cluster_sync_all();
-    // the CTAs of the cluster share the rows' dims
+    // the CTAs of the cluster share the rows' dims; a thread's loads from all of them are under way together
     for (int i = split * kWarps * 32 + threadIdx.x; i < kRows * HD; i += splits * kWarps * 32) {
         const int r = i / HD, d = i - r * HD;
-        if (row0 + r >= rows) continue;
+        const uint32_t row = row0 + r;
+        if (row >= rows) continue;
+        float mc[kMaxSplits], lc[kMaxSplits], ac[kMaxSplits];
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c)
+            if (c < splits) {
+                mc[c] = ld_cluster_f32(map_to_rank(smem_u32(&c_m[r]), c));
+                lc[c] = ld_cluster_f32(map_to_rank(smem_u32(&c_l[r]), c));
+                ac[c] = ld_cluster_f32(map_to_rank(smem_u32(&c_acc[r][d]), c));
+            }
         float mx = -INFINITY;
-        for (int c = 0; c < splits; ++c) mx = fmaxf(mx, ld_cluster_f32(map_to_rank(smem_u32(&c_m[r]), c)));
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c)
+            if (c < splits) mx = fmaxf(mx, mc[c]);
         float sum = 0.f, a = 0.f;
-        for (int c = 0; c < splits; ++c) {
-            const float lc = ld_cluster_f32(map_to_rank(smem_u32(&c_l[r]), c));
-            if (lc == 0.f) continue;
-            const float f = ex2_from(ld_cluster_f32(map_to_rank(smem_u32(&c_m[r]), c)), mx);
-            sum += lc * f;
-            a += ld_cluster_f32(map_to_rank(smem_u32(&c_acc[r][d]), c)) * f;
-        }
-        const int64_t row = row0 + r, qi = row / g;
+#pragma unroll
+        for (int c = 0; c < kMaxSplits; ++c)
+            if (c < splits && lc[c] != 0.f) {
+                const float f = ex2_from(mc[c], mx);
+                sum += lc[c] * f;
+                a += ac[c] * f;
+            }
+        const int64_t qi = row / static_cast<uint32_t>(g);
         const int h = hk * g + static_cast<int>(row - qi * g);
         const float o = n == 0 ? 0.f : a / sum;
         reinterpret_cast<__nv_bfloat16*>(p.out)[((static_cast<int64_t>(b) * p.c.Nq + qi) * p.c.H + h) * HD + d] =
@@ -243,107 +243,10 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     cluster_sync_all();                                  // no CTA leaves while others read its memory
 }
 
-// ---- backward ---------------------------------------------------------------------------------
-
-// delta[b][h][i] = sum_d dout * out; a half-warp per row.
-__global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant__ CrossBackward p)
-{
-    const int sub = threadIdx.x & 15;
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;   // (b, i, h)
-    const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Nq * p.c.H;
-    const int64_t safe = row < rows ? row : rows - 1;
-    const Vec8 a = unpack8(load_vec(p.out + safe * HD + sub * 8));
-    const Vec8 d = unpack8(load_vec(p.dout + safe * HD + sub * 8));
-    const float s = half_sum(dot8(a, d));
-    if (row < rows && sub == 0) {
-        const int64_t bi = row / p.c.H;
-        const int h = static_cast<int>(row - bi * p.c.H);
-        const int64_t b = bi / p.c.Nq;
-        p.stats[(b * p.c.H + h) * p.c.Nq + (bi - b * p.c.Nq)] = s;
-    }
-}
-
-// dQ: half-warp per (b, h, i); a block's 16 rows are consecutive queries of one head.
-__global__ void __launch_bounds__(256) cross_rows_dq_kernel(const __grid_constant__ CrossBackward p, int blocks_per_head)
-{
-    const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
-    const int64_t bh = blockIdx.x / blocks_per_head;
-    const int64_t i = static_cast<int64_t>(blockIdx.x - bh * blocks_per_head) * 16 + half;
-    const int h = static_cast<int>(bh % p.c.H), b = static_cast<int>(bh / p.c.H);
-    const int hk = h / (p.c.H / p.c.Hk);
-    const int64_t safe = i < p.c.Nq ? i : p.c.Nq - 1;
-    const int n = p.c.n[b];
-    const float sl2 = p.c.scale * kLog2e;
-    const int64_t o = ((static_cast<int64_t>(b) * p.c.Nq + safe) * p.c.H + h) * HD + sub * 8;
-    const Vec8 q = unpack8(load_vec(p.c.q + b * p.c.qs.batch + safe * p.c.qs.tok + h * p.c.qs.hd + sub * 8));
-    const Vec8 dout = unpack8(load_vec(p.dout + o));
-    const float lse2 = p.lse[bh * p.c.Nq + safe] * kLog2e, delta = p.stats[bh * p.c.Nq + safe];
-    const uint16_t* kb = p.c.k + b * p.c.kvs.batch + hk * p.c.kvs.hd + sub * 8;
-    const uint16_t* vb = p.c.v + b * p.c.kvs.batch + hk * p.c.kvs.hd + sub * 8;
-    float acc[8] = {};
-    for (int j = 0; n > 1 && j < n; ++j) {
-        const Vec8 k = unpack8(load_vec(kb + j * p.c.kvs.tok));
-        const Vec8 v = unpack8(load_vec(vb + j * p.c.kvs.tok));
-        const float s = half_sum(dot8(q, k)), dp = half_sum(dot8(dout, v));
-        const float ds = exp2f(fmaf(s, sl2, -lse2)) * (dp - delta);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d] = fmaf(ds, k.x[d], acc[d]);
-    }
-    if (i < p.c.Nq) {
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d] *= p.c.scale;
-        *reinterpret_cast<uint4*>(p.dq + o) = pack8(acc);
-    }
-}
-
-// dK, dV: half-warp per (b, key head, j).
-__global__ void __launch_bounds__(256) cross_rows_dkv_kernel(const __grid_constant__ CrossBackward p, int blocks_per_head)
-{
-    const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
-    const int64_t bh = blockIdx.x / blocks_per_head;
-    const int64_t j = static_cast<int64_t>(blockIdx.x - bh * blocks_per_head) * 16 + half;
-    const int hk = static_cast<int>(bh % p.c.Hk), b = static_cast<int>(bh / p.c.Hk);
-    const int g = p.c.H / p.c.Hk, n = p.c.n[b];
-    const float sl2 = p.c.scale * kLog2e;
-    const int64_t first = j - half;                       // the block's first key
-    float dk[8] = {}, dv[8] = {};
-    if (first < n) {
-        const int64_t safe = j < n ? j : n - 1;
-        const Vec8 k = unpack8(load_vec(p.c.k + b * p.c.kvs.batch + safe * p.c.kvs.tok + hk * p.c.kvs.hd + sub * 8));
-        const Vec8 v = unpack8(load_vec(p.c.v + b * p.c.kvs.batch + safe * p.c.kvs.tok + hk * p.c.kvs.hd + sub * 8));
-        for (int h = hk * g; h < (hk + 1) * g; ++h) {
-            const int64_t stat = (static_cast<int64_t>(b) * p.c.H + h) * p.c.Nq;
-            for (int64_t i = 0; i < p.c.Nq; ++i) {
-                const Vec8 q = unpack8(load_vec(p.c.q + b * p.c.qs.batch + i * p.c.qs.tok + h * p.c.qs.hd + sub * 8));
-                const Vec8 dout =
-                    unpack8(load_vec(p.dout + ((static_cast<int64_t>(b) * p.c.Nq + i) * p.c.H + h) * HD + sub * 8));
-                const float s = half_sum(dot8(q, k)), dp = half_sum(dot8(dout, v));
-                const float pr = exp2f(fmaf(s, sl2, -p.lse[stat + i] * kLog2e));
-                const float ds = n > 1 ? pr * (dp - p.stats[stat + i]) : 0.f;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    dk[d] = fmaf(ds, q.x[d], dk[d]);
-                    dv[d] = fmaf(pr, dout.x[d], dv[d]);
-                }
-            }
-        }
-    }
-    if (j < p.c.Nk) {
-        const int64_t o = ((static_cast<int64_t>(b) * p.c.Nk + j) * p.c.Hk + hk) * HD + sub * 8;
-        const bool live = j < n;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-            dk[d] = live ? dk[d] * p.c.scale : 0.f;
-            dv[d] = live ? dv[d] : 0.f;
-        }
-        *reinterpret_cast<uint4*>(p.dk + o) = pack8(dk);
-        *reinterpret_cast<uint4*>(p.dv + o) = pack8(dv);
-    }
-}
-
 }  // namespace
 
-cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
+template <int kRows>
+static cudaError_t launch_rows(const CrossForward& p, cudaStream_t s)
 {
     const int64_t rows = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq;
     const int64_t row_blocks = (rows + kRows - 1) / kRows;
@@ -352,8 +255,8 @@ cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
     for (int b = 0; b < p.c.B; ++b) longest = std::max(longest, p.c.n[b]);
     // a key split holds at least one round of loads of its half-warps; split until the SMs are full
     int splits = 1;
-    while (splits < 8 && units * splits < 304 && longest > splits * kHalves * kKeysAtOnce) splits *= 2;
-    if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
+    while (splits < kMaxSplits && units * splits < 304 && longest > splits * kHalves * kKeysAtOnce) splits *= 2;
+    if (rows > INT32_MAX || units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
     cfg.blockDim = dim3(kWarps * 32);
@@ -364,20 +267,13 @@ cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cross_rows_kernel, p, splits, static_cast<int>(row_blocks));
+    return cudaLaunchKernelEx(&cfg, cross_rows_kernel<kRows>, p, splits, static_cast<int>(row_blocks));
 }
 
-cudaError_t launch_cross_rows_backward(const CrossBackward& p, cudaStream_t s)
+cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
 {
-    const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Nq * p.c.H;
-    const int64_t qb = (static_cast<int64_t>(p.c.Nq) + 15) / 16, kb = (static_cast<int64_t>(p.c.Nk) + 15) / 16;
-    const int64_t dq_blocks = qb * p.c.B * p.c.H, dkv_blocks = kb * p.c.B * p.c.Hk;
-    if ((rows + 15) / 16 > INT32_MAX || dq_blocks > INT32_MAX || dkv_blocks > INT32_MAX)
-        return cudaErrorInvalidConfiguration;
-    cross_delta_kernel<<<static_cast<unsigned>((rows + 15) / 16), 256, 0, s>>>(p);
-    cross_rows_dq_kernel<<<static_cast<unsigned>(dq_blocks), 256, 0, s>>>(p, static_cast<int>(qb));
-    if (dkv_blocks > 0) cross_rows_dkv_kernel<<<static_cast<unsigned>(dkv_blocks), 256, 0, s>>>(p, static_cast<int>(kb));
-    return cudaGetLastError();
+    const int64_t rows = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq;
+    return rows == 1 ? launch_rows<1>(p, s) : launch_rows<2>(p, s);
 }
 
 }  // namespace sdv2

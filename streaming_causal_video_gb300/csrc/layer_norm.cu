@@ -528,7 +528,9 @@ Team forward_team(int cols, bool aligned)
         if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kSingle};
         return {4, round32((vecs + 3) / 4), kSingle};
     }
-    for (int nv = 4; nv >= 1; --nv)
+    // few warps exchange a narrow row quickly (1536 columns: 9.9 us with two, 13.6 us with three); a wide row needs
+    // them to hide each other's latencies (5120: 32.3 us with ten, 35.3 us with five)
+    for (int nv = vecs > 256 ? 2 : 4; nv >= 1; --nv)
         if (vecs % (32 * nv) == 0 && vecs / nv <= kMaxThreads) return {nv, vecs / nv, kFull};
     if (vecs <= 32) return {1, 32, kVector};
     if (vecs <= 64) return {2, 32, kVector};
