@@ -16,6 +16,8 @@ _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c
 
 
 class _Config(ctypes.Structure):
+    """A configuration and, until a field is set, what the binding derives from it."""
+
     @classmethod
     def make(cls, **kw):
         names = {n for n, _ in cls._fields_}
@@ -24,6 +26,16 @@ class _Config(ctypes.Structure):
                 raise TypeError("%s has no field %r" % (cls.__name__, k))
         return cls(**kw)
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("plan", None)
+        super().__setattr__(name, value)
+
+    def derived(self):
+        plan = self.__dict__.get("plan")
+        if plan is None:
+            plan = self.__dict__["plan"] = self._derive()
+        return plan
+
 
 class CrossConfig(_Config):
     """Mirror of sdv2_cross_cfg."""
@@ -31,12 +43,41 @@ class CrossConfig(_Config):
                 ("kv_len", _i64), ("q_token_stride", _i64), ("q_head_stride", _i64), ("q_batch_stride", _i64),
                 ("kv_token_stride", _i64), ("kv_head_stride", _i64), ("kv_batch_stride", _i64)]
 
+    def _derive(self):
+        """Shape, strides and bytes of q and of k and v; bytes of dense rows of q, of
+        log-sum-exps and of k; bytes of the workspace for a backward pass."""
+        B, H, Hk = self.batch, self.heads, self.kv_heads or self.heads
+        rows, kv_rows = max(B, 0) * max(H, 0) * max(self.q_len, 0), max(B, 0) * max(Hk, 0) * max(self.kv_len, 0)
+
+        def operand(length, heads, tok, hd, batch):
+            hd = hd or 128
+            tok = tok or heads * 128
+            batch = batch or max(max(length, 1) * tok, heads * hd)
+            span = 2 * ((B - 1) * batch + (length - 1) * tok + (heads - 1) * hd + 128) if min(B, length, heads) > 0 else 0
+            return (B, length, heads, 128), (batch, tok, hd, 1), span
+        return (operand(self.q_len, H, self.q_token_stride, self.q_head_stride, self.q_batch_stride),
+                operand(self.kv_len, Hk, self.kv_token_stride, self.kv_head_stride, self.kv_batch_stride),
+                rows * 256, rows * 4, kv_rows * 256, cross_workspace_bytes(self, True))
+
 
 class NormConfig(_Config):
     """Mirror of sdv2_norm_cfg."""
     _fields_ = [("rows", _i64), ("cols", _i32), ("x_dtype", _i32), ("y_dtype", _i32), ("weight_plus_one", _i32),
                 ("x_row_stride", _i64), ("y_row_stride", _i64), ("rows_per_group", _i64), ("group_stride", _i64),
                 ("eps", _f32)]
+
+    def _derive(self):
+        """Shape, strides, type and bytes of x and of y; bytes of the parameters, of their
+        gradients, of a value per row, and of the workspace."""
+        def operand(dtype, stride):
+            kind, size = _TYPE.get(dtype, (None, 4))
+            stride = stride or self.cols
+            return (self.rows, self.cols), (stride, 1), kind, _b._row_span(self.rows, stride, self.cols, size)
+        per = self.rows_per_group or self.rows
+        groups = (self.rows + per - 1) // per if per > 0 else 0
+        return (operand(self.x_dtype, self.x_row_stride), operand(self.y_dtype, self.y_row_stride),
+                _b._row_span(groups, self.group_stride or self.cols, self.cols, 4), groups * self.cols * 4, self.rows * 4,
+                norm_workspace_bytes(self))
 
 
 _LIB = None
@@ -80,28 +121,39 @@ class _Operands:
     __slots__ = ("device",)
 
     def __init__(self):
-        self.device = -1
+        self.device = -2
 
     def __call__(self, t, name, dtype, nbytes, dense=False):
         if t is None or type(t) is int:
             return t
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dtype is not dtype:
-            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
         device = t.get_device()
         if device != self.device:
-            if self.device >= 0:
+            if device < 0:
+                raise ValueError("%s must be a CUDA tensor" % name)
+            if self.device != -2:
                 raise ValueError("%s is on device %d, not on device %d" % (name, device, self.device))
             if device != _current_device():
                 raise ValueError("%s is on device %d, the current device is %d" % (name, device, _current_device()))
             self.device = device
-        if not t.is_contiguous():
-            if dense:
-                raise ValueError("%s must be contiguous" % name)
-        elif t.nbytes >= nbytes:
-            return t.data_ptr()
+        if t.dtype is not dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.is_contiguous():
+            if t.nbytes >= nbytes:
+                return t.data_ptr()
+        elif dense:
+            raise ValueError("%s must be contiguous" % name)
         return _b._dev(t, name, nbytes)
+
+    def view(self, t, name, dtype, shape, strides, nbytes):
+        """A view of the configuration's rank must have its shape and strides; a tensor of another rank is a
+        buffer that they are applied to."""
+        if t is not None and type(t) is not int and t.dim() == len(shape):
+            if t.shape != shape:
+                raise ValueError("%s is %s, the configuration says %s" % (name, tuple(t.shape), shape))
+            have = t.stride()
+            if have != strides and any(n > 1 and h != w for n, h, w in zip(shape, have, strides)):
+                raise ValueError("%s has strides %s, the configuration says %s" % (name, have, strides))
+        return self(t, name, dtype, nbytes)
 
 
 _BF, _FP, _U8 = torch.bfloat16, torch.float32, torch.uint8
@@ -121,108 +173,60 @@ def cross_workspace_init(cfg, ws, stream=None):
               "sdv2_cross_workspace_init")
 
 
-def _strides(heads, length, tok, hd, batch):
-    hd = hd or 128
-    tok = tok or heads * 128
-    return tok, hd, batch or max(max(length, 1) * tok, heads * hd)
-
-
-def _span(batch, length, heads, st):
-    """Bytes from an operand's first element to past its last."""
-    if batch < 1 or length < 1 or heads < 1:
-        return 0
-    return 2 * ((batch - 1) * st[2] + (length - 1) * st[0] + (heads - 1) * st[1] + 128)
-
-
-def _cross_operand(op, t, name, batch, length, heads, st):
-    """A [B][length][heads][128] view must have the configuration's strides; a tensor of another rank is
-    a buffer that they are applied to."""
-    if t is not None and type(t) is not int and t.dim() == 4:
-        if t.shape != (batch, length, heads, 128):
-            raise ValueError("%s is %s, the configuration says %s" % (name, tuple(t.shape), (batch, length, heads, 128)))
-        want, have = (st[2], st[0], st[1], 1), t.stride()
-        if want != have and any(n > 1 and w != h for n, w, h in zip(t.shape, want, have)):
-            raise ValueError("%s has strides %s, the configuration says %s" % (name, have, want))
-    return op(t, name, _BF, _span(batch, length, heads, st))
-
-
 def _lens(cfg, kv_lens):
     return None if kv_lens is None else _b._i64_array(kv_lens, cfg.batch)
 
 
-def _cross_inputs(cfg, op, q, k, v):
-    B, H, Hk = cfg.batch, cfg.heads, cfg.kv_heads or cfg.heads
-    qs = _strides(H, cfg.q_len, cfg.q_token_stride, cfg.q_head_stride, cfg.q_batch_stride)
-    ks = _strides(Hk, cfg.kv_len, cfg.kv_token_stride, cfg.kv_head_stride, cfg.kv_batch_stride)
-    return (_cross_operand(op, q, "q", B, cfg.q_len, H, qs), _cross_operand(op, k, "k", B, cfg.kv_len, Hk, ks),
-            _cross_operand(op, v, "v", B, cfg.kv_len, Hk, ks))
+def _cross_inputs(op, q, k, v, qs, ks):
+    return op.view(q, "q", _BF, *qs), op.view(k, "k", _BF, *ks), op.view(v, "v", _BF, *ks)
 
 
 def cross_attention(cfg, q, k, v, out, ws, kv_lens=None, lse=None, scale=0.0, stream=None):
     """q: [B][Nq][H][128], k, v: [B][Nk][Hk][128] bf16 with cfg's strides; out: [B][Nq][H][128] bf16 and
     lse: fp32 [B][H][Nq], dense; kv_lens: valid rows of k and v per stream (host integers)."""
     op = _Operands()
-    rows = max(cfg.batch, 0) * max(cfg.heads, 0) * max(cfg.q_len, 0)
-    _b._check(_lib().sdv2_cross_attention(ctypes.byref(cfg), _lens(cfg, kv_lens), *_cross_inputs(cfg, op, q, k, v),
-                                          float(scale), op(out, "out", _BF, rows * 256, True),
-                                          op(lse, "lse", _FP, rows * 4, True),
-                                          op(ws, "ws", _U8, 256), _stream(stream)), "sdv2_cross_attention")
+    qs, ks, rows, stats, _, _ = cfg.derived()
+    status = _lib().sdv2_cross_attention(ctypes.byref(cfg), _lens(cfg, kv_lens), *_cross_inputs(op, q, k, v, qs, ks), scale,
+                                         op(out, "out", _BF, rows, True), op(lse, "lse", _FP, stats, True),
+                                         op(ws, "ws", _U8, 256), _stream(stream))
+    if status:
+        _b._check(status, "sdv2_cross_attention")
 
 
 def cross_attention_backward(cfg, q, k, v, out, lse, dout, dq, dk, dv, ws, kv_lens=None, scale=0.0, stream=None):
     """Gradients dq [B][Nq][H][128] and dk, dv [B][Nk][Hk][128] (bf16, dense) of cross_attention, whose out
     and lse are given with the gradient dout of out; ws: cross_workspace_bytes(cfg, backward=True) bytes."""
     op = _Operands()
-    rows = max(cfg.batch, 0) * max(cfg.heads, 0) * max(cfg.q_len, 0)
-    kv_rows = max(cfg.batch, 0) * (cfg.kv_heads or cfg.heads) * max(cfg.kv_len, 0)
-    _b._check(_lib().sdv2_cross_attention_backward(
-        ctypes.byref(cfg), _lens(cfg, kv_lens), *_cross_inputs(cfg, op, q, k, v), op(out, "out", _BF, rows * 256, True),
-        op(lse, "lse", _FP, rows * 4, True), op(dout, "dout", _BF, rows * 256, True), float(scale),
-        op(dq, "dq", _BF, rows * 256, True), op(dk, "dk", _BF, kv_rows * 256, True),
-        op(dv, "dv", _BF, kv_rows * 256, True), op(ws, "ws", _U8, cross_workspace_bytes(cfg, True)),
-        _stream(stream)), "sdv2_cross_attention_backward")
-
-
-def _rows(cfg, op, t, name, dtype, stride):
-    """Rows of x or y: a 2-D tensor must be [rows][cols] with the configuration's row stride."""
-    kind, size = _TYPE.get(dtype, (None, 4))
-    stride = stride or cfg.cols
-    if t is not None and type(t) is not int and t.dim() == 2:
-        if t.shape != (cfg.rows, cfg.cols) or (cfg.cols > 1 and t.stride(1) != 1) or \
-                (cfg.rows > 1 and t.stride(0) != stride):
-            raise ValueError("%s is %s with strides %s, the configuration says %s and row stride %d" %
-                             (name, tuple(t.shape), tuple(t.stride()), (cfg.rows, cfg.cols), stride))
-    return op(t, name, kind, _b._row_span(cfg.rows, stride, cfg.cols, size))
-
-
-def _groups(cfg):
-    per = cfg.rows_per_group or cfg.rows
-    return (cfg.rows + per - 1) // per if per > 0 else 0
+    qs, ks, rows, stats, kv_rows, scratch = cfg.derived()
+    status = _lib().sdv2_cross_attention_backward(
+        ctypes.byref(cfg), _lens(cfg, kv_lens), *_cross_inputs(op, q, k, v, qs, ks), op(out, "out", _BF, rows, True),
+        op(lse, "lse", _FP, stats, True), op(dout, "dout", _BF, rows, True), scale, op(dq, "dq", _BF, rows, True),
+        op(dk, "dk", _BF, kv_rows, True), op(dv, "dv", _BF, kv_rows, True), op(ws, "ws", _U8, scratch), _stream(stream))
+    if status:
+        _b._check(status, "sdv2_cross_attention_backward")
 
 
 def layer_norm(cfg, x, y, weight=None, bias=None, mean=None, rstd=None, stream=None):
     """x: [rows][cols] of cfg.x_dtype; y: of cfg.y_dtype; weight, bias: fp32 [groups][cols], group_stride
     apart; mean, rstd: fp32 [rows], written for the backward pass."""
     op = _Operands()
-    par = _b._row_span(_groups(cfg), cfg.group_stride or cfg.cols, cfg.cols, 4)
-    _b._check(_lib().sdv2_layer_norm(ctypes.byref(cfg), _rows(cfg, op, x, "x", cfg.x_dtype, cfg.x_row_stride),
-                                     op(weight, "weight", _FP, par), op(bias, "bias", _FP, par),
-                                     _rows(cfg, op, y, "y", cfg.y_dtype, cfg.y_row_stride),
-                                     op(mean, "mean", _FP, cfg.rows * 4, True), op(rstd, "rstd", _FP, cfg.rows * 4, True),
-                                     _stream(stream)), "sdv2_layer_norm")
+    (shape, xs, xt, xb), (_, ys, yt, yb), par, _, stats, _ = cfg.derived()
+    status = _lib().sdv2_layer_norm(ctypes.byref(cfg), op.view(x, "x", xt, shape, xs, xb), op(weight, "weight", _FP, par),
+                                    op(bias, "bias", _FP, par), op.view(y, "y", yt, shape, ys, yb),
+                                    op(mean, "mean", _FP, stats, True), op(rstd, "rstd", _FP, stats, True), _stream(stream))
+    if status:
+        _b._check(status, "sdv2_layer_norm")
 
 
 def layer_norm_backward(cfg, dy, x, mean, rstd, dx, ws, weight=None, dweight=None, dbias=None, stream=None):
     """dx (of x's type and stride), and fp32 dweight, dbias [groups][cols] (dense, or None), from the
     gradient dy of y and what layer_norm read and wrote; ws: norm_workspace_bytes(cfg) bytes."""
     op = _Operands()
-    par = _b._row_span(_groups(cfg), cfg.group_stride or cfg.cols, cfg.cols, 4)
-    grads = _groups(cfg) * cfg.cols * 4
-    _b._check(_lib().sdv2_layer_norm_backward(
-        ctypes.byref(cfg), _rows(cfg, op, dy, "dy", cfg.y_dtype, cfg.y_row_stride),
-        _rows(cfg, op, x, "x", cfg.x_dtype, cfg.x_row_stride), op(weight, "weight", _FP, par),
-        op(mean, "mean", _FP, cfg.rows * 4, True), op(rstd, "rstd", _FP, cfg.rows * 4, True),
-        _rows(cfg, op, dx, "dx", cfg.x_dtype, cfg.x_row_stride), op(dweight, "dweight", _FP, grads, True),
-        op(dbias, "dbias", _FP, grads, True),
-        op(ws, "ws", _U8, norm_workspace_bytes(cfg) if (dweight is not None or dbias is not None) else 0),
-        _stream(stream)), "sdv2_layer_norm_backward")
+    (shape, xs, xt, xb), (_, ys, yt, yb), par, grads, stats, scratch = cfg.derived()
+    status = _lib().sdv2_layer_norm_backward(
+        ctypes.byref(cfg), op.view(dy, "dy", yt, shape, ys, yb), op.view(x, "x", xt, shape, xs, xb), op(weight, "weight", _FP, par),
+        op(mean, "mean", _FP, stats, True), op(rstd, "rstd", _FP, stats, True), op.view(dx, "dx", xt, shape, xs, xb),
+        op(dweight, "dweight", _FP, grads, True), op(dbias, "dbias", _FP, grads, True),
+        op(ws, "ws", _U8, scratch if (dweight is not None or dbias is not None) else 0), _stream(stream))
+    if status:
+        _b._check(status, "sdv2_layer_norm_backward")

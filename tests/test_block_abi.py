@@ -1,8 +1,10 @@
 """CPU tests of the block operators' C ABI: the library exports what include/sdv2_block.h declares,
 bad arguments are refused on the host with a status and a message, and the binding refuses tensors
 that do not match the configuration.  No kernel is launched here."""
+import copy
 import ctypes
 import os
+import pickle
 import re
 
 import pytest
@@ -36,6 +38,15 @@ def test_struct_layouts():
     assert sd.NormConfig.eps.offset == 56
     with pytest.raises(TypeError, match="no field"):
         sd.CrossConfig.make(head=3)
+
+
+def test_a_changed_configuration_is_derived_again():
+    c = norm(rows=6)
+    assert c.derived()[0][0] == (6, 40)
+    d = copy.copy(c)
+    c.rows = 7
+    assert c.derived()[0][0] == (7, 40) and d.derived()[0][0] == (6, 40) and d.rows == 6
+    assert pickle.loads(pickle.dumps(c)).derived() == c.derived()
 
 
 def cross(**over):
@@ -182,8 +193,9 @@ def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
     x, y = FakeTensor((6, 40)), FakeTensor((6, 40))
     w = FakeTensor((2, 40), torch.float32)
     for a, kw, match in (((FakeTensor((6, 40), torch.float32), y), {}, "x must be torch.bfloat16"),
-                         ((x, FakeTensor((6, 40), strides=(48, 1))), {}, "row stride 40"),
-                         ((x, FakeTensor((6, 40), strides=(1, 6))), {}, "y is"),
+                         ((x, FakeTensor((6, 40), strides=(48, 1))), {}, "y has strides"),
+                         ((x, FakeTensor((6, 40), strides=(1, 6))), {}, "y has strides"),
+                         ((FakeTensor((40, 6)), y), {}, "x is"),
                          ((x, y), dict(weight=FakeTensor((1, 40), torch.float32)), "weight: "),
                          ((x, y), dict(weight=w, mean=FakeTensor((5,), torch.float32)), "mean: ")):
         with pytest.raises(ValueError, match=match):
