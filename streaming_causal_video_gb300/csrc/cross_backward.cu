@@ -27,7 +27,9 @@
 // and R1, once for many steps), and of the second T1 slot in dQ (V is only needed for dP).
 // A first kernel leaves -lse (log2 units) and -delta of every query tile's 128 rows side by side in the
 // workspace, so that dKV copies them with the tiles.
-// Tensor memory: acc0 | acc1 | S | dP, 128 columns each.
+// Tensor memory: acc0 | acc1 | S | dP, 128 columns each.  dQ has no acc1: its columns hold Q and dO, which the
+// compute warps put there as the A operands of S and dP, so that their shared memory takes the next
+// unit's tiles while this unit runs (loading them between units cost 2000 of a unit's 12600 cycles).
 #include <algorithm>
 #include <atomic>
 
@@ -52,7 +54,7 @@ constexpr int kSms = 152;
 constexpr int kMaxSplits = 8;
 
 enum Bar { RFULL, REMPTY, T0FULL, T0EMPTY = T0FULL + T0ST, T1FULL = T0EMPTY + T0ST, T1EMPTY = T1FULL + 2, SFULL = T1EMPTY + 2,
-           SREAD, DPFULL, DSFULL, ACCFULL, MMADONE, NBARS };
+           SREAD, DPFULL, DSFULL, ACCFULL, RREADY, MMADONE, NBARS };
 
 constexpr uint32_t SMEM_TILES = 7 * TILE;                      // R0 R1, T0 slots, T1 slots, dQ: an output tile
 constexpr uint32_t SMEM_STATS = (T0ST + 2) * BM * 4;           // dKV: -lse per T0 slot, -delta per T1 slot
@@ -156,26 +158,35 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
     const uint64_t tmo = p.timeout_ns;
     const int used_rows = p.pack * p.tokens;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), i == SREAD || i == DSFULL ? COMPUTE : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
+    // The load warps only need the barriers: they start while the rest of the block is still setting up.
+    if (warp >= T0_WARP) {
+        if (threadIdx.x == T0_WARP * 32) {
+            for (int i = 0; i < NBARS; ++i)
+                mbar_init(bar(i), i == SREAD || i == DSFULL || i == RREADY || (i == REMPTY && !DKV) ? COMPUTE : 1);
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+    } else {
+        // Rows of a query tile that no load writes (the pack does not divide 128) are zero: as streamed tiles
+        // they are summed over, with probability 0.
+        for (int i = threadIdx.x; i < (BM - used_rows) * 16 * 7; i += COMPUTE) {
+            const int part = i & 15, r = i >> 4, tile = r / (BM - used_rows), row = used_rows + r - tile * (BM - used_rows);
+            *reinterpret_cast<uint4*>(smem + tile * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
     }
-    // Rows of a query tile that no load writes (the pack does not divide 128) are zero: as streamed tiles
-    // they are summed over, with probability 0.
-    for (int i = threadIdx.x; i < (BM - used_rows) * 16 * 7; i += NTHREADS) {
-        const int part = i & 15, r = i >> 4, tile = r / (BM - used_rows), row = used_rows + r - tile * (BM - used_rows);
-        *reinterpret_cast<uint4*>(smem + tile * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+    uint32_t tmem = 0;
+    if (warp <= MMA_WARP && warp != T0_WARP) {
+        if (warp == MMA_WARP) {
+            tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 3, 544;" ::: "memory");           // compute warps and the MMA warp
+        tc_fence_after();
+        tmem = *tmem_slot;
     }
-    fence_proxy_async();
-    if (warp == MMA_WARP) {
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     Walk<DKV, CAP> walk(p);
     Unit u;
     bool ok = true;
@@ -277,6 +288,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity, tmo, abort_flag));
             return ok;
         };
+        auto product_tm = [&](uint32_t d, uint32_t a, uint32_t b) {      // D = A B^T, A in tensor memory
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+                mma_ts_warp(tmem + d, tmem + a + k * 8, desc(b + (k >> 2) * HALF + (k & 3) * 32, 16), idKK, k > 0 ? 1u : 0u);
+        };
         auto product = [&](uint32_t d, uint32_t a, uint32_t b) {         // D = A B^T
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
@@ -298,22 +314,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         auto begin_s = [&]() {
             if (!wait(T0FULL + s_slot, s_ph)) return;
             tc_fence_after();
-            product(SCOL, sR, sT0 + s_slot * TILE);
+            if constexpr (DKV) product(SCOL, sR, sT0 + s_slot * TILE);
+            else product_tm(SCOL, ACC1, sT0 + s_slot * TILE);
             mma_commit_warp(bar(SFULL));
             if (++s_slot == T0ST) {
                 s_slot = 0;
                 s_ph ^= 1u;
             }
         };
-        auto begin_dp = [&](bool last) {
+        auto begin_dp = [&]() {
             if (!wait(T1FULL + p_slot, p_ph)) return;
             tc_fence_after();
-            product(XCOL, sR + TILE, sT1 + p_slot * TILE);
+            if constexpr (DKV) product(XCOL, sR + TILE, sT1 + p_slot * TILE);
+            else product_tm(XCOL, ACC1 + 64, sT1 + p_slot * TILE);
             mma_commit_warp(bar(DPFULL));
-            if (!DKV) {
-                mma_commit_warp(bar(T1EMPTY + p_slot));                  // V has done its part
-                if (last) mma_commit_warp(bar(REMPTY));
-            }
+            if (!DKV) mma_commit_warp(bar(T1EMPTY + p_slot));            // V has done its part
             if (++p_slot == T1ST) {
                 p_slot = 0;
                 p_ph ^= 1u;
@@ -322,11 +337,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         while (ok && walk.next(p, u)) {
             if (u.steps == 0) continue;
             // the unit before has read its last S and written its last dS, so both score tiles are free
-            if (!wait(RFULL, units & 1u)) break;
+            if (!wait(DKV ? RFULL : RREADY, units & 1u)) break;
             ++units;
+            tc_fence_after();
             begin_s();
             if (!ok) break;
-            begin_dp(u.steps == 1);
+            begin_dp();
             for (int i = 0; ok && i < u.steps; ++i, ++count) {
                 const bool more = i + 1 < u.steps;
                 if (DKV || more) {
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 mma_commit_warp(bar(T0EMPTY + a_slot0));
                 if (++a_slot0 == T0ST) a_slot0 = 0;
                 if (!more) mma_commit_warp(bar(ACCFULL));
-                else begin_dp(i + 2 == u.steps);
+                else begin_dp();
             }
         }
         if (!ok && lane == 0) give_up(abort_flag, p.err);
@@ -375,9 +391,41 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         };
         int slot0 = 0, slot1 = 0;              // dKV: T slots of the step
         uint32_t phase0 = 0, phase1 = 0;
+        uint32_t resident = 0;                 // dQ: units whose Q and dO went to tensor memory
+        auto put_resident = [&](const Unit& v) {
+            if constexpr (!DKV) {
+                if (v.steps == 0) return;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(RFULL), resident & 1u, tmo, abort_flag));
+                ++resident;
+                tc_fence_after();
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    const uint8_t* src = smem + which * TILE + (quarter >> 1) * HALF + row * 128;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(src + ((((quarter & 1) * 4 + e) ^ (row & 7)) << 4));
+                        w[4 * e] = x.x;
+                        w[4 * e + 1] = x.y;
+                        w[4 * e + 2] = x.z;
+                        w[4 * e + 3] = x.w;
+                    }
+                    tmem_st_x16(tL + ACC1 + which * 64 + quarter * 16, w);
+                }
+                mbar_arrive(bar(REMPTY));
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(RREADY));
+            }
+        };
         bool has = walk.next(p, u);
-        if (has) fetch_unit(u);
+        if (has) {
+            fetch_unit(u);
+            put_resident(u);
+        }
         while (has) {
+            Unit nx;                           // decoded here, not between the last step and the read-out
+            const bool more_units = walk.next(p, nx);
             const bool constant = DKV && p.n[u.b] == 1;           // a softmax over one key has no gradient
             const uint64_t lse2 = f32x2_pack(row_lse, row_lse), delta2 = f32x2_pack(row_delta, row_delta);
             // a thread whose wait ran out still runs through all steps, to meet the others at every barrier
@@ -447,10 +495,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                     }
                 }
             }
-            // the next unit's statistics are on their way while the accumulators are read out
-            Unit nx;
-            has = walk.next(p, nx);
-            if (has) fetch_unit(nx);
+            // the next unit's statistics and tiles are on their way while the accumulators are read out
+            has = more_units;
+            if (has) {
+                put_resident(nx);              // dP of the last step is there, so the unit is done with its own
+                fetch_unit(nx);
+            }
             // ------------------------------------------------------------ read out the accumulators
             if (u.steps > 0) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(ACCFULL), units & 1u, tmo, abort_flag));
@@ -621,6 +671,26 @@ struct Shape {
     int64_t kunits;                            // (stream, key head, key tile)
 };
 
+// Streamed tiles of a key tile's unit.
+int64_t steps_of(const Shape& s) { return static_cast<int64_t>(s.qtiles) * (s.group / s.pack); }
+
+// Ranges of query tiles for `units` key tiles: the smallest estimated time, a unit costing its steps and four more
+// for its start, end and parts.
+int best_splits(int64_t units, int64_t steps, int most)
+{
+    int splits = 1;
+    int64_t best = INT64_MAX;
+    for (int k = 1; k <= most && k <= steps; ++k) {
+        const int64_t t = ((units * k + kSms - 1) / kSms) * ((steps + k - 1) / k + 4);
+        if (t < best) {
+            best = t;
+            splits = k;
+        }
+    }
+    return splits;
+}
+
+// The splits are those for full streams; they size the workspace.
 Shape shape_of(int B, int H, int Hk, int64_t Nq, int64_t Nk)
 {
     Shape s;
@@ -631,17 +701,7 @@ Shape shape_of(int B, int H, int Hk, int64_t Nq, int64_t Nk)
     s.packs = H / s.pack;
     s.ktiles = static_cast<int>((Nk + BM - 1) / BM);
     s.kunits = static_cast<int64_t>(B) * Hk * s.ktiles;
-    // ranges of query tiles: the smallest estimated time, a unit costing its steps and four for its start, end and parts
-    const int64_t steps = static_cast<int64_t>(s.qtiles) * (s.group / s.pack);
-    s.splits = 1;
-    int64_t best = INT64_MAX;
-    for (int k = 1; k <= kMaxSplits && k <= steps; ++k) {
-        const int64_t t = ((s.kunits * k + kSms - 1) / kSms) * ((steps + k - 1) / k + 4);
-        if (t < best) {
-            best = t;
-            s.splits = k;
-        }
-    }
+    s.splits = best_splits(s.kunits, steps_of(s), kMaxSplits);
     return s;
 }
 
@@ -674,7 +734,11 @@ template <int CAP>
 cudaError_t launch(const CrossBackward& f, cudaStream_t s)
 {
     const CrossProblem& c = f.c;
-    const Shape sh = shape_of(c.B, c.H, c.Hk, c.Nq, c.Nk);
+    Shape sh = shape_of(c.B, c.H, c.Hk, c.Nq, c.Nk);
+    // key tiles behind a stream's last row have no work: no more ranges than the others need
+    int64_t live = 0;
+    for (int b = 0; b < c.B; ++b) live += static_cast<int64_t>(c.Hk) * ((c.n[b] + BM - 1) / BM);
+    sh.splits = best_splits(std::max<int64_t>(live, 1), steps_of(sh), sh.splits);
     static thread_local Params<CAP> p;
     p = Params<CAP>{};
     const CrossStrides dense = {int64_t(c.H) * HD, HD, int64_t(c.H) * HD * c.Nq};
