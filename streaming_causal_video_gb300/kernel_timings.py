@@ -13,6 +13,7 @@ import sys
 import torch
 
 from . import _binding as sd
+from . import _block as block
 from .layer import StreamSession
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -40,7 +41,7 @@ def main():
     ap.add_argument("--peak-gbs", type=float, default=0.0, help="HBM peak (GB/s); default: MEASURED_PEAKS.json or 6800")
     ap.add_argument("--layers", type=int, default=8, help="distinct layer caches cycled (more than L2 in total)")
     ap.add_argument("--only", default="", help="comma-separated subset of: append, attention, rerotate, sink, "
-                    "qkv, cublas, unfused, qkv14b, motion, noise, copies (default: all)")
+                    "qkv, cublas, unfused, qkv14b, cross, norm, motion, noise, copies (default: all)")
     args = ap.parse_args()
     only = {x.strip() for x in args.only.split(",") if x.strip()}
 
@@ -208,6 +209,42 @@ def main():
                    ms=_time(cp, 60, stream))
             del srcs, dsts
         torch.cuda.empty_cache()
+    # ---- around the chunk attention: cross attention to 512 prompt states and the norms, forward and backward
+    bf = lambda *shape: torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)
+    for ww in (w, WORKLOADS["wan14b_480p"]):
+        n, H, C, nk = 4, ww.heads, ww.heads * 128, 512
+        if want("cross"):
+            cross = block.CrossConfig.make(batch=1, heads=H, kv_heads=H, head_dim=128, q_len=ww.nq, kv_len=nk)
+            ws = torch.empty(block.cross_workspace_bytes(cross, True), dtype=torch.uint8, device=dev)
+            block.cross_workspace_init(cross, ws, stream)
+            sets = [dict(q=bf(1, ww.nq, H, 128), k=bf(1, nk, H, 128), v=bf(1, nk, H, 128), out=bf(1, ww.nq, H, 128),
+                         lse=torch.empty((1, H, ww.nq), dtype=torch.float32, device=dev)) for _ in range(n)]
+            grads = [dict(dout=bf(1, ww.nq, H, 128), dq=bf(1, ww.nq, H, 128), dk=bf(1, nk, H, 128), dv=bf(1, nk, H, 128))
+                     for _ in range(n)]
+            flops = 4.0 * H * 128 * ww.nq * nk
+            report("sdv2_cross_attention", ww.name + " (512 states)", flops_per_call=flops,
+                   ms=_time(lambda i: block.cross_attention(cross, ws=ws, stream=stream, **sets[i % n]), 60, stream))
+            report("sdv2_cross_attention_backward", ww.name + " (512 states)", flops_per_call=2.5 * flops,
+                   ms=_time(lambda i: block.cross_attention_backward(cross, ws=ws, stream=stream, **sets[i % n], **grads[i % n]),
+                            60, stream))
+            sd.check_device_error(ws, stream)
+            del sets, grads
+        if want("norm"):
+            cfg_n = block.NormConfig.make(rows=ww.nq, cols=C, rows_per_group=ww.hw, weight_plus_one=1, x_dtype=block.F32, eps=1e-6)
+            x = [torch.randn((ww.nq, C), generator=g, device=dev) for _ in range(n)]
+            y, dx = bf(ww.nq, C), torch.empty((ww.nq, C), device=dev)
+            par = torch.randn((4, ww.chunk_frames, C), generator=g, device=dev)
+            mean, rstd = (torch.empty(ww.nq, device=dev) for _ in range(2))
+            wsn = torch.empty(block.norm_workspace_bytes(cfg_n), dtype=torch.uint8, device=dev)
+            report("sdv2_layer_norm", ww.name + " (fp32 in, bf16 out, scale and shift per frame)", bytes_per_call=ww.nq * C * 6,
+                   ms=_time(lambda i: block.layer_norm(cfg_n, x[i % n], y, weight=par[0], bias=par[1], mean=mean, rstd=rstd,
+                                                    stream=stream), 60, stream))
+            report("sdv2_layer_norm_backward", ww.name + " (the same)", bytes_per_call=ww.nq * C * 10,
+                   ms=_time(lambda i: block.layer_norm_backward(cfg_n, y, x[i % n], mean, rstd, dx, wsn, weight=par[0],
+                                                             dweight=par[2], dbias=par[3], stream=stream), 60, stream))
+            del x
+        torch.cuda.empty_cache()
+
     if not (want("motion") or want("noise")):
         return out
 

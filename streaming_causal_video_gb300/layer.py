@@ -2,11 +2,15 @@
 
 A StreamSession owns the workspace, one LayerCache (k, v, slot metadata) per DiT layer and the
 q_rot / out buffers; layer_step() issues sdv2_rope_append_kv then sdv2_chunk_attention for one
-layer of one denoise step.  Nothing here computes: it allocates and calls the library.
+layer of one denoise step.  Around it, norm_step() normalises a chunk's tokens (before the
+projections) and cross_step() attends to the layer's prompt states, which set_prompt() names and
+which stay for all chunks and steps until the prompt changes.  Nothing here computes: it allocates
+and calls the library.
 """
 import torch
 
 from . import _binding as sd
+from . import _block as block
 
 
 class LayerCache:
@@ -32,6 +36,8 @@ class StreamSession:
         self.layers = [LayerCache(cfg, device, stream) for _ in range(layers)]
         self.q_rot = torch.empty((B, H, nq, D), dtype=torch.bfloat16, device=device)
         self.out = torch.empty((B, nq, H, D), dtype=torch.bfloat16, device=device)
+        self.prompts = [None] * layers
+        self.cross_ws = None
 
     def layer_step(self, layer: int, chunk_index, q, k, v, out=None, lse=None, stream=None):
         """Causal-RoPE + cache append, then chunk attention, for one layer.  q, k, v: [B][Nq][H][D]."""
@@ -40,4 +46,52 @@ class StreamSession:
         sd.rope_append_kv(self.cfg, self.start_frames, chunk_index, q, k, v, self.q_rot, L.k, L.v, L.meta,
                           self.ws, stream)
         sd.chunk_attention(self.cfg, chunk_index, self.q_rot, L.k, L.v, out, self.ws, lse=lse, stream=stream)
+        return out
+
+    def set_prompt(self, layer: int, k, v, lens=None, stream=None):
+        """States of the prompt encoder that cross_step(layer, ...) attends to: k, v [B][Nk][Hk][128] bf16, views
+        with any strides of whole 16 bytes (the same for both), kept by reference; lens: valid rows of each stream."""
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must be [B][Nk][Hk][128] with the same shape and strides")
+        if k.stride(3) != 1:
+            raise ValueError("k and v must be dense in their last dimension")
+        c = self.cfg
+        B, nk, hk, D = k.shape
+        if B != c.batch:
+            raise ValueError("k and v hold %d streams, the session %d" % (B, c.batch))
+        # a dimension of size one has no stride to speak of
+        tok = k.stride(1) if nk > 1 else 0
+        hd = k.stride(2) if hk > 1 else 0
+        batch = k.stride(0) if B > 1 else 0
+        cross = block.CrossConfig.make(batch=B, heads=c.heads, kv_heads=hk, head_dim=D, q_len=c.nq, kv_len=nk,
+                                       kv_token_stride=tok, kv_head_stride=hd, kv_batch_stride=batch)
+        lens = [nk] * B if lens is None else [int(n) for n in lens]
+        need = block.cross_workspace_bytes(cross)
+        if self.cross_ws is None or not need:          # init names what is wrong with a configuration without a size
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.ws.device)
+            block.cross_workspace_init(cross, ws, stream)
+            self.cross_ws = ws
+        self.prompts[layer] = (cross, k, v, lens)
+
+    def cross_step(self, layer: int, q, out=None, lse=None, stream=None):
+        """The chunk's queries q [B][Nq][H][128] attend to the layer's prompt; out as q (the session's by default)."""
+        if self.prompts[layer] is None:
+            raise ValueError("layer %d has no prompt: call set_prompt first" % layer)
+        cross, k, v, lens = self.prompts[layer]
+        out = self.out if out is None else out
+        block.cross_attention(cross, q, k, v, out, self.cross_ws, kv_lens=lens, lse=lse, stream=stream)
+        return out
+
+    def norm_step(self, x, out, weight=None, bias=None, modulated=False, eps=1e-6, stream=None):
+        """Layer norm of a chunk's tokens x [B][Nq][C] (bf16 or fp32) into out [B][Nq][C].  weight, bias fp32: [C], the
+        learned affine; or, modulated, [B*F][C], the scale and shift of every latent frame: xhat * (1 + weight) + bias."""
+        kinds = {torch.bfloat16: block.BF16, torch.float32: block.F32}
+        if x.dtype not in kinds or out.dtype not in kinds:
+            raise ValueError("x and out must be bf16 or fp32")
+        if x.shape != out.shape or not x.is_contiguous() or not out.is_contiguous():
+            raise ValueError("x and out must be contiguous and of one shape")
+        cfg = block.NormConfig.make(rows=x.numel() // x.shape[-1], cols=x.shape[-1], x_dtype=kinds[x.dtype],
+                                    y_dtype=kinds[out.dtype], weight_plus_one=int(modulated),
+                                    rows_per_group=self.cfg.hw if modulated else 0, eps=eps)
+        block.layer_norm(cfg, x, out, weight=weight, bias=bias, stream=stream)
         return out

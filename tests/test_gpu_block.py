@@ -533,3 +533,44 @@ def test_norm_projection_and_cross_attention_as_a_layer_runs_them():
     assert rel(c.out, out.detach()) <= 6 * BF
     for what, a, r in zip(("dx", "dweight", "dbias", "dk", "dv"), (n.dx, n.dweight, n.dbias, c.dk, c.dv), grads):
         assert rel(a, r) <= 6 * BF, what
+
+
+def test_session_runs_a_layer_with_norms_and_a_prompt():
+    """A session's layer as a model calls it: modulated norm -> fused projection -> chunk attention -> affine norm ->
+    query projection -> cross attention, for two chunks and a prompt that changes between them."""
+    B, H, D, F = 2, 2, 128, 3
+    C = H * D
+    cfg = sd.StreamConfig.make(batch=B, heads=H, head_dim=D, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=4, grid_w=6,
+                               chunk_frames=F, sink_frames=3, window_frames=4, refresh_chunks=0, qkv_token_stride=0)
+    sess = sd.StreamSession(cfg, 1, [0, 50], "cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    f32 = lambda *s: torch.randn(s, generator=g, device="cuda")
+    w_qkv, w_q = (f32(3 * C, C) / C ** 0.5).bfloat16(), (f32(C, C) / C ** 0.5).bfloat16()
+    scale, shift = 0.3 * f32(B * F, C), 0.3 * f32(B * F, C)
+    weight, bias = 1 + 0.1 * f32(1, C), 0.1 * f32(1, C)
+    y, z = (torch.empty((B, cfg.nq, C), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with pytest.raises(ValueError, match="no prompt"):
+        sess.cross_step(0, y.view(B, cfg.nq, H, D))
+    for chunk in range(2):
+        x = f32(B, cfg.nq, C)
+        sess.norm_step(x, y, scale, shift, modulated=True)
+        refs, tols = norm_reference(x.view(-1, C), scale, shift, cfg.hw, 1e-6, True, BF)
+        within(y.view(-1, C), refs[0], tols[0], "modulated norm")
+        L = sess.layers[0]
+        sd.qkv_rope_append(cfg, sess.start_frames, [chunk] * B, y, w_qkv, sess.q_rot, L.k, L.v, L.meta, sess.ws)
+        sd.chunk_attention(cfg, [chunk] * B, sess.q_rot, L.k, L.v, sess.out, sess.ws)
+        h = x + sess.out.view(B, cfg.nq, C).float()
+        sess.norm_step(h, z, weight, bias)
+        refs, tols = norm_reference(h.view(-1, C), weight, bias, B * cfg.nq, 1e-6, False, BF)
+        within(z.view(-1, C), refs[0], tols[0], "affine norm")
+        q = (z.float() @ w_q.float().t()).bfloat16().view(B, cfg.nq, H, D)
+        kv = torch.randn((B, 90 + chunk, 2, H, D), generator=g, device="cuda").bfloat16()     # packed keys and values
+        lens = [90, 31 + chunk]
+        sess.set_prompt(0, kv[:, :, 0], kv[:, :, 1], lens)
+        lse = torch.empty((B, H, cfg.nq), device="cuda")
+        out = sess.cross_step(0, q, lse=lse)
+        sd.check_device_error(sess.ws)
+        sd.check_device_error(sess.cross_ws)
+        ref, lse_ref, tol, lse_tol = cross_reference(q, kv[:, :, 0], kv[:, :, 1], lens, 1 / math.sqrt(D))
+        within(out, ref, tol, "cross attention")
+        within(lse, lse_ref, lse_tol, "lse")
