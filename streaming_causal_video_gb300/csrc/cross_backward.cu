@@ -26,7 +26,10 @@
 // tiles fit; the third T0 slot takes the place of an output tile in dKV (its read-out goes through R0
 // and R1, once for many steps), and of the second T1 slot in dQ (V is only needed for dP).
 // A first kernel leaves -lse (log2 units) and -delta of every query tile's 128 rows side by side in the
-// workspace, so that dKV copies them with the tiles.
+// workspace, so that dKV copies them with the tiles.  O is at hand in bf16 only, and its rounding reaches every dS
+// of the row through delta; the fewer keys, the less of it averages out (three keys, two queries: 0.005 of dQ, where
+// the roundings of P, dS and dQ come to 0.0024).  With one key tile (128 keys or fewer) the dQ launch has the
+// whole row: it takes delta = rowsum(P * dP) instead and puts it in the workspace for dKV.
 // Tensor memory: acc0 | acc1 | S | dP, 128 columns each.  dQ has no acc1: its columns hold Q and dO, which the
 // compute warps put there as the A operands of S and dP, so that their shared memory takes the next
 // unit's tiles while this unit runs (loading them between units cost 2000 of a unit's 12600 cycles).
@@ -68,7 +71,7 @@ struct Params {
     CUtensorMap kmap[CAP], vmap[CAP];          // per stream: valid rows
     CUtensorMap dkmap, dvmap;                  // (D, Hk, Nk, B): boxes of 64 dims x 1 x 128 rows
     int32_t n[CAP];
-    const float* stats;                        // [query tile][-lse (log2 units), -delta][128]
+    float* stats;                              // [query tile][-lse (log2 units), -delta][128]
     uint16_t *dk, *dv;                         // [B][Nk][Hk][D]
     float* part;                               // dKV: [split][unit][2][D/4][128][4]
     uint32_t* err;
@@ -427,7 +430,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             Unit nx;                           // decoded here, not between the last step and the read-out
             const bool more_units = walk.next(p, nx);
             const bool constant = DKV && p.n[u.b] == 1;           // a softmax over one key has no gradient
-            const uint64_t lse2 = f32x2_pack(row_lse, row_lse), delta2 = f32x2_pack(row_delta, row_delta);
+            const uint64_t lse2 = f32x2_pack(row_lse, row_lse);
+            uint64_t delta2 = f32x2_pack(row_delta, row_delta);
             // a thread whose wait ran out still runs through all steps, to meet the others at every barrier
 #pragma unroll 1
             for (int i = 0; i < u.steps; ++i, ++count) {
@@ -461,10 +465,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 if constexpr (DKV) tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(SREAD));
+                if constexpr (!DKV) {
+                    // Columns behind the stream's last key have a score of 0, whose exponential is no number where
+                    // the row's lse is below -88; their keys are zero, but the product would not be.
+                    const int keys = p.n[u.b] - i * BM - quarter * 32;
+                    if (keys < 32)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pr[e] = 2 * e >= keys ? 0 : 2 * e + 1 >= keys ? pr[e] & 0xFFFFFFFFu : pr[e];
+                }
                 if constexpr (DKV) ok = ok && mbar_wait_bounded(bar(T1FULL + slot1), phase1, tmo, abort_flag);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(DPFULL), count & 1u, tmo, abort_flag));
                 if (!ok) give_up(abort_flag, p.err);
                 tc_fence_after();
+                if constexpr (!DKV)
+                    if (u.steps == 1) {                            // delta = rowsum(P * dP), see the head of the file
+                        uint64_t sum2 = 0;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t x[16];
+                            tmem_ld_x16_sync(tL + XCOL + quarter * 32 + c * 16, x);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                sum2 = ffma2(f32x2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), pr[c * 8 + e], sum2);
+                        }
+                        float a, b;
+                        f32x2_unpack(sum2, a, b);
+                        float* part = reinterpret_cast<float*>(smem + SMEM_TILES);     // [quarter][row]
+                        part[quarter * BM + row] = a + b;
+                        compute_barrier();                         // the next write lies behind the read-out's barriers
+                        const float d = -((part[row] + part[BM + row]) + (part[2 * BM + row] + part[3 * BM + row]));
+                        delta2 = f32x2_pack(d, d);
+                        if (quarter == 0) p.stats[static_cast<int64_t>(u.index) * 2 * BM + BM + row] = d;
+                    }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t x[16], w[8];

@@ -59,7 +59,8 @@ def cross_reference(q, k, v, lens, scale):
 
 def cross_backward_reference(q, k, v, dout, lens, scale):
     """dq [B][Nq][H][D], dk, dv [B][Nk][Hk][D] in 64 bits and their bounds, when the kernel is given the
-    forward kernel's out (whose bound enters through delta = rowsum(dO * O))."""
+    forward kernel's out (whose bound enters through delta = rowsum(dO * O)); a stream of 128 keys or fewer
+    takes delta = rowsum(P * dP), in 32 bits from the same P and dP."""
     B, nq, H, D = q.shape
     nk, Hk = k.shape[1], k.shape[2]
     mk = lambda *s: torch.zeros(s, dtype=torch.float64, device=q.device)
@@ -76,9 +77,12 @@ def cross_backward_reference(q, k, v, dout, lens, scale):
         dp = db @ vb.transpose(1, 2)
         delta = (p * dp).sum(-1, keepdim=True)
         ds = p * (dp - delta)
-        delta_err = (db.abs() * out_tol[b].transpose(0, 1)).sum(-1, keepdim=True)
-        ds_err = (BF + prob) * ds.abs() + (1 + BF) * p * (delta_err + SUM * (db.abs() @ vb.abs().transpose(1, 2)) +
-                                                           SUM * delta_err)
+        dp_size = db.abs() @ vb.abs().transpose(1, 2)
+        if n <= 128:
+            delta_err = (p * ((prob + SUM) * dp.abs() + SUM * dp_size)).sum(-1, keepdim=True)
+        else:
+            delta_err = (db.abs() * out_tol[b].transpose(0, 1)).sum(-1, keepdim=True)
+        ds_err = (BF + prob) * ds.abs() + (1 + BF) * p * (delta_err + SUM * dp_size + SUM * delta_err)
         if n == 1:
             ds, ds_err = torch.zeros_like(ds), torch.zeros_like(ds_err)
         fold = lambda t: t.view(Hk, H // Hk, n, D).sum(1).transpose(0, 1)

@@ -172,6 +172,33 @@ def test_cross_attention_follows_growing_scores(nq, nk):
         within(c.lse, torch.logsumexp(s, -1), 2.0 ** -20 * (1 + s.abs().amax(-1)), "lse")
 
 
+@pytest.mark.parametrize("nq,nk,lens", [(3, 5, [5]), (150, 130, [130]), (70, 300, [300, 31])])
+def test_cross_attention_of_scores_far_below_zero(nq, nk, lens):
+    """Every score near -280: exp(-lse) is out of range, so a place behind the last key must not reach a sum."""
+    c = Cross(len(lens), 2, 2, nq, nk, lens, seed=4)
+    c.q.copy_(5.0 + 0.1 * c.q.float())
+    c.k.copy_(-5.0 + 0.1 * c.k.float())
+    c.forward()
+    c.check_forward()
+    assert float(c.lse.max()) < -150
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.parametrize("heads,kv_heads,nq,nk,lens", [(4, 4, 2, 3, [3]), (2, 2, 300, 3, [3, 2]), (6, 2, 9, 128, [128, 4, 127]),
+                                                       (3, 1, 40, 600, [2, 600, 33])])
+def test_gradients_of_few_keys_do_not_carry_the_rounding_of_out(heads, kv_heads, nq, nk, lens):
+    """With 128 keys or fewer delta comes from P and dP.  An out that is one bf16 step off in one direction would
+    move delta by a step of rowsum(|dO * O|), which the bound for so few keys has no room for."""
+    c = Cross(len(lens), heads, kv_heads, nq, nk, lens, seed=6)
+    c.forward()
+    for b, n in enumerate(lens):
+        if n <= 128:
+            c.out[b] = (c.out[b].float() * (1 + 2.0 ** -7)).to(torch.bfloat16)
+    c.backward()
+    c.check_backward()
+
+
 def test_nan_and_infinity_in_valid_rows_reach_only_what_reads_them():
     c = Cross(2, 2, 2, 140, 300, [300, 200], seed=9)
     c.forward()
