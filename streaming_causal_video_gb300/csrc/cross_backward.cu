@@ -217,14 +217,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                     mbar_arrive_expect_tx(bar(RFULL), 2 * query_bytes);
                     load_queries(&p.qmap, sR, RFULL, u.head, u.tile * p.tokens, u.b);
                     load_queries(&p.domap, sR + TILE, RFULL, u.head, u.tile * p.tokens, u.b);
-                    // the next unit's tiles reach L2 while this one runs: its load is on the way between units
-                    Walk<DKV, CAP> ahead = walk;
-                    Unit nx;
-                    if (ahead.next(p, nx) && nx.steps > 0)
-                        for (int hf = 0; hf < 2; ++hf) {
-                            tma_prefetch_4d(&p.qmap, hf * 64, nx.head, nx.tile * p.tokens, nx.b);
-                            tma_prefetch_4d(&p.domap, hf * 64, nx.head, nx.tile * p.tokens, nx.b);
-                        }
                 }
                 ++units;
             }
