@@ -179,9 +179,13 @@ size_t sdv2_cross_workspace_bytes(const sdv2_cross_cfg* c, int32_t backward)
     CrossStrides qs, kvs;
     if (check_cross(c, &qs, &kvs) != SDV2_OK) return 0;
     size_t bytes = kHeaderBytes;
-    if (backward)
-        bytes += stats_bytes(c) + cross_backward_part_bytes(std::min(c->batch, kCrossStreams), c->heads, kv_heads_of(c), c->q_len,
-                                                            c->kv_len);
+    if (backward) {
+        // the streams left over behind whole launches are fewer units, so that they may be cut into more ranges
+        auto parts = [&](int streams) {
+            return streams ? cross_backward_part_bytes(streams, c->heads, kv_heads_of(c), c->q_len, c->kv_len) : 0;
+        };
+        bytes += stats_bytes(c) + std::max(parts(std::min(c->batch, kCrossStreams)), parts(c->batch % kCrossStreams));
+    }
     return bytes;
 }
 

@@ -112,6 +112,18 @@ def test_invalid_cross_arguments():
         assert backward(cross(kv_len=0), k=None, v=None, dk=None, dv=None) in (2, 3)
 
 
+@pytest.mark.parametrize("heads,nq,nk", [(1, 200, 140), (4, 300, 512), (12, 4680, 512), (2, 5000, 60)])
+def test_cross_workspace_holds_every_launch_of_a_large_batch(heads, nq, nk):
+    """32 streams go into a launch.  The streams left over are cut into more ranges than a whole launch is, and the
+    partial sums of theirs need their room as well."""
+    make = lambda b: sd.CrossConfig.make(batch=b, heads=heads, head_dim=128, q_len=nq, kv_len=nk)
+    stats = lambda b: b * heads * -(-nq // 128) * 1024
+    scratch = lambda b: sd.cross_workspace_bytes(make(b), True) - stats(min(b, 32))
+    for rest in (1, 2, 5, 31):
+        for whole in (32, 64):
+            assert scratch(whole + rest) >= max(scratch(32), scratch(rest))
+
+
 def test_cross_workspace_sizes():
     c = cross(batch=3, heads=5, kv_heads=5, q_len=11)
     assert sd.cross_workspace_bytes(c) >= 256

@@ -111,6 +111,7 @@ CROSS = [
     (33, 2, 1, 20, 40, [(7 * b) % 41 for b in range(33)], "dense"),
     (33, 1, 1, 200, 140, [(37 * b) % 141 for b in range(33)], "packed"),
     (2, 2, 2, 50, 64, [0, 0], "dense"),
+    (34, 4, 4, 260, 300, [300 - b for b in range(34)], "dense"),       # the last two streams in more ranges than the others
 ]
 
 
