@@ -1,6 +1,10 @@
 """GPU tests of cross attention and layer norm, forward and backward, against plain 64-bit
 implementations with derived bounds (block_common.py)."""
 import math
+import subprocess
+import sys
+import threading
+from pathlib import Path
 
 import pytest
 import torch
@@ -602,3 +606,83 @@ def test_session_runs_a_layer_with_norms_and_a_prompt():
         ref, lse_ref, tol, lse_tol = cross_reference(q, kv[:, :, 0], kv[:, :, 1], lens, 1 / math.sqrt(D))
         within(out, ref, tol, "cross attention")
         within(lse, lse_ref, lse_tol, "lse")
+
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import streaming_causal_video_gb300 as sd
+g = torch.Generator(device="cuda").manual_seed(1)
+bf = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+cfgs = [sd.CrossConfig.make(batch=1, heads=2, head_dim=128, q_len=nq, kv_len=200) for nq in (1, 300)]
+ws = torch.zeros(max(sd.cross_workspace_bytes(c, True) for c in cfgs), dtype=torch.uint8, device="cuda")
+norm = sd.NormConfig.make(rows=300, cols=256, eps=1e-6)
+wsn = torch.zeros(sd.norm_workspace_bytes(norm), dtype=torch.uint8, device="cuda")
+k, v = bf(1, 200, 2, 128), bf(1, 200, 2, 128)
+def buffers(c):
+    n = c.q_len
+    return dict(q=bf(1, n, 2, 128), out=bf(1, n, 2, 128), lse=torch.zeros((1, 2, n), device="cuda"), dout=bf(1, n, 2, 128),
+                dq=bf(1, n, 2, 128), dk=bf(1, 200, 2, 128), dv=bf(1, 200, 2, 128))
+sets = [buffers(c) for c in cfgs]
+x, y, dy, dx = (bf(300, 256) for _ in range(4))
+mean, rstd = (torch.zeros(300, device="cuda") for _ in range(2))
+dw, db = (torch.zeros((1, 256), device="cuda") for _ in range(2))
+def work(i):
+    c, t = cfgs[i], sets[i]
+    sd.cross_attention(c, t["q"], k, v, t["out"], ws, lse=t["lse"])
+    sd.cross_attention_backward(c, t["q"], k, v, t["out"], t["lse"], t["dout"], t["dq"], t["dk"], t["dv"], ws)
+    sd.layer_norm(norm, x, y, mean=mean, rstd=rstd)
+    sd.layer_norm_backward(norm, dy, x, mean, rstd, dx, wsn, dweight=dw, dbias=db)
+torch.cuda.synchronize()
+graphs, stream = [], torch.cuda.Stream()
+for i in range(2):                       # the first calls of the process are captured; the graphs share the workspaces
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        work(i)
+    graphs.append(graph)
+names = ("out", "lse", "dq", "dk", "dv")
+for graph in graphs + graphs:
+    graph.replay()
+torch.cuda.synchronize()
+got = [[t[n].clone() for n in names] for t in sets] + [[y.clone(), dx.clone(), dw.clone(), db.clone()]]
+for i in range(2):
+    work(i)
+torch.cuda.synchronize()
+want = [[t[n] for n in names] for t in sets] + [[y, dx, dw, db]]
+assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+assert float(got[1][0].float().abs().max()) > 0 and float(got[2][2].abs().max()) > 0
+sd.check_device_error(ws)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS, str(Path(__file__).resolve().parents[1])], capture_output=True,
+                         text=True, timeout=240)
+    assert run.returncode == 0 and run.stdout.strip().endswith("same"), run.stderr[-2000:]
+
+
+def test_calls_from_several_host_threads():
+    """Each thread has its stream, workspace and buffers; the results are those of the same calls alone."""
+    def one(i):
+        return Cross(1 + i % 2, 2, 2, 40 + 90 * i, 130 + i, [130 + i] * (1 + i % 2), seed=20 + i)
+    want, cases = [one(i) for i in range(4)], [one(i) for i in range(4)]
+    for c in want:
+        c.forward()
+        c.backward()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+
+    def body(c, s):
+        for _ in range(20):
+            c.forward(stream=s)
+            c.backward(stream=s)
+    threads = [threading.Thread(target=body, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        sd.check_device_error(c.ws)
+        assert all(torch.equal(getattr(c, n), getattr(w, n)) for n in ("out", "lse", "dq", "dk", "dv"))
