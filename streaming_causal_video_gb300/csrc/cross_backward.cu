@@ -30,12 +30,15 @@
 // of the row through delta; the fewer keys, the less of it averages out (three keys, two queries: 0.005 of dQ, where
 // the roundings of P, dS and dQ come to 0.0024).  With one key tile (128 keys or fewer) the dQ launch has the
 // whole row: it takes delta = rowsum(P * dP) instead and puts it in the workspace for dKV.
+// The launches are chained: a kernel's CTAs set up, and load what no launch writes, on SMs that the launch before has
+// left (480p: 67.6 us in a stream and 57.2 in a graph without, 57.8 and 54.9 with).
 // Tensor memory: acc0 | acc1 | S | dP, 128 columns each.  dQ has no acc1: its columns hold Q and dO, which the
 // compute warps put there as the A operands of S and dP, so that their shared memory takes the next
 // unit's tiles while this unit runs (loading them between units cost 2000 of a unit's 12600 cycles).
 #include <algorithm>
 #include <atomic>
 
+#include "chained.cuh"
 #include "cross_tma.cuh"
 #include "internal.h"
 #include "softmax_tile.cuh"
@@ -140,6 +143,7 @@ __device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, 51
 template <bool DKV, int CAP>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __grid_constant__ Params<CAP> p)
 {
+    if constexpr (!DKV) launch_dependents();   // from dKV for the fold it is slower (480p: 57.2 us in a graph, 54.9 without)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     if (static_cast<uint32_t>(smem - smem_raw) + SMEM_USED > SMEM_BYTES) {   // uniform: the base is the same for all
@@ -231,6 +235,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             const int nst = t0 ? T0ST : T1ST;
             const int full = t0 ? T0FULL : T1FULL, empty = t0 ? T0EMPTY : T1EMPTY;
             const uint32_t ring = t0 ? sT0 : sT1, stat_ring = t0 ? sL : sD;
+            if constexpr (DKV) {
+                wait_for_launch_before();      // the statistics, and the deltas that dQ put there
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+            }
             int slot = 0;
             uint32_t phase = 0, pending = 0;
             while (ok && walk.next(p, u)) {
@@ -414,6 +422,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             }
         };
         bool has = walk.next(p, u);
+        if constexpr (!DKV) wait_for_launch_before();              // the statistics
         if (has) {
             fetch_unit(u);
             put_resident(u);
@@ -603,6 +612,7 @@ __global__ void __launch_bounds__(256) cross_fold_kernel(const float4* __restric
                                                          int Hk, int Nk, float scale, uint16_t* __restrict__ dk,
                                                          uint16_t* __restrict__ dv)
 {
+    wait_for_launch_before();
     __shared__ __align__(16) uint16_t tile[BM][32 + 8];
     const int64_t unit = blockIdx.x;
     const int which = blockIdx.y;
@@ -648,6 +658,7 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* __rest
                                                           const float* __restrict__ lse, float* __restrict__ stats, int H,
                                                           int Nq, int pack, int tokens, int qtiles, int packs)
 {
+    launch_dependents();
     const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
     const uint32_t bp = blockIdx.x / static_cast<uint32_t>(qtiles);
     const int tile = static_cast<int>(blockIdx.x - bp * qtiles);
@@ -816,8 +827,8 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
 
     int ctas = static_cast<int>(std::min<int64_t>(qunits, kSms));
     cut(p.start, ctas, c.B, static_cast<int64_t>(sh.packs) * sh.qtiles, [&](int64_t b) { return c.n[b] > 1 ? (c.n[b] + BM - 1) / BM + int64_t(1) : 1; });
-    dq_kernel<<<dim3(static_cast<unsigned>(ctas)), NTHREADS, SMEM_BYTES, s>>>(p);
-    if (c.Nk == 0) return cudaGetLastError();
+    e = launch_chained(dq_kernel, dim3(static_cast<unsigned>(ctas)), dim3(NTHREADS), SMEM_BYTES, s, p);
+    if (e != cudaSuccess || c.Nk == 0) return e;
     // dKV: a run is a key tile's splits
     const int64_t all_steps = static_cast<int64_t>(sh.qtiles) * (sh.group / sh.pack);
     ctas = static_cast<int>(std::min<int64_t>(sh.kunits * sh.splits, kSms));
@@ -826,12 +837,11 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
         return (r % sh.ktiles) * BM < c.n[b] ? (all_steps + sh.splits - 1) / sh.splits + 4 : int64_t(1);
     });
     p.units = sh.kunits;
-    dkv_kernel<<<dim3(static_cast<unsigned>(ctas)), NTHREADS, SMEM_BYTES, s>>>(p);
-    if (sh.splits > 1)
-        cross_fold_kernel<<<dim3(static_cast<unsigned>(sh.kunits), 2, 4), 256, 0, s>>>(reinterpret_cast<const float4*>(f.part), sh.splits,
-                                                                                    sh.kunits, sh.ktiles, c.Hk, c.Nk, c.scale,
-                                                                                    f.dk, f.dv);
-    return cudaGetLastError();
+    e = launch_chained(dkv_kernel, dim3(static_cast<unsigned>(ctas)), dim3(NTHREADS), SMEM_BYTES, s, p);
+    if (e == cudaSuccess && sh.splits > 1)
+        e = launch_chained(cross_fold_kernel, dim3(static_cast<unsigned>(sh.kunits), 2, 4), dim3(256), 0, s,
+                           reinterpret_cast<const float4*>(f.part), sh.splits, sh.kunits, sh.ktiles, c.Hk, c.Nk, c.scale, f.dk, f.dv);
+    return e;
 }
 
 }  // namespace

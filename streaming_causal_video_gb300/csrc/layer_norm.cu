@@ -27,6 +27,7 @@
 #include <algorithm>
 
 #include "block.h"
+#include "chained.cuh"
 #include "softmax_tile.cuh"
 
 namespace sdv2 {
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
 template <int NV, Rows MODE, bool XF32, bool YF32>
 __global__ void __launch_bounds__(kMaxThreads, NV == 1 && MODE != kSingle ? 2 : 1) norm_backward_kernel(const NormParams p)
 {
+    launch_dependents();                       // the fold (4680 x 1536: 20.7 us in a stream unchained, 18.8 chained)
     constexpr bool VECTOR = MODE != kSingle;
     constexpr int C = columns(XF32, YF32), N = NV * 8 / C;
     constexpr int S = stages(NV * 16 * ((XF32 ? 2 : 1) + (YF32 ? 2 : 1)));
@@ -493,6 +495,7 @@ __global__ void __launch_bounds__(32 * kFoldLanes) norm_fold_kernel(const float*
                                                                     float* dweight, float* dbias)
 {
     float* out = blockIdx.z ? dbias : dweight;
+    wait_for_launch_before();
     if (!out) return;
     __shared__ float part[kFoldLanes][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
@@ -645,7 +648,7 @@ cudaError_t launch_layer_norm_backward(const NormParams& p, cudaStream_t s)
     if (p.slices > 1 && (p.dweight || p.dbias)) {
         const int64_t groups = (p.rows + p.rows_per_group - 1) / p.rows_per_group;
         const dim3 fold(static_cast<unsigned>((p.cols + 31) / 32), static_cast<unsigned>(groups), 2);
-        norm_fold_kernel<<<fold, dim3(32, kFoldLanes), 0, s>>>(p.partial, p.slices, p.cols, p.dweight, p.dbias);
+        return launch_chained(norm_fold_kernel, fold, dim3(32, kFoldLanes), 0, s, p.partial, p.slices, p.cols, p.dweight, p.dbias);
     }
     return cudaGetLastError();
 }
