@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "chained.cuh"
 #include "cross_tma.cuh"
 #include "internal.h"
 #include "ptx_pair.cuh"
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
         tc_fence_after();
         tmem = *tmem_slot;
     }
+    wait_for_launch_before();
     Walk walk(p);
     Item it;
     bool ok = true;
@@ -731,12 +733,12 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
     cfg.blockDim = dim3(NTHREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(splits);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2] = {chained_attribute(), {}};
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -608,9 +608,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
 
 // Adds the splits of a key tile's dK or dV in order.  grid: (units, 2, 4): a block adds 32 dims of 128 rows, turned
 // around in shared memory because the parts lie [dims / 4][row].
-__global__ void __launch_bounds__(256) cross_fold_kernel(const float4* __restrict__ part, int splits, int64_t units, int ktiles,
-                                                         int Hk, int Nk, float scale, uint16_t* __restrict__ dk,
-                                                         uint16_t* __restrict__ dv)
+__global__ void __launch_bounds__(256) cross_fold_kernel(const float4* part, int splits, int64_t units, int ktiles, int Hk,
+                                                         int Nk, float scale, uint16_t* dk, uint16_t* dv)
 {
     wait_for_launch_before();
     __shared__ __align__(16) uint16_t tile[BM][32 + 8];
@@ -654,11 +653,11 @@ __global__ void __launch_bounds__(256) cross_fold_kernel(const float4* __restric
 
 // -lse (log2 units) and -delta = -rowsum(dO * O) of a query tile's rows; rows that are none get lse = infinity, so
 // that their probabilities are 0.  grid: (query tiles, 4): a half-warp per row, two rows each.
-__global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* __restrict__ out, const uint16_t* __restrict__ dout,
-                                                          const float* __restrict__ lse, float* __restrict__ stats, int H,
-                                                          int Nq, int pack, int tokens, int qtiles, int packs)
+__global__ void __launch_bounds__(256) cross_stats_kernel(const uint16_t* out, const uint16_t* dout, const float* lse,
+                                                          float* stats, int H, int Nq, int pack, int tokens, int qtiles, int packs)
 {
-    launch_dependents();
+    wait_for_launch_before();
+    launch_dependents();                       // behind the wait: dQ reads what was there before the call without one
     const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
     const uint32_t bp = blockIdx.x / static_cast<uint32_t>(qtiles);
     const int tile = static_cast<int>(blockIdx.x - bp * qtiles);
@@ -816,9 +815,8 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     const int64_t qunits = static_cast<int64_t>(c.B) * sh.packs * sh.qtiles;
     if (qunits > INT32_MAX || sh.kunits * sh.splits > INT32_MAX) return cudaErrorInvalidConfiguration;
 
-    cross_stats_kernel<<<dim3(static_cast<unsigned>(qunits), 4), 256, 0, s>>>(f.out, f.dout, f.lse, f.stats, c.H, c.Nq, sh.pack,
-                                                                           sh.tokens, sh.qtiles, sh.packs);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_chained(cross_stats_kernel, dim3(static_cast<unsigned>(qunits), 4), dim3(256), 0, s, f.out, f.dout, f.lse,
+                                   f.stats, c.H, c.Nq, sh.pack, sh.tokens, sh.qtiles, sh.packs);
     if (e != cudaSuccess) return e;
     static std::atomic<uint64_t> dq_set{0}, dkv_set{0};
     auto dq_kernel = cross_backward_kernel<false, CAP>;

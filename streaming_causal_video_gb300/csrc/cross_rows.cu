@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "block.h"
+#include "chained.cuh"
 #include "ptx.cuh"
 #include "ptx_pair.cuh"
 
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     const int j1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits);
     const float sl2 = p.c.scale * kLog2e;
 
+    wait_for_launch_before();
     Vec8 q[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -261,12 +263,12 @@ static cudaError_t launch_rows(const CrossForward& p, cudaStream_t s)
     cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(splits);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2] = {chained_attribute(), {}};
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, cross_rows_kernel<kRows>, p, splits, static_cast<int>(row_blocks));
 }
 

@@ -100,12 +100,12 @@ __device__ __forceinline__ void load_param(const float* p, bool vector, int n, u
     if (vector) {
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p + k));
+            const float4 a = *reinterpret_cast<const float4*>(p + k);
             x[k] = a.x; x[k + 1] = a.y; x[k + 2] = a.z; x[k + 3] = a.w;
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k) x[k] = k < n ? __ldg(p + k) : 0.f;
+        for (int k = 0; k < C; ++k) x[k] = k < n ? p[k] : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < C / 2; ++k) v[k] = f32x2_pack(x[2 * k], x[2 * k + 1]);
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
     int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= p.rows) return;                         // whole team: its barrier is its own
+    wait_for_launch_before();
     using RingX = Ring<N, C, XF32, MODE>;
     const RingX ring{shared_address(copied) + (threadIdx.y * team + t) * RingX::BYTES, team * static_cast<int>(blockDim.y)};
     uint64_t next[VECTOR ? 1 : NV * 4];                // single elements: the next row
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 && MODE != kSingle ? 2 : 
         ring_x.copy(slot, row_of(p.x, r, p.xs, XF32), team, t, p.cols);
         ring_y.copy(slot, row_of(p.dy, r, p.ys, YF32), team, t, p.cols);
     };
+    wait_for_launch_before();
     float next_mean = 0.f, next_rstd = 0.f;
     if (row < row_end) {
         next_mean = p.mean[row];
@@ -584,8 +586,8 @@ cudaError_t forward(const NormParams& p, int threads, cudaStream_t s)
     auto kernel = norm_forward_kernel<NV, MODE, XF32, YF32>;
     const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)), smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)),
+                          smem, s, p);
 }
 
 template <int NV, Rows MODE, bool XF32, bool YF32>
@@ -600,9 +602,8 @@ cudaError_t backward(const NormParams& p, int threads, cudaStream_t s)
     auto kernel = norm_backward_kernel<NV, MODE, XF32, YF32>;
     const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(static_cast<unsigned>(groups * p.slices)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)),
-             smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kernel, dim3(static_cast<unsigned>(groups * p.slices)),
+                          dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)), smem, s, p);
 }
 
 // Calls f<NV, MODE, XF32, YF32>(p, threads, s) for the row's width, alignment and types.

@@ -686,3 +686,56 @@ def test_calls_from_several_host_threads():
     for c, w in zip(cases, want):
         sd.check_device_error(c.ws)
         assert all(torch.equal(getattr(c, n), getattr(w, n)) for n in ("out", "lse", "dq", "dk", "dv"))
+
+
+def test_results_follow_what_other_streams_and_copies_bring():
+    """The launches start early and wait for what is before them: a kernel, a copy, a fill, another stream's event;
+    eagerly and captured.  The inputs change right in front of every call, and the outputs are read right behind."""
+    c, want = Cross(1, 2, 2, 300, 260, [260], seed=31), Cross(1, 2, 2, 300, 260, [260], seed=32)
+    n = Norm(rows=300, cols=512, per=100)
+    want.forward()
+    want.backward()
+    n.forward()
+    n.backward()
+    ref = [t.clone() for t in (n.y, n.dx, n.dweight, n.dbias)]
+    x, dy = n.x.clone(), n.dy.clone()
+    other = torch.cuda.Stream()
+    busy = torch.zeros(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+
+    def spoil():
+        for t in (c.q, c.k, c.v, c.dout, c.out, c.dq, c.dk, c.dv, n.x, n.dy, n.y, n.dx):
+            t.fill_(7.0)
+
+    def run(kind):
+        main = torch.cuda.current_stream()
+        spoil()
+        busy.add_(1.0)                         # long enough for a launch that does not wait to overtake
+        if kind == "stream":
+            other.wait_stream(main)
+            with torch.cuda.stream(other):
+                for a, b in ((c.q, want.q), (c.k, want.k), (c.v, want.v), (c.dout, want.dout), (n.x, x), (n.dy, dy)):
+                    a.copy_(b * 1.0)
+            main.wait_stream(other)
+        else:                                  # copies (device to device) or kernels
+            for a, b in ((c.q, want.q), (c.k, want.k), (c.v, want.v), (c.dout, want.dout), (n.x, x), (n.dy, dy)):
+                a.copy_(b) if kind == "copy" else torch.mul(b, 1.0, out=a)
+        c.forward()
+        c.backward()
+        n.forward()
+        n.backward()
+        return [t.clone() for t in (c.out, c.lse, c.dq, c.dk, c.dv, n.y, n.dx, n.dweight, n.dbias)]
+
+    expect = [want.out, want.lse, want.dq, want.dk, want.dv] + ref
+    for kind in ("copy", "kernel", "stream"):
+        for _ in range(3):
+            got = run(kind)
+            assert all(torch.equal(a, b) for a, b in zip(got, expect)), kind
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            got = run(kind)
+        for _ in range(3):
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(got, expect)), "captured " + kind
+    sd.check_device_error(c.ws)
