@@ -127,6 +127,15 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// 1 / sqrt(v) within a step: one of Newton's steps from the hardware's estimate, which is within two.  The step has no
+// value where the estimate is 0 or infinite.  A division by a square root took two calls with branches.
+__device__ __forceinline__ float reciprocal_root(float v)
+{
+    const float r = rsqrtf(v);
+    const float better = fmaf(r, fmaf(-0.5f * v * r, r, 0.5f), r);
+    return v > 0.f && v < INFINITY ? better : r;
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -219,6 +228,12 @@ struct Ring {
 
 // Rows copied ahead: up to 192 bytes a thread.
 constexpr int stages(int bytes_per_row) { return bytes_per_row <= 32 ? 6 : bytes_per_row <= 48 ? 4 : bytes_per_row <= 64 ? 3 : 2; }
+// In the forward pass, which takes rows in pairs where registers hold two: up to 256 bytes.
+constexpr int forward_stages(int bytes_per_row) { return bytes_per_row <= 32 ? 6 : bytes_per_row <= 64 ? 4 : 2; }
+// Threads that the kernel is compiled for, which caps its registers: by them the launch counts the blocks of an SM.
+constexpr int forward_bound(int nv, Rows mode) { return mode == kSingle || nv > 2 ? 512 : nv == 2 ? 640 : 1024; }
+constexpr int forward_registers(int nv, Rows mode) { return 65536 / forward_bound(nv, mode) / 8 * 8; }
+constexpr int forward_rows(int nv, Rows mode, bool x_f32) { return mode != kSingle && (nv == 2 || (nv == 3 && !x_f32)) ? 2 : 1; }
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -229,13 +244,13 @@ __device__ __forceinline__ const char* row_of(const void* base, int64_t row, int
 
 // blockDim = (team, teams): a team takes the rows of its index, then every gridDim * teams further.
 template <int NV, Rows MODE, bool XF32, bool YF32>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormParams p)
+__global__ void __launch_bounds__(forward_bound(NV, MODE)) norm_forward_kernel(const NormParams p)
 {
     constexpr bool VECTOR = MODE != kSingle;
     constexpr int C = columns(XF32, YF32), N = NV * 8 / C;
-    constexpr int S = stages(NV * 16 * (XF32 ? 2 : 1));
+    constexpr int S = forward_stages(NV * 16 * (XF32 ? 2 : 1)), R = forward_rows(NV, MODE, XF32);
     extern __shared__ __align__(16) uint8_t copied[];
-    __shared__ float scratch[2][2][kMaxThreads / 32];
+    __shared__ float scratch[2][2][R * kMaxThreads / 32];
     const int team = blockDim.x, t = threadIdx.x;
     const int warps = team >> 5, warp = t >> 5;
     const int id = 1 + threadIdx.y;
@@ -264,10 +279,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
     uint64_t gain[NV * 4], bias[NV * 4];
     int64_t group_end = 0;
     int slot = 0, phase = 0;
-#pragma unroll 1
-    for (; row < p.rows; row += step) {
-        if (row >= group_end) {
-            const int64_t group = row / p.rows_per_group;
+    auto parameters = [&](int64_t r) {
+        if (r >= group_end) {
+            const int64_t group = r / p.rows_per_group;
             group_end = (group + 1) * p.rows_per_group;
             for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
 #pragma unroll
@@ -284,55 +298,76 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
                 if (p.bias) load_param<C>(p.bias + group * p.gs + c, VECTOR, n, bias + i);
             });
         }
-        uint64_t v[NV * 4];
+    };
+#pragma unroll 1
+    for (; row < p.rows; row += R * step) {
+        if constexpr (!VECTOR) parameters(row);        // in front of the sums: 14.0 us, 15.0 behind them (3001 x 1001)
+        uint64_t v[R][NV * 4];
         if constexpr (VECTOR) {
-            copy_wait<S - 1>();
-            ring.read(slot, team, t, p.cols, v);
-            if (row + S * step < p.rows) ring.copy(slot, row_of(p.x, row + S * step, p.xs, XF32), team, t, p.cols);
-            copy_commit();
-            if (++slot == S) slot = 0;
+            copy_wait<S - R>();
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                ring.read(slot, team, t, p.cols, v[k]);
+                if (row + (S + k) * step < p.rows) ring.copy(slot, row_of(p.x, row + (S + k) * step, p.xs, XF32), team, t, p.cols);
+                copy_commit();
+                if (++slot == S) slot = 0;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV * 4; ++i) v[i] = next[i];
+            for (int i = 0; i < NV * 4; ++i) v[0][i] = next[i];
             if (row + step < p.rows) fetch(row + step);
         }
-        uint64_t two[2] = {0, 0};
+        // a second row behind the last is worked on like any other (its slot holds something older) and not stored
+        float mean[R], var[R];
 #pragma unroll
-        for (int i = 0; i < NV * 4; ++i) two[i & 1] = fadd2(two[i & 1], v[i]);
-        float mean[1] = {add_pair(fadd2(two[0], two[1]))};
-        // two sets of scratch in turn: a warp that is a row ahead does not touch what others still read
-        team_sums<1>(mean, warps, warp, scratch[phase][0] + threadIdx.y * warps, id);
-        mean[0] *= inv_cols;
-        two[0] = two[1] = 0;
-        const uint64_t minus = both(-mean[0]);
-        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int, int n) {
+        for (int k = 0; k < R; ++k) {
+            uint64_t two[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < C / 2; ++k) {
-                uint64_t d = fadd2(v[i + k], minus);
-                if constexpr (!VECTOR) {               // columns past the row's end stay 0
-                    float a, b;
-                    f32x2_unpack(d, a, b);
-                    d = f32x2_pack(2 * k < n ? a : 0.f, 2 * k + 1 < n ? b : 0.f);
-                }
-                v[i + k] = d;
-                two[k & 1] = ffma2(d, d, two[k & 1]);
-            }
-        });
-        float var[1] = {add_pair(fadd2(two[0], two[1]))};
-        team_sums<1>(var, warps, warp, scratch[phase][1] + threadIdx.y * warps, id);
-        phase ^= 1;
-        const float rstd = 1.0f / sqrtf(fmaf(var[0], inv_cols, p.eps));
-        if (t == 0) {
-            if (p.mean) p.mean[row] = mean[0];
-            if (p.rstd) p.rstd[row] = rstd;
+            for (int i = 0; i < NV * 4; ++i) two[i & 1] = fadd2(two[i & 1], v[k][i]);
+            mean[k] = add_pair(fadd2(two[0], two[1]));
         }
-        const uint64_t rstd2 = both(rstd);
-        for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
-            uint64_t y[C / 2];
+        // two sets of scratch in turn: a warp that is an iteration ahead does not touch what others still read
+        team_sums<R>(mean, warps, warp, scratch[phase][0] + threadIdx.y * warps * R, id);
 #pragma unroll
-            for (int k = 0; k < C / 2; ++k) y[k] = ffma2(fmul2(v[i + k], rstd2), gain[i + k], bias[i + k]);
-            store_columns<C, YF32, VECTOR>(p.y, row * p.ys + c, n, y);
-        });
+        for (int k = 0; k < R; ++k) {
+            mean[k] *= inv_cols;
+            uint64_t two[2] = {0, 0};
+            const uint64_t minus = both(-mean[k]);
+            for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int, int n) {
+#pragma unroll
+                for (int e = 0; e < C / 2; ++e) {
+                    uint64_t d = fadd2(v[k][i + e], minus);
+                    if constexpr (!VECTOR) {           // columns past the row's end stay 0
+                        float a, b;
+                        f32x2_unpack(d, a, b);
+                        d = f32x2_pack(2 * e < n ? a : 0.f, 2 * e + 1 < n ? b : 0.f);
+                    }
+                    v[k][i + e] = d;
+                    two[e & 1] = ffma2(d, d, two[e & 1]);
+                }
+            });
+            var[k] = add_pair(fadd2(two[0], two[1]));
+        }
+        team_sums<R>(var, warps, warp, scratch[phase][1] + threadIdx.y * warps * R, id);
+        phase ^= 1;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = row + k * step;
+            if (k > 0 && r >= p.rows) break;
+            const float rstd = reciprocal_root(fmaf(var[k], inv_cols, p.eps));
+            if (t == 0) {
+                if (p.mean) p.mean[r] = mean[k];
+                if (p.rstd) p.rstd[r] = rstd;
+            }
+            if constexpr (VECTOR) parameters(r);
+            const uint64_t rstd2 = both(rstd);
+            for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
+                uint64_t y[C / 2];
+#pragma unroll
+                for (int e = 0; e < C / 2; ++e) y[e] = ffma2(fmul2(v[k][i + e], rstd2), gain[i + e], bias[i + e]);
+                store_columns<C, YF32, VECTOR>(p.y, r * p.ys + c, n, y);
+            });
+        }
     }
 }
 
@@ -572,15 +607,14 @@ cudaError_t allow_shared(K kernel, size_t bytes)
 template <int NV, Rows MODE, bool XF32, bool YF32>
 cudaError_t forward(const NormParams& p, int threads, cudaStream_t s)
 {
-    constexpr int S = stages(NV * 16 * (XF32 ? 2 : 1));
+    constexpr int S = forward_stages(NV * 16 * (XF32 ? 2 : 1));
     constexpr int kBytes = MODE != kSingle ? S * NV * 16 * (XF32 ? 2 : 1) : 0;          // of shared memory per thread
     // teams of a block: none idle while there are SMs without one
     const int64_t spread = (p.rows + kSms - 1) / kSms;
     const int teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(15, kMaxThreads / threads), spread)));
     const int block = teams * threads;
-    // resident blocks: by shared memory, and by the registers of this width (an estimate: more blocks than fit wait)
-    constexpr int kRegs = MODE == kSingle ? 128 : NV == 1 ? 64 : NV == 2 ? 96 : 128;
-    const int fit = std::max(1, std::min(kBytes ? 220 * 1024 / (kBytes * block + 1024) : 8, 65536 / (kRegs * block)));
+    // resident blocks: by shared memory, and by registers
+    const int fit = std::max(1, std::min(kBytes ? 220 * 1024 / (kBytes * block + 1024) : 8, 65536 / (forward_registers(NV, MODE) * block)));
     const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams, static_cast<int64_t>(kSms) * fit);
     const size_t smem = static_cast<size_t>(kBytes) * block;
     auto kernel = norm_forward_kernel<NV, MODE, XF32, YF32>;
