@@ -560,7 +560,7 @@ struct Team {
     Rows mode;
 };
 
-Team forward_team(int cols, bool aligned)
+Team forward_team(int cols, bool aligned, bool x_f32)
 {
     const int vecs = (cols + 7) / 8;
     if (!aligned) {                                    // the next row takes registers as well
@@ -568,12 +568,16 @@ Team forward_team(int cols, bool aligned)
         if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kSingle};
         return {4, round32((vecs + 3) / 4), kSingle};
     }
-    // few warps exchange a narrow row quickly (1536 columns: 9.9 us with two, 13.6 us with three); a wide row needs
-    // them to hide each other's latencies (5120: 32.3 us with ten, 35.3 us with five)
-    for (int nv = vecs > 256 ? 2 : 4; nv >= 1; --nv)
-        if (vecs % (32 * nv) == 0 && vecs / nv <= kMaxThreads) return {nv, vecs / nv, kFull};
+    // Widths whose rows go in pairs first: three vectors where x is bf16 and the row narrow (fewer warps exchange: 768
+    // columns 7.2 us, 11.5 with one; 1536: 8.1, 9.0 with two), two otherwise (1536 fp32: 11.9 us, 17.8 with three and
+    // rows one by one; 2048: 10.5, 12.2 with four; 5120 before pairs: 32.3 with two, 35.3 with four).
+    const int order[2][3] = {{3, 2, 1}, {2, 3, 1}};
+    for (int nv : order[x_f32])
+        if (vecs % (32 * nv) == 0 && vecs / nv <= kMaxThreads && (nv < 3 || vecs <= 256)) return {nv, vecs / nv, kFull};
     if (vecs <= 32) return {1, 32, kVector};
     if (vecs <= 64) return {2, 32, kVector};
+    if (vecs <= 128) return {4, 32, kVector};          // one warp exchanges nothing (640: 8.6 us, 11.5 in pairs with two)
+    if (vecs <= 1024) return {2, round32((vecs + 1) / 2), kVector};
     return {4, round32((vecs + 3) / 4), kVector};
 }
 
@@ -661,12 +665,12 @@ int norm_backward_slices(int64_t rows, int64_t rows_per_group, int cols, bool al
 
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s)
 {
-    const Team tm = forward_team(p.cols, p.aligned);
+    const Team tm = forward_team(p.cols, p.aligned, p.x_f32);
     switch (tm.nv) {
     case 1: return SDV2_NORM(forward, 1);
     case 2: return SDV2_NORM(forward, 2);
     case 3: return SDV2_NORM_TYPES(forward, 3, kFull);
-    default: return SDV2_NORM(forward, 4);
+    default: return tm.mode == kVector ? SDV2_NORM_TYPES(forward, 4, kVector) : SDV2_NORM_TYPES(forward, 4, kSingle);
     }
 }
 
