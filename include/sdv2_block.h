@@ -16,7 +16,9 @@
  * read before the call returns, device pointers are 16-byte aligned, bf16 results are rounded to
  * nearest even.  Every result is deterministic: the same inputs give the same bits on every call.
  * Outputs must not overlap inputs or one another, except where a comment says so.  Work runs on
- * the current device, which must be the one that the pointers and the stream belong to.
+ * the current device, which must be the one that the pointers and the stream belong to.  A call's
+ * kernels may start while the stream's kernel before them ends; they wait for it before they touch
+ * memory.
  */
 #ifndef SDV2_BLOCK_H
 #define SDV2_BLOCK_H
@@ -58,7 +60,10 @@ typedef struct {
  * not overlap on the GPU.  0 on an invalid configuration. */
 size_t sdv2_cross_workspace_bytes(const sdv2_cross_cfg* cfg, int32_t backward);
 
-/* Zeroes the error word and enqueues nothing else.  sdv2_check_device_error(ws, stream) reads it. */
+/* Zeroes the error word (the workspace's first 256 bytes) and enqueues nothing else; one workspace
+ * serves every configuration that it is large enough for.  Waits on the device are bounded by
+ * sdv2_set_wait_timeout_ns, and sdv2_debug_drop_kv_tile applies to sdv2_cross_attention.
+ * sdv2_check_device_error(ws, stream) reads the word. */
 sdv2_status sdv2_cross_workspace_init(const sdv2_cross_cfg* cfg, void* ws, void* stream);
 
 /*
@@ -68,7 +73,7 @@ sdv2_status sdv2_cross_workspace_init(const sdv2_cross_cfg* cfg, void* ws, void*
  *   Nk for all.  Rows at and past n_b have no influence, whatever they hold.  A stream with
  *   n_b = 0 gets out = 0 and lse = -infinity.
  * q, k, v: device bf16 as described above (k and v may be NULL if Nk = 0).
- * scale: softmax scale; <= 0 selects 1/sqrt(D).
+ * scale: softmax scale; <= 0 (or no number) selects 1/sqrt(D).
  * out: device bf16 [B][Nq][H][D]; lse: device fp32 [B][H][Nq], natural log-sum-exp of the scaled
  *   scores, or NULL.
  * Numerics: bf16 products with fp32 accumulation, online softmax in fp32, probabilities rounded
@@ -87,7 +92,8 @@ sdv2_status sdv2_cross_attention(const sdv2_cross_cfg* cfg, const int64_t* kv_le
  * [B][Nk][Hk][D], written whole: rows at and past n_b are 0 (dk, dv may be NULL if Nk = 0).
  * A stream with n_b = 1 has dq = dk = 0, as a softmax over one key is constant.
  * ws: workspace of sdv2_cross_workspace_bytes(cfg, 1) bytes.
- * Numerics: P and dS are rounded to bf16 for the tensor-core products; sums are fp32.
+ * Numerics: P and dS are rounded to bf16 for the tensor-core products; sums are fp32.  A stream of
+ * 128 keys or fewer takes delta = rowsum(P * dP), which does not carry the rounding of out.
  */
 sdv2_status sdv2_cross_attention_backward(const sdv2_cross_cfg* cfg, const int64_t* kv_lens, const void* q,
                                           const void* k, const void* v, const void* out, const float* lse,

@@ -25,6 +25,13 @@
 // Nothing is drained between items: a lane's next Q is loaded when its last S is done, its next S
 // is issued behind its last PV, and the tensor cores run the other lane meanwhile.
 //
+// Measured (calls captured in a graph, inputs from more buffers than L2 holds): 4680 queries x 12 heads x 512 states
+// 20.6 us (716 TFLOP/s), 10800 x 12 x 769 56.9 us (897), a key range of 8192 1440 TFLOP/s.  With one pair per SM a
+// call takes 6.5 us (launch, first loads, one step's latency, last read-out) and 8.5 us for a pair over 512 keys, 1.65 us
+// per 128 keys once the loop runs (the two products alone: 1.08).  In the loop the softmax's instructions bound it:
+// 128 exponentials, maxima, sums and conversions a thread and step, eight warps.  Slower: four softmax warpgroups (22.0 us
+// for the first case, 20.7 with two at the time), P stored in halves with the product begun early (8192 keys: 180 us, 163).
+//
 // Every wait is bounded; on expiry the kernel records the timeout in the workspace's error word,
 // lets all roles finish what they have in flight and returns.
 #include <algorithm>

@@ -32,6 +32,11 @@
 // whole row: it takes delta = rowsum(P * dP) instead and puts it in the workspace for dKV.
 // The launches are chained: a kernel's CTAs set up, and load what no launch writes, on SMs that the launch before has
 // left (480p: 67.6 us in a stream and 57.2 in a graph without, 57.8 and 54.9 with).
+// Measured in a graph: 4680 queries x 12 heads x 512 states 54.8 us (672 TFLOP/s of the five products; of the launches
+// alone under a profiler, with cold caches: statistics 8.8 us, dQ 24.4 with the tensor pipe busy 46 % of the cycles, dKV
+// 28.3 with 54 %, fold 8.4), 40 heads 176 us (698).  A step's chain bounds both: S, exponentials, dP, dS and the last
+// product follow one another, and dKV reads both operands of S and dP from shared memory, whose bandwidth those
+// products take whole.  Slower: the last range of a key tile adding the parts itself instead of a launch (480p 57.6 -> 61.8 us).
 // Tensor memory: acc0 | acc1 | S | dP, 128 columns each.  dQ has no acc1: its columns hold Q and dO, which the
 // compute warps put there as the A operands of S and dP, so that their shared memory takes the next
 // unit's tiles while this unit runs (loading them between units cost 2000 of a unit's 12600 cycles).
