@@ -59,6 +59,8 @@ class StreamSession:
         B, nk, hk, D = k.shape
         if B != c.batch:
             raise ValueError("k and v hold %d streams, the session %d" % (B, c.batch))
+        if B > 1 and k.stride(0) == 0:
+            raise ValueError("streams that share a prompt need a copy of it each")
         # a dimension of size one has no stride to speak of
         tok = k.stride(1) if nk > 1 else 0
         hd = k.stride(2) if hk > 1 else 0

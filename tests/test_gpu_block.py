@@ -583,6 +583,10 @@ def test_session_runs_a_layer_with_norms_and_a_prompt():
     y, z = (torch.empty((B, cfg.nq, C), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     with pytest.raises(ValueError, match="no prompt"):
         sess.cross_step(0, y.view(B, cfg.nq, H, D))
+    one = torch.zeros((1, 5, H, D), dtype=torch.bfloat16, device="cuda")
+    for k in (one, one.expand(B, -1, -1, -1), one.expand(B, -1, -1, -1).repeat(1, 1, 1, 2)[..., ::2]):
+        with pytest.raises(ValueError):
+            sess.set_prompt(0, k, k)
     for chunk in range(2):
         x = f32(B, cfg.nq, C)
         sess.norm_step(x, y, scale, shift, modulated=True)
