@@ -541,6 +541,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 fetch_unit(nx);
             }
             // ------------------------------------------------------------ read out the accumulators
+            if (DKV && u.steps == 0 && p.splits == 1) {            // rows behind the stream's last are zero
+                // not through R0 and R1, which may hold the next unit; a half-warp a row (a thread a row: 3 us a unit)
+                const int64_t first = (static_cast<int64_t>(u.b) * p.Nk + u.tile * BM) * p.Hk + u.head;
+                const int rows = min(BM, p.Nk - u.tile * BM);
+                for (int i = threadIdx.x; i < rows * 16; i += COMPUTE) {
+                    const int64_t at = (first + static_cast<int64_t>(i >> 4) * p.Hk) * HD + (i & 15) * 8;
+                    *reinterpret_cast<uint4*>(p.dk + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(p.dv + at) = make_uint4(0, 0, 0, 0);
+                }
+                u = nx;
+                continue;
+            }
             if (u.steps > 0) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(ACCFULL), units & 1u, tmo, abort_flag));
                 ++units;
@@ -567,13 +579,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     w[e] = zero ? 0u : bf16_pair(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
-                if (DKV && u.steps == 0) {                         // rows behind the stream's last: R may hold the next unit
-                    uint16_t* dst = (acc == 0 ? p.dk : p.dv) + ((static_cast<int64_t>(u.b) * p.Nk + u.tile * BM + row) * p.Hk + u.head) * HD + quarter * 32;
-                    if (u.tile * BM + row < p.Nk)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
-                    continue;
-                }
                 if (!DKV) {
                     if (leader) tma_store_wait_read();             // the output tile is free
                     compute_barrier();
