@@ -231,8 +231,11 @@ struct Ring {
     }
 };
 
-// Rows copied ahead: up to 192 bytes a thread.
-constexpr int stages(int bytes_per_row) { return bytes_per_row <= 32 ? 6 : bytes_per_row <= 48 ? 4 : bytes_per_row <= 64 ? 3 : 2; }
+// Rows copied ahead: up to 384 bytes a thread, of at most 512 threads (the widest rows of two fp32 tensors have 256 each).
+constexpr int stages(int bytes_per_row)
+{
+    return bytes_per_row <= 32 ? 6 : bytes_per_row <= 48 ? 4 : bytes_per_row <= 64 ? 3 : bytes_per_row <= 192 ? 2 : 1;
+}
 // In the forward pass, which takes rows in pairs where registers hold two: up to 256 bytes.
 constexpr int forward_stages(int bytes_per_row) { return bytes_per_row <= 32 ? 6 : bytes_per_row <= 64 ? 4 : 2; }
 // Threads that the kernel is compiled for, which caps its registers: by them the launch counts the blocks of an SM.

@@ -418,7 +418,9 @@ NORMS = [dict(rows=1, cols=1), dict(rows=1, cols=1536), dict(rows=3, cols=7, xt=
          dict(rows=5, cols=16383), dict(rows=40, cols=640, xpad=8, ypad=16, gpad=24, per=13),
          dict(rows=40, cols=640, xpad=3, ypad=0, per=13), dict(rows=40, cols=96, ypad=5, gpad=1, per=40),
          dict(rows=2000, cols=64, per=1), dict(rows=999, cols=128, per=333, offset=30.0, xt="f32"),
-         dict(rows=1500, cols=1536, offset=-8.0)]
+         dict(rows=1500, cols=1536, offset=-8.0), dict(rows=700, cols=16384, xt="f32", yt="f32", per=300),
+         dict(rows=330, cols=15000, xt="f32", yt="f32"), dict(rows=340, cols=8192, xt="f32", yt="f32", plus_one=True),
+         dict(rows=2500, cols=640, per=700, plus_one=True), dict(rows=2501, cols=768, xt="f32"), dict(rows=1801, cols=1024)]
 
 
 @pytest.mark.parametrize("case", NORMS, ids=lambda c: "-".join("%s%s" % i for i in c.items()))
