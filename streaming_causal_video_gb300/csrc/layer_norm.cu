@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(forward_bound(NV, MODE)) norm_forward_kernel(c
     constexpr bool VECTOR = MODE != kSingle;
     constexpr int C = columns(XF32, YF32), N = NV * 8 / C;
     constexpr int S = forward_stages(NV * 16 * (XF32 ? 2 : 1)), R = forward_rows(NV, MODE, XF32);
+    constexpr bool EARLY = !VECTOR || NV == 1;
     extern __shared__ __align__(16) uint8_t copied[];
     __shared__ float scratch[2][2][R * kMaxThreads / 32];
     const int team = blockDim.x, t = threadIdx.x;
@@ -309,7 +310,9 @@ __global__ void __launch_bounds__(forward_bound(NV, MODE)) norm_forward_kernel(c
     };
 #pragma unroll 1
     for (; row < p.rows; row += R * step) {
-        if constexpr (!VECTOR) parameters(row);        // in front of the sums: 14.0 us, 15.0 behind them (3001 x 1001)
+        // A short row's time is one latency after the other, so that they are loaded in front of the sums (72 x 256: 1.8 us,
+        // 2.0 behind; 3001 x 1001: 14.0, 15.0); others have the registers for the row then (4680 x 5120: 27.3 us, 24.8 behind).
+        if constexpr (EARLY) parameters(row);
         uint64_t v[R][NV * 4];
         if constexpr (VECTOR) {
             copy_wait<S - R>();
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(forward_bound(NV, MODE)) norm_forward_kernel(c
                 if (p.mean) p.mean[r] = mean[k];
                 if (p.rstd) p.rstd[r] = rstd;
             }
-            if constexpr (VECTOR) parameters(r);
+            if constexpr (!EARLY) parameters(r);
             const uint64_t rstd2 = both(rstd);
             for_vectors<N, C, MODE>(team, t, p.cols, [&](int i, int c, int n) {
                 uint64_t y[C / 2];
