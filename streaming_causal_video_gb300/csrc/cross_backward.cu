@@ -25,6 +25,11 @@
 // the next step's S: with two slots of each, a dKV step waited about 1500 cycles for its load.  Seven
 // tiles fit; the third T0 slot takes the place of an output tile in dKV (its read-out goes through R0
 // and R1, once for many steps), and of the second T1 slot in dQ (V is only needed for dP).
+// What orders the reads of a slot before its next copy: -lse lies in the T0 slot, which is released behind DSFULL, after
+// every read of it.  The T1 slot is released earlier, by the product behind SREAD, and its -delta is read later, when dS
+// is formed: it has a barrier of its own (DFREE), at which the MMA warp arrives once DSFULL of the step is through.  The
+// load of dO goes ahead of it, the 512 bytes of -delta wait for it.  T1FULL completes with both copies, so that it cannot
+// go round again before every compute thread is past it.
 // A first kernel leaves -lse (log2 units) and -delta of every query tile's 128 rows side by side in the
 // workspace, so that dKV copies them with the tiles.  O is at hand in bf16 only, and its rounding reaches every dS
 // of the row through delta; the fewer keys, the less of it averages out (three keys, two queries: 0.005 of dQ, where
@@ -64,8 +69,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 8;
 
-enum Bar { RFULL, REMPTY, T0FULL, T0EMPTY = T0FULL + T0ST, T1FULL = T0EMPTY + T0ST, T1EMPTY = T1FULL + 2, SFULL = T1EMPTY + 2,
-           SREAD, DPFULL, DSFULL, ACCFULL, RREADY, MMADONE, NBARS };
+enum Bar { RFULL, REMPTY, T0FULL, T0EMPTY = T0FULL + T0ST, T1FULL = T0EMPTY + T0ST, T1EMPTY = T1FULL + 2, DFREE = T1EMPTY + 2,
+           SFULL = DFREE + 2, SREAD, DPFULL, DSFULL, ACCFULL, RREADY, MMADONE, NBARS };
 
 constexpr uint32_t SMEM_TILES = 7 * TILE;                      // R0 R1, T0 slots, T1 slots, dQ: an output tile
 constexpr uint32_t SMEM_STATS = (T0ST + 2) * BM * 4;           // dKV: -lse per T0 slot, -delta per T1 slot
@@ -263,6 +268,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                     if constexpr (DKV) {
                         mbar_arrive_expect_tx(bar(full + slot), query_bytes + BM * 4);
                         load_queries(t0 ? &p.qmap : &p.domap, dst, full + slot, h0, tile * p.tokens, u.b);
+                        // copied even when the wait runs out, so that the phase that dO has begun completes
+                        if (!t0 && !mbar_wait_bounded(bar(DFREE + slot), phase ^ 1u, tmo, abort_flag)) ok = false;
                         bulk_load(stat_ring + slot * BM * 4, stat, BM * 4, bar(full + slot));
                         stat += 2 * BM;        // the packs of a key head follow one another
                         if (++tile == p.qtiles) {
@@ -274,6 +281,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                         load_keys(t0 ? &p.kmap[u.b] : &p.vmap[u.b], dst, full + slot, hk, i * BM);
                     }
                     pending = (pending & ~(17u << slot)) | (1u << slot) | (phase << (slot + 4));
+                    if (!ok) break;
                     if (++slot == nst) {
                         slot = 0;
                         phase ^= 1u;
@@ -360,7 +368,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 if constexpr (DKV) {
                     accumulate(ACC1, SCOL, sT1 + a_slot1 * TILE, i > 0);         // dV += P^T dO
                     mma_commit_warp(bar(T1EMPTY + a_slot1));
-                    if (++a_slot1 == T1ST) a_slot1 = 0;
                 }
                 if (more) {
                     begin_s();
@@ -371,6 +378,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 accumulate(ACC0, XCOL, sT0 + a_slot0 * TILE, i > 0);             // dQ += dS K, dK += dS^T Q
                 mma_commit_warp(bar(T0EMPTY + a_slot0));
                 if (++a_slot0 == T0ST) a_slot0 = 0;
+                if constexpr (DKV) {
+                    mbar_arrive_warp(bar(DFREE + a_slot1));                      // every thread has read the step's -delta
+                    if (++a_slot1 == T1ST) a_slot1 = 0;
+                }
                 if (!more) mma_commit_warp(bar(ACCFULL));
                 else begin_dp();
             }
