@@ -186,10 +186,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         asm volatile("bar.sync 2, 128;" ::: "memory");
     } else {
         // Rows of a query tile that no load writes (the pack does not divide 128) are zero: as streamed tiles
-        // they are summed over, with probability 0.
-        for (int i = threadIdx.x; i < (BM - used_rows) * 16 * 7; i += COMPUTE) {
+        // they are summed over, with probability 0.  Only the tiles that queries go to: key tiles are loaded
+        // whole, by warps that do not wait for this.
+        constexpr int kFirst = DKV ? 2 : 0, kTiles = DKV ? T0ST + 2 : 2;
+        for (int i = threadIdx.x; i < (BM - used_rows) * 16 * kTiles; i += COMPUTE) {
             const int part = i & 15, r = i >> 4, tile = r / (BM - used_rows), row = used_rows + r - tile * (BM - used_rows);
-            *reinterpret_cast<uint4*>(smem + tile * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + (kFirst + tile) * TILE + (part >> 3) * HALF + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
     }

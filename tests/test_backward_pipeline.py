@@ -179,3 +179,17 @@ def test_the_kernel_waits_and_arrives_as_the_model_does():
                      r"bulk_load\(", SOURCE)
     body = SOURCE[SOURCE.index("if (!wait(DSFULL, count & 1u)) break;"):]
     assert "mbar_arrive_warp(bar(DFREE + a_slot1));" in body[:body.index("ACCFULL")]
+
+
+@pytest.mark.parametrize("dkv", [True, False])
+def test_rows_that_are_zeroed_at_the_start_belong_to_query_tiles(dkv):
+    """A block's compute warps zero the rows of query tiles that no load writes.  Nothing orders that with the loads,
+    which write the other rows of those tiles, and whole tiles of keys."""
+    assert re.search(r"sT0 = sR \+ 2 \* TILE, sT1 = sT0 \+ T0ST \* TILE;", SOURCE)
+    t0, t1 = rings()
+    held, streamed = {0, 1}, set(range(2, 2 + t0 + (t1 if dkv else 1)))
+    queries = streamed if dkv else held
+    first, tiles = re.search(r"kFirst = DKV \? (\d+) : (\d+), kTiles = DKV \? T0ST \+ (\d+) : (\d+);", SOURCE).group(
+        *((1, 3) if dkv else (2, 4)))
+    assert "i < (BM - used_rows) * 16 * kTiles;" in SOURCE and "smem + (kFirst + tile) * TILE +" in SOURCE
+    assert set(range(int(first), int(first) + int(tiles) + (t0 if dkv else 0))) == queries

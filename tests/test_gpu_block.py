@@ -190,6 +190,24 @@ def test_cross_attention_of_scores_far_below_zero(nq, nk, lens):
     c.check_backward()
 
 
+@pytest.mark.parametrize("heads,kv_heads,nq,nk", [(3, 1, 60, 128), (10, 2, 40, 300), (7, 1, 100, 256), (100, 1, 3, 384)])
+def test_gradients_where_heads_do_not_fill_a_tile_and_the_last_rows_of_key_tiles_matter(heads, kv_heads, nq, nk):
+    """Heads that share a key head in numbers that do not divide 128: a query tile has rows that no load writes, while
+    key tiles have all 128, the last of which hold nearly all the probability here."""
+    c = Cross(1, heads, kv_heads, nq, nk, [nk], seed=heads)
+    last = torch.arange(nk, device="cuda") % 128 >= 120
+    c.q.copy_((1.0 + 0.1 * c.q.float()))
+    c.k.copy_(torch.where(last[None, :, None, None], 0.5, -0.5) + 0.1 * c.k.float())
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    first = [t.clone() for t in (c.dq, c.dk, c.dv)]
+    for _ in range(10):
+        c.backward()
+        assert all(torch.equal(a, b) for a, b in zip(first, (c.dq, c.dk, c.dv)))
+
+
 @pytest.mark.parametrize("heads,kv_heads,nq,nk,lens", [(4, 4, 2, 3, [3]), (2, 2, 300, 3, [3, 2]), (6, 2, 9, 128, [128, 4, 127]),
                                                        (3, 1, 40, 600, [2, 600, 33])])
 def test_gradients_of_few_keys_do_not_carry_the_rounding_of_out(heads, kv_heads, nq, nk, lens):
