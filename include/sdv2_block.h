@@ -62,8 +62,10 @@ size_t sdv2_cross_workspace_bytes(const sdv2_cross_cfg* cfg, int32_t backward);
 
 /* Zeroes the error word (the workspace's first 256 bytes) and enqueues nothing else; one workspace
  * serves every configuration that it is large enough for.  Waits on the device are bounded by
- * sdv2_set_wait_timeout_ns, and sdv2_debug_drop_kv_tile applies to sdv2_cross_attention.
- * sdv2_check_device_error(ws, stream) reads the word. */
+ * sdv2_set_wait_timeout_ns; sdv2_check_device_error(ws, stream) reads the word.  With
+ * sdv2_debug_drop_kv_tile set, sdv2_cross_attention leaves out the copy of that key tile, and
+ * sdv2_cross_attention_backward, where dQ is formed, that of the key tile, and where dK and dV are
+ * formed, that of the query tile with this number. */
 sdv2_status sdv2_cross_workspace_init(const sdv2_cross_cfg* cfg, void* ws, void* stream);
 
 /*

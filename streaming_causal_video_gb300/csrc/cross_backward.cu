@@ -89,6 +89,7 @@ struct Params {
     float* part;                               // dKV: [split][unit][2][D/4][128][4]
     uint32_t* err;
     uint64_t timeout_ns;
+    int64_t drop_tile;                         // this streamed tile is not copied (-1: none), for tests of the waits
     int32_t B, H, Hk, Nq, Nk;
     int32_t pack, tokens, group;               // heads and tokens of a query tile, query heads of a key head
     int32_t qtiles, packs;                     // query tiles of a (stream, pack), packs of a stream
@@ -267,23 +268,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 for (int i = 0; i < u.steps; ++i) {
                     if (!mbar_wait_bounded(bar(empty + slot), phase ^ 1u, tmo, abort_flag)) { ok = false; break; }
                     const uint32_t dst = ring + slot * TILE;
+                    if ((DKV ? tile : i) != p.drop_tile) {
+                        if constexpr (DKV) {
+                            mbar_arrive_expect_tx(bar(full + slot), query_bytes + BM * 4);
+                            load_queries(t0 ? &p.qmap : &p.domap, dst, full + slot, h0, tile * p.tokens, u.b);
+                            // copied even when the wait runs out, so that the phase that dO has begun completes
+                            if (!t0 && !mbar_wait_bounded(bar(DFREE + slot), phase ^ 1u, tmo, abort_flag)) ok = false;
+                            bulk_load(stat_ring + slot * BM * 4, stat, BM * 4, bar(full + slot));
+                        } else {
+                            mbar_arrive_expect_tx(bar(full + slot), TILE);
+                            load_keys(t0 ? &p.kmap[u.b] : &p.vmap[u.b], dst, full + slot, hk, i * BM);
+                        }
+                        pending = (pending & ~(17u << slot)) | (1u << slot) | (phase << (slot + 4));
+                        if (!ok) break;
+                    }
                     if constexpr (DKV) {
-                        mbar_arrive_expect_tx(bar(full + slot), query_bytes + BM * 4);
-                        load_queries(t0 ? &p.qmap : &p.domap, dst, full + slot, h0, tile * p.tokens, u.b);
-                        // copied even when the wait runs out, so that the phase that dO has begun completes
-                        if (!t0 && !mbar_wait_bounded(bar(DFREE + slot), phase ^ 1u, tmo, abort_flag)) ok = false;
-                        bulk_load(stat_ring + slot * BM * 4, stat, BM * 4, bar(full + slot));
                         stat += 2 * BM;        // the packs of a key head follow one another
                         if (++tile == p.qtiles) {
                             tile = 0;
                             h0 += p.pack;
                         }
-                    } else {
-                        mbar_arrive_expect_tx(bar(full + slot), TILE);
-                        load_keys(t0 ? &p.kmap[u.b] : &p.vmap[u.b], dst, full + slot, hk, i * BM);
                     }
-                    pending = (pending & ~(17u << slot)) | (1u << slot) | (phase << (slot + 4));
-                    if (!ok) break;
                     if (++slot == nst) {
                         slot = 0;
                         phase ^= 1u;
@@ -413,10 +418,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         int slot0 = 0, slot1 = 0;              // dKV: T slots of the step
         uint32_t phase0 = 0, phase1 = 0;
         uint32_t resident = 0;                 // dQ: units whose Q and dO went to tensor memory
+        // Every lane takes part in the vote over a wait's outcome, which leaves `ok` the same in all of a warp: tensor-memory
+        // loads are warp-collective, and a lane that went past a vote alone would leave the others there.
+        auto all = [&](bool here) { return __all_sync(0xffffffffu, here); };
+        auto arrived = [&](int i, uint32_t parity) { return mbar_wait_bounded(bar(i), parity, tmo, abort_flag); };
         auto put_resident = [&](const Unit& v) {
             if constexpr (!DKV) {
                 if (v.steps == 0) return;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(RFULL), resident & 1u, tmo, abort_flag));
+                ok = all(ok && arrived(RFULL, resident & 1u));
                 ++resident;
                 tc_fence_after();
 #pragma unroll
@@ -456,8 +465,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             for (int i = 0; i < u.steps; ++i, ++count) {
                 const float* cl = reinterpret_cast<const float*>(smem + SMEM_TILES) + slot0 * BM + quarter * 32;
                 const float* cd = reinterpret_cast<const float*>(smem + SMEM_TILES) + (T0ST + slot1) * BM + quarter * 32;
-                if constexpr (DKV) ok = ok && mbar_wait_bounded(bar(T0FULL + slot0), phase0, tmo, abort_flag);
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(SFULL), count & 1u, tmo, abort_flag));
+                ok = all(ok && (!DKV || arrived(T0FULL + slot0, phase0)) && arrived(SFULL, count & 1u));
                 tc_fence_after();
                 const uint64_t sl2x2 = f32x2_pack(p.scale_log2, p.scale_log2);
                 uint64_t pr[16];                                   // P, two columns each
@@ -493,8 +501,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                         for (int e = 0; e < 16; ++e)
                             pr[e] = 2 * e >= keys ? 0 : 2 * e + 1 >= keys ? pr[e] & 0xFFFFFFFFu : pr[e];
                 }
-                if constexpr (DKV) ok = ok && mbar_wait_bounded(bar(T1FULL + slot1), phase1, tmo, abort_flag);
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(DPFULL), count & 1u, tmo, abort_flag));
+                ok = all(ok && (!DKV || arrived(T1FULL + slot1, phase1)) && arrived(DPFULL, count & 1u));
                 if (!ok) give_up(abort_flag, p.err);
                 tc_fence_after();
                 if constexpr (!DKV)
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 continue;
             }
             if (u.steps > 0) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar(ACCFULL), units & 1u, tmo, abort_flag));
+                ok = all(ok && arrived(ACCFULL, units & 1u));
                 ++units;
                 tc_fence_after();
             }
@@ -821,6 +828,7 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     p.dv = f.dv;
     p.err = c.err;
     p.timeout_ns = c.timeout_ns;
+    p.drop_tile = debug_drop_tile();
     p.B = c.B;
     p.H = c.H;
     p.Hk = c.Hk;

@@ -349,6 +349,30 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
         case.check_forward()
 
 
+@pytest.mark.parametrize("shape", [(1, 2, 2, 300, 100), (2, 6, 2, 700, 500), (2, 40, 40, 300, 300)],
+                         ids=["dkv", "both", "many units"])
+def test_waits_of_the_backward_pass_that_run_out_are_reported_and_the_next_call_is_right(shape):
+    """The copy of one streamed tile is left out: key tile 1 for dQ, query tile 1 for dK and dV."""
+    B, H, Hk, nq, nk = shape
+    c = Cross(B, H, Hk, nq, nk, [nk] * B, seed=8)
+    c.forward()
+    try:
+        sd.set_wait_timeout_ns(50_000_000)
+        sd.debug_drop_kv_tile(1)
+        c.backward()
+        with pytest.raises(sd.SDV2Error) as e:
+            sd.check_device_error(c.ws)
+        assert e.value.status == 4
+    finally:
+        sd.debug_drop_kv_tile(-1)
+        sd.set_wait_timeout_ns(2_000_000_000)
+    refs, tols = cross_backward_reference(c.q, c.k, c.v, c.dout, c.lens, c.real_scale)
+    if nk <= 128:                              # the other launch had no such tile
+        within(c.dq, refs[0], tols[0], "dq")
+    c.backward()
+    c.check_backward()
+
+
 def test_cross_gradients_against_differences():
     """<gradient, direction> against central differences of the 64-bit forward."""
     c = Cross(1, 2, 1, 150, 200, [200], seed=31)
