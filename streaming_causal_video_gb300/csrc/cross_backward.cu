@@ -36,7 +36,9 @@
 // the roundings of P, dS and dQ come to 0.0024).  With one key tile (128 keys or fewer) the dQ launch has the
 // whole row: it takes delta = rowsum(P * dP) instead and puts it in the workspace for dKV.
 // The launches are chained: a kernel's CTAs set up, and load what no launch writes, on SMs that the launch before has
-// left (480p: 67.6 us in a stream and 57.2 in a graph without, 57.8 and 54.9 with).
+// left (480p: 67.6 us in a stream and 57.2 in a graph without, 57.8 and 54.9 with).  dKV may be there as long as dQ
+// runs, so that its roles wait for dQ's end before their first bounded wait for one another: the limit is for what a
+// block waits of itself, not for the launch before.
 // Measured in a graph: 4680 queries x 12 heads x 512 states 54.8 us (672 TFLOP/s of the five products; of the launches
 // alone under a profiler, with cold caches: statistics 8.8 us, dQ 24.4 with the tensor pipe busy 46 % of the cycles, dKV
 // 28.3 with 54 %, fold 8.4), 40 heads 176 us (698).  A step's chain bounds both: S, exponentials, dP, dS and the last
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                     load_queries(&p.domap, sR + TILE, RFULL, u.head, u.tile * p.tokens, u.b);
                 }
                 ++units;
+                if (DKV && units == 1) wait_for_launch_before();
             }
             if (!ok) give_up(abort_flag, p.err);
             volatile int never = 0;            // every copy lands before the CTA may exit
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
                 p_ph ^= 1u;
             }
         };
+        if constexpr (DKV) wait_for_launch_before();
         while (ok && walk.next(p, u)) {
             if (u.steps == 0) continue;
             // the unit before has read its last S and written its last dS, so both score tiles are free
@@ -450,6 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
         };
         bool has = walk.next(p, u);
         if constexpr (!DKV) wait_for_launch_before();              // the statistics
+        bool waited = false;                                       // dKV: rows behind a stream's last need not wait
         if (has) {
             fetch_unit(u);
             put_resident(u);
@@ -458,6 +463,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_backward_kernel(const __gri
             Unit nx;                           // decoded here, not between the last step and the read-out
             const bool more_units = walk.next(p, nx);
             const bool constant = DKV && p.n[u.b] == 1;           // a softmax over one key has no gradient
+            if (DKV && u.steps > 0 && !waited) {
+                wait_for_launch_before();
+                waited = true;
+            }
             const uint64_t lse2 = f32x2_pack(row_lse, row_lse);
             uint64_t delta2 = f32x2_pack(row_delta, row_delta);
             // a thread whose wait ran out still runs through all steps, to meet the others at every barrier

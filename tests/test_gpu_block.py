@@ -349,8 +349,8 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
         case.check_forward()
 
 
-@pytest.mark.parametrize("shape", [(1, 2, 2, 300, 100), (2, 6, 2, 700, 500), (2, 40, 40, 300, 300)],
-                         ids=["dkv", "both", "many units"])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 300, 100), (1, 2, 2, 100, 300), (2, 6, 2, 700, 500), (2, 40, 40, 300, 300)],
+                         ids=["dkv", "dq", "both", "many units"])
 def test_waits_of_the_backward_pass_that_run_out_are_reported_and_the_next_call_is_right(shape):
     """The copy of one streamed tile is left out: key tile 1 for dQ, query tile 1 for dK and dV."""
     B, H, Hk, nq, nk = shape
@@ -369,6 +369,9 @@ def test_waits_of_the_backward_pass_that_run_out_are_reported_and_the_next_call_
     refs, tols = cross_backward_reference(c.q, c.k, c.v, c.dout, c.lens, c.real_scale)
     if nk <= 128:                              # the other launch had no such tile
         within(c.dq, refs[0], tols[0], "dq")
+    if nq <= 128:                              # and does not count dQ's wait as its own
+        within(c.dk, refs[1], tols[1], "dk")
+        within(c.dv, refs[2], tols[2], "dv")
     c.backward()
     c.check_backward()
 
