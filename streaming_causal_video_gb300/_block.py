@@ -67,16 +67,17 @@ class NormConfig(_Config):
                 ("eps", _f32)]
 
     def _derive(self):
-        """Shape, strides, type and bytes of x and of y; bytes of the parameters, of their
-        gradients, of a value per row, and of the workspace."""
+        """Shape, strides, type and bytes of x and of y; shape, stride and bytes of the parameters;
+        bytes of their gradients, of a value per row, and of the workspace."""
         def operand(dtype, stride):
             kind, size = _TYPE.get(dtype, (None, 4))
             stride = stride or self.cols
             return (self.rows, self.cols), (stride, 1), kind, _b._row_span(self.rows, stride, self.cols, size)
         per = self.rows_per_group or self.rows
         groups = (self.rows + per - 1) // per if per > 0 else 0
+        stride = self.group_stride or self.cols
         return (operand(self.x_dtype, self.x_row_stride), operand(self.y_dtype, self.y_row_stride),
-                _b._row_span(groups, self.group_stride or self.cols, self.cols, 4), groups * self.cols * 4, self.rows * 4,
+                ((groups, self.cols), stride, _b._row_span(groups, stride, self.cols, 4)), groups * self.cols * 4, self.rows * 4,
                 norm_workspace_bytes(self))
 
 
@@ -145,15 +146,40 @@ class _Operands:
         return _b._dev(t, name, nbytes)
 
     def view(self, t, name, dtype, shape, strides, nbytes):
-        """A view of the configuration's rank must have its shape and strides; a tensor of another rank is a
-        buffer that they are applied to."""
-        if t is not None and type(t) is not int and t.dim() == len(shape):
-            if t.shape != shape:
-                raise ValueError("%s is %s, the configuration says %s" % (name, tuple(t.shape), shape))
-            have = t.stride()
-            if have != strides and any(n > 1 and h != w for n, h, w in zip(shape, have, strides)):
-                raise ValueError("%s has strides %s, the configuration says %s" % (name, have, strides))
+        """A view of the configuration's rank must have its shape and strides; a contiguous tensor of another rank
+        is a buffer that they are applied to, and any other has to have them when it is seen in that shape."""
+        if t is not None and type(t) is not int:
+            if t.dim() == len(shape):
+                if t.shape != shape:
+                    raise ValueError("%s is %s, the configuration says %s" % (name, tuple(t.shape), shape))
+                _check_strides(t, name, shape, strides)
+            elif not t.is_contiguous():
+                _check_strides(_seen_as(t, name, shape), name, shape, strides)
         return self(t, name, dtype, nbytes)
+
+    def parameters(self, t, name, shape, stride, nbytes):
+        """fp32 rows of shape (groups, cols), `stride` apart.  Two-dimensional parameters must have that stride (rows
+        behind the last group may follow); a contiguous tensor of another shape is a buffer."""
+        p = self(t, name, _FP, nbytes)
+        if t is not None and type(t) is not int and not (stride == shape[1] and t.is_contiguous()):
+            if t.dim() == 2 and t.shape[1] == shape[1] and t.shape[0] >= shape[0]:
+                _check_strides(t, name, shape, (stride, 1))
+            elif not t.is_contiguous():
+                _check_strides(_seen_as(t, name, shape), name, shape, (stride, 1))
+        return p
+
+
+def _check_strides(t, name, shape, strides):
+    have = t.stride()
+    if have != strides and any(n > 1 and h != w for n, h, w in zip(shape, have, strides)):
+        raise ValueError("%s has strides %s, the configuration says %s" % (name, have, strides))
+
+
+def _seen_as(t, name, shape):
+    try:
+        return t.view(shape)
+    except RuntimeError:
+        raise ValueError("%s (%s, strides %s) must be contiguous or a view of %s" % (name, tuple(t.shape), t.stride(), shape)) from None
 
 
 _BF, _FP, _U8 = torch.bfloat16, torch.float32, torch.uint8
@@ -211,8 +237,8 @@ def layer_norm(cfg, x, y, weight=None, bias=None, mean=None, rstd=None, stream=N
     apart; mean, rstd: fp32 [rows], written for the backward pass."""
     op = _Operands()
     (shape, xs, xt, xb), (_, ys, yt, yb), par, _, stats, _ = cfg.derived()
-    status = _lib().sdv2_layer_norm(ctypes.byref(cfg), op.view(x, "x", xt, shape, xs, xb), op(weight, "weight", _FP, par),
-                                    op(bias, "bias", _FP, par), op.view(y, "y", yt, shape, ys, yb),
+    status = _lib().sdv2_layer_norm(ctypes.byref(cfg), op.view(x, "x", xt, shape, xs, xb),
+                                    op.parameters(weight, "weight", *par), op.parameters(bias, "bias", *par), op.view(y, "y", yt, shape, ys, yb),
                                     op(mean, "mean", _FP, stats, True), op(rstd, "rstd", _FP, stats, True), _stream(stream))
     if status:
         _b._check(status, "sdv2_layer_norm")
@@ -224,7 +250,7 @@ def layer_norm_backward(cfg, dy, x, mean, rstd, dx, ws, weight=None, dweight=Non
     op = _Operands()
     (shape, xs, xt, xb), (_, ys, yt, yb), par, grads, stats, scratch = cfg.derived()
     status = _lib().sdv2_layer_norm_backward(
-        ctypes.byref(cfg), op.view(dy, "dy", yt, shape, ys, yb), op.view(x, "x", xt, shape, xs, xb), op(weight, "weight", _FP, par),
+        ctypes.byref(cfg), op.view(dy, "dy", yt, shape, ys, yb), op.view(x, "x", xt, shape, xs, xb), op.parameters(weight, "weight", *par),
         op(mean, "mean", _FP, stats, True), op(rstd, "rstd", _FP, stats, True), op.view(dx, "dx", xt, shape, xs, xb),
         op(dweight, "dweight", _FP, grads, True), op(dbias, "dbias", _FP, grads, True),
         op(ws, "ws", _U8, scratch if (dweight is not None or dbias is not None) else 0), _stream(stream))

@@ -212,3 +212,69 @@ def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
                          ((x, y), dict(weight=w, mean=FakeTensor((5,), torch.float32)), "mean: ")):
         with pytest.raises(ValueError, match=match):
             sd.layer_norm(n, *a, stream=0, **kw)
+
+
+def reached(call):
+    """The call passes the binding's checks and reaches the library's device check (no GPU here) or its own checks."""
+    try:
+        call()
+    except sd.SDV2Error as e:
+        assert e.status in (2, 3), e
+    return True
+
+
+def wide(shape, strides, dtype=torch.float32):
+    return FakeTensor(shape, dtype, strides=strides)
+
+
+@pytest.mark.parametrize("name", ["weight", "bias"])
+def test_binding_refuses_parameters_with_other_strides(monkeypatch, name):
+    """A modulation's scale and shift are slices of one tensor: read as if they were dense they would be other rows."""
+    monkeypatch.setattr(_block, "_current_device", lambda: 0)
+    monkeypatch.setattr(_block, "_raw_stream", lambda device: 0)
+    x, y = FakeTensor((6, 40)), FakeTensor((6, 40))
+    ok = FakeTensor((3, 40), torch.float32)
+    stats = FakeTensor((6,), torch.float32)
+    ws = FakeTensor((1 << 16,), torch.uint8)
+
+    def calls(c, t):
+        yield lambda: sd.layer_norm(c, x, y, **{name: t})
+        if name == "weight":
+            yield lambda: sd.layer_norm_backward(c, y, x, stats, stats, FakeTensor((6, 40)), ws, weight=t)
+    dense, spaced = norm(rows_per_group=2), norm(rows_per_group=2, group_stride=240)
+    for c, t in ((dense, wide((3, 40), (240, 1))), (dense, wide((3, 40), (1, 3))), (dense, wide((3, 40), (80, 2))),
+                 (dense, wide((1, 3, 40), (1, 240, 1))), (dense, wide((4, 40), (240, 1))), (dense, wide((40, 3), (3, 2))),
+                 (spaced, wide((3, 40), (80, 1))), (spaced, wide((3, 40, 2), (240, 2, 1))),
+                 (norm(), wide((40,), (2,))), (norm(), wide((1, 40), (80, 2)))):
+        t._t = torch.empty(4096).as_strided(t._t.shape, t._t.stride())       # long enough for any reading
+        for call in calls(c, t):
+            with pytest.raises(ValueError, match=name):
+                call()
+    if not torch.cuda.is_available():
+        for c, t in ((dense, ok), (dense, FakeTensor((120,), torch.float32)), (dense, FakeTensor((5, 40), torch.float32)),
+                     (spaced, wide((3, 40), (240, 1))), (spaced, wide((1, 3, 40), (720, 240, 1))), (spaced, wide((4, 40), (240, 1))),
+                     (spaced, FakeTensor((3, 240), torch.float32)), (spaced, FakeTensor((3, 6, 40), torch.float32)),
+                     (norm(), FakeTensor((40,), torch.float32)), (norm(), wide((1, 40), (999, 1)))):
+            for call in calls(c, t):
+                assert reached(call)
+
+
+def test_binding_refuses_operands_of_another_rank_with_other_strides(monkeypatch):
+    """A packed projection's slice in three dimensions is no dense [B][Nq][H][128]."""
+    monkeypatch.setattr(_block, "_current_device", lambda: 0)
+    monkeypatch.setattr(_block, "_raw_stream", lambda device: 0)
+    q, kv, out = FakeTensor((2, 5, 4, 128)), FakeTensor((2, 7, 2, 128)), FakeTensor((2, 5, 4, 128))
+    ws = FakeTensor((256,), torch.uint8)
+    packed = FakeTensor((2, 5, 512), strides=(5 * 1536, 1536, 1))
+    for bad in (packed, FakeTensor((10, 512), strides=(1, 10)), FakeTensor((5120,), strides=(2,))):
+        with pytest.raises(ValueError, match="q "):
+            sd.cross_attention(cross(), bad, kv, kv, out, ws)
+    y = FakeTensor((6, 40))
+    for bad in (FakeTensor((2, 3, 40), strides=(144, 48, 1)), FakeTensor((2, 3, 40), strides=(200, 40, 1))):
+        with pytest.raises(ValueError, match="x "):
+            sd.layer_norm(norm(), bad, y)
+    if not torch.cuda.is_available():
+        assert reached(lambda: sd.cross_attention(cross(q_token_stride=1536), packed, kv, kv, out, ws))
+        assert reached(lambda: sd.cross_attention(cross(), FakeTensor((10, 512)), kv, kv, out, ws))
+        assert reached(lambda: sd.layer_norm(norm(x_row_stride=48), FakeTensor((2, 3, 40), strides=(144, 48, 1)), y))
+        assert reached(lambda: sd.layer_norm(norm(x_row_stride=48), FakeTensor((6 * 48,)), y))
