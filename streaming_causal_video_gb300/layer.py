@@ -86,14 +86,35 @@ class StreamSession:
 
     def norm_step(self, x, out, weight=None, bias=None, modulated=False, eps=1e-6, stream=None):
         """Layer norm of a chunk's tokens x [B][Nq][C] (bf16 or fp32) into out [B][Nq][C].  weight, bias fp32: [C], the
-        learned affine; or, modulated, [B*F][C], the scale and shift of every latent frame: xhat * (1 + weight) + bias."""
+        learned affine; or, modulated, [B*F][C], the scale and shift of every latent frame: xhat * (1 + weight) + bias.
+        Those may be slices of one modulation tensor such as [B*F][6][C] (of the same one, as they share a stride)."""
         kinds = {torch.bfloat16: block.BF16, torch.float32: block.F32}
         if x.dtype not in kinds or out.dtype not in kinds:
             raise ValueError("x and out must be bf16 or fp32")
         if x.shape != out.shape or not x.is_contiguous() or not out.is_contiguous():
             raise ValueError("x and out must be contiguous and of one shape")
-        cfg = block.NormConfig.make(rows=x.numel() // x.shape[-1], cols=x.shape[-1], x_dtype=kinds[x.dtype],
-                                    y_dtype=kinds[out.dtype], weight_plus_one=int(modulated),
-                                    rows_per_group=self.cfg.hw if modulated else 0, eps=eps)
+        C = x.shape[-1]
+        rows = x.numel() // C
+        groups = -(-rows // self.cfg.hw) if modulated else 1
+        strides = set()
+
+        def by_group(t, name):
+            if t is None or isinstance(t, int):
+                return t
+            if t.shape[-1:] != (C,) or t.numel() != groups * C:
+                raise ValueError("%s is %s, not [%d][%d]" % (name, tuple(t.shape), groups, C))
+            try:
+                t = t.view(groups, C)
+            except RuntimeError:
+                raise ValueError("%s (strides %s) has no stride between its rows" % (name, t.stride())) from None
+            if groups > 1:
+                strides.add(t.stride(0))
+            return t
+        weight, bias = by_group(weight, "weight"), by_group(bias, "bias")
+        if len(strides) > 1 or any(n < C for n in strides):
+            raise ValueError("weight and bias must have one stride between rows, of at least %d, not %s" % (C, sorted(strides)))
+        cfg = block.NormConfig.make(rows=rows, cols=C, x_dtype=kinds[x.dtype], y_dtype=kinds[out.dtype],
+                                    weight_plus_one=int(modulated), rows_per_group=self.cfg.hw if modulated else 0,
+                                    group_stride=strides.pop() if strides else 0, eps=eps)
         block.layer_norm(cfg, x, out, weight=weight, bias=bias, stream=stream)
         return out

@@ -278,3 +278,38 @@ def test_binding_refuses_operands_of_another_rank_with_other_strides(monkeypatch
         assert reached(lambda: sd.cross_attention(cross(), FakeTensor((10, 512)), kv, kv, out, ws))
         assert reached(lambda: sd.layer_norm(norm(x_row_stride=48), FakeTensor((2, 3, 40), strides=(144, 48, 1)), y))
         assert reached(lambda: sd.layer_norm(norm(x_row_stride=48), FakeTensor((6 * 48,)), y))
+
+
+def test_norm_step_takes_the_parameters_stride_and_refuses_other_shapes(monkeypatch):
+    sess = sd.StreamSession.__new__(sd.StreamSession)        # its configuration only: nothing is allocated or launched
+    sess.cfg = sd.StreamConfig.make(batch=2, heads=2, head_dim=128, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=4,
+                                    grid_w=6, chunk_frames=3, sink_frames=3, window_frames=4, refresh_chunks=0, qkv_token_stride=0)
+    C, groups = 256, 6
+    x = torch.zeros(2, sess.cfg.nq, C)
+    y = torch.zeros(2, sess.cfg.nq, C, dtype=torch.bfloat16)
+    seen = []
+    monkeypatch.setattr(_block, "layer_norm", lambda cfg, x, y, weight=None, bias=None, stream=None: seen.append((cfg, weight, bias)))
+    mod = torch.arange(groups * 6 * C, dtype=torch.float32).view(groups, 6, C)
+    halves = mod.view(groups, 6 * C)[:, :2 * C].chunk(2, -1)
+    frames = mod.view(2, 3, 6, C)
+    for w, b, stride in ((mod[:, 1], mod[:, 0], 6 * C), (*halves, 6 * C), (frames[:, :, 2], frames[:, :, 5], 6 * C),
+                         (mod[:, 1].contiguous(), None, C), (None, mod[:, 3], 6 * C), (mod[:, 1].contiguous().view(2, 3, C), None, C)):
+        assert sess.norm_step(x, y, w, b, modulated=True) is y
+        cfg, gw, gb = seen.pop()
+        assert (cfg.rows, cfg.cols, cfg.rows_per_group, cfg.weight_plus_one, cfg.group_stride) == (2 * sess.cfg.nq, C, 24, 1, stride)
+        for given, got in ((w, gw), (b, gb)):
+            assert given is None and got is None or (torch.equal(got, given.reshape(groups, C)) and got.data_ptr() == given.data_ptr())
+    sess.norm_step(x, y, mod[0, 0], mod[:1, 1])
+    cfg, gw, gb = seen.pop()
+    assert (cfg.rows_per_group, cfg.weight_plus_one, cfg.group_stride) == (0, 0, 0) and torch.equal(gw[0], mod[0, 0])
+    sess.norm_step(x, y)
+    assert seen.pop()[1:] == (None, None)
+    whole = mod[:, 0].contiguous()
+    for args, modulated in (((whole, whole), False),                    # one row is used: the others would be lost
+                            ((whole[:1], whole[:1]), True), ((whole[0], None), True), ((mod[0, 0].expand(groups, C), None), True),
+                            ((whole, mod[:, 1]), True), ((mod[:, 1], whole), True), ((None, whole[:, :128]), True),
+                            ((whole.t().contiguous().t(), None), True), ((whole.view(C, groups), None), True),
+                            ((frames[:, :2, 0].expand(2, 2, C)[:, :, ::2], None), True)):
+        with pytest.raises(ValueError):
+            sess.norm_step(x, y, *args, modulated=modulated)
+    assert not seen

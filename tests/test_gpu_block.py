@@ -659,6 +659,23 @@ def test_session_runs_a_layer_with_norms_and_a_prompt():
         within(lse, lse_ref, lse_tol, "lse")
 
 
+def test_norm_step_reads_scale_and_shift_out_of_one_modulation_tensor():
+    B, F, C = 2, 3, 384
+    cfg = sd.StreamConfig.make(batch=B, heads=C // D, head_dim=D, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=5, grid_w=7,
+                               chunk_frames=F, sink_frames=3, window_frames=4, refresh_chunks=0, qkv_token_stride=0)
+    sess = sd.StreamSession(cfg, 1, [0, 0], "cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((B, cfg.nq, C), generator=g, device="cuda")
+    y = torch.empty((B, cfg.nq, C), dtype=torch.bfloat16, device="cuda")
+    mod = 0.3 * torch.randn((B * F, 6, C), generator=g, device="cuda")
+    scale, shift = mod.view(B * F, 6 * C)[:, :2 * C].chunk(2, -1)
+    for w, b in ((mod[:, 1], mod[:, 4]), (scale, shift), (mod.view(B, F, 6, C)[:, :, 5], mod.view(B, F, 6, C)[:, :, 3])):
+        y.fill_(float("nan"))
+        sess.norm_step(x, y, w, b, modulated=True)
+        refs, tols = norm_reference(x.view(-1, C), w.reshape(B * F, C), b.reshape(B * F, C), cfg.hw, 1e-6, True, BF)
+        within(y.view(-1, C), refs[0], tols[0], "modulated norm")
+
+
 FIRST_CALLS = """
 import sys, torch
 sys.path.insert(0, sys.argv[1])
