@@ -1,5 +1,6 @@
 """GPU tests of cross attention and layer norm, forward and backward, against plain 64-bit
 implementations with derived bounds (block_common.py)."""
+import ctypes
 import math
 import subprocess
 import sys
@@ -537,6 +538,23 @@ def test_layer_norm_is_deterministic_and_replays_from_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(first, (n.y, n.dx, n.dweight, n.dbias)):
             assert torch.equal(a, b)
+
+
+def test_layer_norm_backward_does_not_report_or_clear_an_error_of_another_part():
+    """An error that its owner has not asked for yet; calls whose parameter gradients need no second kernel."""
+    n, one = Norm(64, 250, seed=1), Norm(4, 250, seed=2)
+    for m in (n, one):
+        m.forward()
+    dx = torch.empty_like(n.dx)
+    stream = torch.cuda.current_stream().cuda_stream
+    rt = ctypes.CDLL(next(l.split()[-1] for l in open("/proc/self/maps") if "libcudart" in l))
+    torch.cuda.synchronize()
+    left = rt.cudaSetDevice(4096)              # no such device: an error code, nothing else
+    assert left != 0 and rt.cudaPeekAtLastError() == left
+    sd.layer_norm_backward(n.cfg, n.dy, n.x, n.mean, n.rstd, dx, None, weight=n.weight, stream=stream)
+    one.backward(stream)
+    assert rt.cudaGetLastError() == left and rt.cudaGetLastError() == 0
+    one.check_backward()
 
 
 def test_layer_norm_writes_only_its_outputs():
