@@ -35,11 +35,11 @@
 // Every wait is bounded; on expiry the kernel records the timeout in the workspace's error word,
 // lets all roles finish what they have in flight and returns.
 #include <algorithm>
-#include <mutex>
 
 #include "chained.cuh"
 #include "cross_tma.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "ptx_pair.cuh"
 #include "softmax_tile.cuh"
 
@@ -637,34 +637,33 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 }
 
 // How many clusters of each size a device holds at once (a cluster lies within one of the GPU's processing
-// clusters, whose sizes differ: 152 SMs take 36 clusters of 4, but 23 of 6 and 7 of 16).  Asked once per device.
+// clusters, whose sizes differ: 152 SMs take 36 clusters of 4, but 23 of 6 and 7 of 16).
 struct Placement {
-    std::once_flag once;
-    cudaError_t error = cudaSuccess;
     int clusters[kMaxCluster + 1] = {};
     template <typename K>
-    cudaError_t prepare(K kernel)
+    cudaError_t ask(K kernel)
     {
-        std::call_once(once, [&]() {
-            error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-            if (error != cudaSuccess) return;
-            const bool wide = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-            for (int n = 2; n <= (wide ? kMaxCluster : 8); ++n) {
-                cudaLaunchConfig_t cfg{};
-                cfg.gridDim = dim3(static_cast<unsigned>(n));
-                cfg.blockDim = dim3(NTHREADS);
-                cfg.dynamicSmemBytes = SMEM_BYTES;
-                cudaLaunchAttribute attr{};
-                attr.id = cudaLaunchAttributeClusterDimension;
-                attr.val.clusterDim.x = static_cast<unsigned>(n);
-                attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-                cfg.attrs = &attr;
-                cfg.numAttrs = 1;
-                if (cudaOccupancyMaxActiveClusters(&clusters[n], kernel, &cfg) != cudaSuccess) clusters[n] = 0;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (int n = 2; e == cudaSuccess && n <= kMaxCluster; ++n) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(n));
+            cfg.blockDim = dim3(NTHREADS);
+            cfg.dynamicSmemBytes = SMEM_BYTES;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(n);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&clusters[n], kernel, &cfg);
+            if (e == cudaErrorInvalidClusterSize) {            // a size that the device does not take
+                cudaGetLastError();
+                clusters[n] = 0;
+                e = cudaSuccess;
             }
-            cudaGetLastError();                // a size that the device does not take is no error
-        });
-        return error;
+        }
+        return e;
     }
 };
 
@@ -704,12 +703,13 @@ cudaError_t launch(const CrossForward& f, int sms, cudaStream_t s)
     const int64_t tiles = static_cast<int64_t>(p.tiles) * (c.H / p.pack) * c.B;
     if (tiles > INT32_MAX / kMaxCluster) return cudaErrorInvalidConfiguration;
     auto kernel = cross_attention_kernel<CAP>;
+    static PerDevice asked;
     static Placement placements[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    const Placement& fit = placements[dev & 63];
-    const cudaError_t prepared = placements[dev & 63].prepare(kernel);
-    if (prepared != cudaSuccess) return prepared;
+    Placement& fit = placements[dev & 63];
+    const cudaError_t e = asked.run(dev, [&]() { return fit.ask(kernel); });
+    if (e != cudaSuccess) return e;
     // A cluster shares a tile's keys, as wide as all tiles' clusters fit at once and every CTA has a key tile.
     int splits = 1;
     for (int c = 2; least != 1 << 30 && c <= std::min(least, kMaxCluster); ++c)

@@ -48,11 +48,11 @@
 // compute warps put there as the A operands of S and dP, so that their shared memory takes the next
 // unit's tiles while this unit runs (loading them between units cost 2000 of a unit's 12600 cycles).
 #include <algorithm>
-#include <atomic>
 
 #include "chained.cuh"
 #include "cross_tma.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "softmax_tile.cuh"
 
 namespace sdv2 {
@@ -794,14 +794,13 @@ void cut(int32_t* start, int ctas, int64_t runs, int64_t units_per_run, F&& cost
 }
 
 template <typename K>
-cudaError_t prepare_kernel(K kernel, std::atomic<uint64_t>& done)
+cudaError_t prepare_kernel(K kernel, PerDevice& prepared)
 {
     int dev = 0;
     cudaGetDevice(&dev);
-    if (done.load() >> (dev & 63) & 1u) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-    if (e == cudaSuccess) done.fetch_or(uint64_t(1) << (dev & 63));
-    return e;
+    return prepared.run(dev, [&]() {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+    });
 }
 
 template <int CAP>
@@ -858,7 +857,7 @@ cudaError_t launch(const CrossBackward& f, cudaStream_t s)
     cudaError_t e = launch_chained(cross_stats_kernel, dim3(static_cast<unsigned>(qunits), 4), dim3(256), 0, s, f.out, f.dout, f.lse,
                                    f.stats, c.H, c.Nq, sh.pack, sh.tokens, sh.qtiles, sh.packs);
     if (e != cudaSuccess) return e;
-    static std::atomic<uint64_t> dq_set{0}, dkv_set{0};
+    static PerDevice dq_set, dkv_set;
     auto dq_kernel = cross_backward_kernel<false, CAP>;
     auto dkv_kernel = cross_backward_kernel<true, CAP>;
     if ((e = prepare_kernel(dq_kernel, dq_set)) != cudaSuccess || (e = prepare_kernel(dkv_kernel, dkv_set)) != cudaSuccess) return e;

@@ -6,6 +6,7 @@ import ctypes
 import os
 import pickle
 import re
+import subprocess
 
 import pytest
 import torch
@@ -313,3 +314,16 @@ def test_norm_step_takes_the_parameters_stride_and_refuses_other_shapes(monkeypa
         with pytest.raises(ValueError):
             sess.norm_step(x, y, *args, modulated=modulated)
     assert not seen
+
+
+def test_a_preparation_that_fails_is_tried_again(tmp_path):
+    """What a kernel needs once per device is kept only where it succeeded."""
+    exe = tmp_path / "per_device"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I",
+                    os.path.join(ROOT, "streaming_causal_video_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "c_abi", "per_device.cpp"), "-o", str(exe)], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0 and run.stdout == "ok\n", run.stdout
+    for name in ("cross_attention.cu", "cross_backward.cu"):
+        text = open(os.path.join(ROOT, "streaming_causal_video_gb300", "csrc", name)).read()
+        assert "call_once" not in text and "PerDevice" in text
