@@ -51,6 +51,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace sdv2 {
 namespace {
@@ -608,39 +609,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) chunk_attention_kernel(const __gr
 #undef BAR
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once; a function-local static is initialised by
-// exactly one thread, so concurrent first calls from several host threads are safe.
-EncodeTiledFn get_encode_tiled()
-{
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(ptr);
-        return nullptr;
-    }();
-    return fn;
-}
-
 // (D = 128 dims, rows, planes) bf16 tensor with row stride 256 bytes; boxes of 64 dims x 128 rows.
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t planes, int64_t plane_stride_bytes)
 {
-    EncodeTiledFn enc = get_encode_tiled();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(HD), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(planes)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(HD * 2), static_cast<cuuint64_t>(plane_stride_bytes)};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(BM), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tensor_map(map, base, 3, dims, strides, box);
 }
 
 }  // namespace

@@ -42,6 +42,7 @@
 #include "per_device.h"
 #include "ptx_pair.cuh"
 #include "softmax_tile.cuh"
+#include "tensor_map.h"
 
 namespace sdv2 {
 namespace {
@@ -602,40 +603,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_attention_kernel(const __gr
     }
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encoder()
-{
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(ptr);
-        return nullptr;
-    }();
-    return fn;
-}
-
-bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box)
-{
-    const EncodeTiledFn enc = encoder();
-    if (!enc) return false;
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    auto attempt = [&]() {
-        return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
-                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    if (attempt()) return true;
-    // a host thread whose first CUDA call this is has no context yet, which the driver's encoder does not make itself
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && attempt();
-}
-
 // How many clusters of each size a device holds at once (a cluster lies within one of the GPU's processing
 // clusters, whose sizes differ: 152 SMs take 36 clusters of 4, but 23 of 6 and 7 of 16).
 struct Placement {
@@ -758,7 +725,7 @@ bool encode_query_map(CUtensorMap* map, const void* base, int heads, int64_t tok
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.hd) * 2, static_cast<cuuint64_t>(st.tok) * 2,
                                    static_cast<cuuint64_t>(st.batch) * 2};
     const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads_box), static_cast<cuuint32_t>(tokens_box), 1};
-    return encode(map, base, 4, dims, strides, box);
+    return encode_tensor_map(map, base, 4, dims, strides, box);
 }
 
 bool encode_key_map(CUtensorMap* map, const void* base, int heads, int64_t rows, const CrossStrides& st)
@@ -766,7 +733,7 @@ bool encode_key_map(CUtensorMap* map, const void* base, int heads, int64_t rows,
     const cuuint64_t dims[3] = {HD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(st.hd) * 2, static_cast<cuuint64_t>(st.tok) * 2};
     const cuuint32_t box[3] = {64, 1, BN};
-    return encode(map, base, 3, dims, strides, box);
+    return encode_tensor_map(map, base, 3, dims, strides, box);
 }
 
 int cross_pack(int group)

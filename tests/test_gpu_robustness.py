@@ -1,5 +1,7 @@
 """Robustness of the CUDA path: checkpoint/resume of the stream state, guard bands around
 every buffer a call writes, and CUDA-graph capture of the per-layer calls."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -278,3 +280,47 @@ def test_undersized_or_offset_buffers_are_refused_on_the_host():
     torch.cuda.synchronize()
     sd.check_device_error(sess.ws)
     assert torch.isfinite(sess.out.float()).all()
+
+
+@pytest.mark.parametrize("first", ["projection", "attention", "cross"])
+def test_the_first_call_of_a_host_thread(first):
+    """A host thread that has made no CUDA call has no context yet, whichever operator it calls first."""
+    cfg = config(W)
+    H, C = W.heads, W.heads * 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    x, w = rand(W.batch, cfg.nq, C), rand(3 * C, C)
+    cross = sd.CrossConfig.make(batch=W.batch, heads=H, head_dim=128, q_len=cfg.nq, kv_len=90)
+    k, v, ws = rand(W.batch, 90, H, 128), rand(W.batch, 90, H, 128), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sess = [sd.StreamSession(cfg, 1, W.start_frames, "cuda") for _ in range(2)]
+    outs = [torch.zeros_like(s.out) for s in sess]
+    stream = torch.cuda.current_stream().cuda_stream
+    chunks = [0] * W.batch
+
+    def calls(s, out):
+        L = s.layers[0]
+        return {"projection": lambda: sd.qkv_rope_append(cfg, W.start_frames, chunks, x, w, s.q_rot, L.k, L.v, L.meta, s.ws,
+                                                         stream=stream),
+                "attention": lambda: sd.chunk_attention(cfg, chunks, s.q_rot, L.k, L.v, s.out, s.ws, stream=stream),
+                "cross": lambda: sd.cross_attention(cross, s.out, k, v, out, ws, stream=stream)}
+    here, there = calls(sess[0], outs[0]), calls(sess[1], outs[1])
+    failed = []
+
+    def thread(call):
+        try:
+            call()
+        except Exception as e:                 # noqa: BLE001  (reported below, in the test's own thread)
+            failed.append(e)
+    for name in here:
+        here[name]()
+        if name == first:
+            t = threading.Thread(target=thread, args=(there[name],))
+            t.start()
+            t.join()
+        else:
+            there[name]()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    np.testing.assert_array_equal(bits(sess[0].out), bits(sess[1].out))
+    np.testing.assert_array_equal(bits(outs[0]), bits(outs[1]))
+    assert bool(outs[0].float().abs().max() > 0)
