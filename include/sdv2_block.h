@@ -65,7 +65,9 @@ size_t sdv2_cross_workspace_bytes(const sdv2_cross_cfg* cfg, int32_t backward);
  * sdv2_set_wait_timeout_ns; sdv2_check_device_error(ws, stream) reads the word.  With
  * sdv2_debug_drop_kv_tile set, sdv2_cross_attention leaves out the copy of that key tile, and
  * sdv2_cross_attention_backward, where dQ is formed, that of the key tile, and where dK and dV are
- * formed, that of the query tile with this number. */
+ * formed, that of the query tile with this number.  It has no effect where no tiles are copied: on
+ * the forward pass of one or two query rows per key head (q_len * heads / kv_heads) whose streams
+ * have at most 1024 valid states. */
 sdv2_status sdv2_cross_workspace_init(const sdv2_cross_cfg* cfg, void* ws, void* stream);
 
 /*

@@ -350,6 +350,24 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
         case.check_forward()
 
 
+@pytest.mark.parametrize("H,Hk,nq,nk,waits", [(2, 2, 2, 1024, False), (4, 2, 1, 900, False), (2, 2, 2, 1025, True), (3, 1, 1, 900, True)])
+def test_a_tile_is_left_out_only_where_tiles_are_copied(H, Hk, nq, nk, waits):
+    c = Cross(1, H, Hk, nq, nk, [nk], seed=8, backward=False)
+    try:
+        sd.set_wait_timeout_ns(50_000_000)
+        sd.debug_drop_kv_tile(1)
+        c.forward()
+        if waits:
+            with pytest.raises(sd.SDV2Error):
+                sd.check_device_error(c.ws)
+    finally:
+        sd.debug_drop_kv_tile(-1)
+        sd.set_wait_timeout_ns(2_000_000_000)
+    if waits:
+        c.forward()
+    c.check_forward()
+
+
 @pytest.mark.parametrize("shape", [(1, 2, 2, 300, 100), (1, 2, 2, 100, 300), (2, 6, 2, 700, 500), (2, 40, 40, 300, 300)],
                          ids=["dkv", "dq", "both", "many units"])
 def test_waits_of_the_backward_pass_that_run_out_are_reported_and_the_next_call_is_right(shape):
