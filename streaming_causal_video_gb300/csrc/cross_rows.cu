@@ -74,10 +74,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     return v;
 }
 
-// grid.x = units * splits, clusters of `splits` CTAs; unit = ((b * Hk) + key head) * row blocks + block.
+// grid.x = units * splits, clusters of `splits` CTAs; unit = b * Hk + key head, whose rows are kRows.
 template <int kRows>
-__global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_constant__ CrossForward p, int splits,
-                                                                 int row_blocks)
+__global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_constant__ CrossForward p, int splits)
 {
     __shared__ float s_m[kHalves][kRows], s_l[kHalves][kRows];
     __shared__ float s_acc[kWarps][kRows][HD];
@@ -87,12 +86,9 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     // 32-bit divisions: a 64-bit one costs as much as a key
     const uint32_t unit = blockIdx.x / static_cast<uint32_t>(splits);
     const int split = static_cast<int>(blockIdx.x - unit * splits);
-    const uint32_t bh = unit / static_cast<uint32_t>(row_blocks);
-    const int b = static_cast<int>(bh / static_cast<uint32_t>(p.c.Hk));
-    const int hk = static_cast<int>(bh - b * p.c.Hk);
+    const int b = static_cast<int>(unit / static_cast<uint32_t>(p.c.Hk));
+    const int hk = static_cast<int>(unit - b * p.c.Hk);
     const int g = p.c.H / p.c.Hk;
-    const uint32_t rows = static_cast<uint32_t>(g) * p.c.Nq;               // the host keeps it below 2^31
-    const uint32_t row0 = (unit - bh * row_blocks) * kRows;
     const int n = p.c.n[b];
     const int j0 = static_cast<int>(static_cast<int64_t>(n) * split / splits);
     const int j1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits);
@@ -102,9 +98,8 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     Vec8 q[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const uint32_t row = row0 + r < rows ? row0 + r : rows - 1;      // rows past the end repeat the last
-        const int64_t i = row / static_cast<uint32_t>(g);
-        const int h = hk * g + static_cast<int>(row - i * g);
+        const int i = r / g;
+        const int h = hk * g + (r - i * g);
         q[r] = unpack8(load_vec(p.c.q + b * p.c.qs.batch + i * p.c.qs.tok + h * p.c.qs.hd + sub * 8));
     }
     const uint16_t* kb = p.c.k + b * p.c.kvs.batch + hk * p.c.kvs.hd + sub * 8;
@@ -212,8 +207,6 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
     // the CTAs of the cluster share the rows' dims; a thread's loads from all of them are under way together
     for (int i = split * kWarps * 32 + threadIdx.x; i < kRows * HD; i += splits * kWarps * 32) {
         const int r = i / HD, d = i - r * HD;
-        const uint32_t row = row0 + r;
-        if (row >= rows) continue;
         float mc[kMaxSplits], lc[kMaxSplits], ac[kMaxSplits];
 #pragma unroll
         for (int c = 0; c < kMaxSplits; ++c)
@@ -234,8 +227,8 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
                 sum += lc[c] * f;
                 a += ac[c] * f;
             }
-        const int64_t qi = row / static_cast<uint32_t>(g);
-        const int h = hk * g + static_cast<int>(row - qi * g);
+        const int qi = r / g;
+        const int h = hk * g + (r - qi * g);
         const float o = n == 0 ? 0.f : a / sum;
         reinterpret_cast<__nv_bfloat16*>(p.out)[((static_cast<int64_t>(b) * p.c.Nq + qi) * p.c.H + h) * HD + d] =
             __float2bfloat16_rn(o);
@@ -250,15 +243,12 @@ __global__ void __launch_bounds__(kWarps * 32) cross_rows_kernel(const __grid_co
 template <int kRows>
 static cudaError_t launch_rows(const CrossForward& p, cudaStream_t s)
 {
-    const int64_t rows = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq;
-    const int64_t row_blocks = (rows + kRows - 1) / kRows;
-    const int64_t units = row_blocks * p.c.B * p.c.Hk;
+    const int64_t units = static_cast<int64_t>(p.c.B) * p.c.Hk;
     int longest = 0;
     for (int b = 0; b < p.c.B; ++b) longest = std::max(longest, p.c.n[b]);
     // a key split holds at least one round of loads of its half-warps; split until the SMs are full
     int splits = 1;
     while (splits < kMaxSplits && units * splits < 304 && longest > splits * kHalves * kKeysAtOnce) splits *= 2;
-    if (rows > INT32_MAX || units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
     cfg.blockDim = dim3(kWarps * 32);
@@ -269,13 +259,13 @@ static cudaError_t launch_rows(const CrossForward& p, cudaStream_t s)
     attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, cross_rows_kernel<kRows>, p, splits, static_cast<int>(row_blocks));
+    return cudaLaunchKernelEx(&cfg, cross_rows_kernel<kRows>, p, splits);
 }
 
 cudaError_t launch_cross_rows(const CrossForward& p, cudaStream_t s)
 {
-    const int64_t rows = static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq;
-    return rows == 1 ? launch_rows<1>(p, s) : launch_rows<2>(p, s);
+    static_assert(kFewRows == 2, "a kernel for each number of rows");
+    return static_cast<int64_t>(p.c.H / p.c.Hk) * p.c.Nq == 1 ? launch_rows<1>(p, s) : launch_rows<2>(p, s);
 }
 
 }  // namespace sdv2
