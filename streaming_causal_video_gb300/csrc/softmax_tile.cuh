@@ -72,7 +72,9 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float sl2
             m = m_new;
         }
     }
-    const uint64_t sl2x2 = f32x2_pack(sl2, sl2), negm2 = f32x2_pack(-m, -m);
+    // scores that have all been -infinity so far (keys of the type's lowest value) leave a max of -infinity: 2^(x - 0) is 0
+    const float base = m == -INFINITY ? 0.f : m;
+    const uint64_t sl2x2 = f32x2_pack(sl2, sl2), negm2 = f32x2_pack(-base, -base);
     uint64_t sum4[4] = {0, 0, 0, 0};
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {

@@ -209,6 +209,29 @@ def test_gradients_where_heads_do_not_fill_a_tile_and_the_last_rows_of_key_tiles
         assert all(torch.equal(a, b) for a, b in zip(first, (c.dq, c.dk, c.dv)))
 
 
+@pytest.mark.parametrize("H,nq,nk,hidden", [(2, 1, 400, 200), (2, 2, 400, 200), (2, 3, 700, 128), (2, 3, 700, 560), (2, 150, 700, 300),
+                                            (2, 150, 128, 100), (40, 700, 300, 140), (40, 1000, 700, 520), (3, 300, 100, 60)])
+def test_keys_of_the_types_lowest_value_have_no_influence(H, nq, nk, hidden):
+    """Keys that a caller has hidden by the type's lowest value: their scores run over to -infinity, a row's whole first
+    key tile at once or one half of its keys.  The others' softmax is what is left, and no gradient reaches the hidden."""
+    c = Cross(1, H, H, nq, nk, [nk], seed=hidden)
+    c.q.copy_(c.q.abs() + 0.1)
+    c.k[:, :hidden] = torch.finfo(torch.bfloat16).min
+    c.forward()
+    rest = [t[:, hidden:] for t in (c.k, c.v)]
+    out, lse, tol, lse_tol = cross_reference(c.q, *rest, [nk - hidden], c.real_scale)
+    within(c.out, out, tol, "out")
+    within(c.lse, lse, lse_tol, "lse")
+    c.backward()
+    sd.check_device_error(c.ws)
+    assert (nk <= 128) == (nk - hidden <= 128)      # delta by the same rule for the rest alone
+    refs, tols = cross_backward_reference(c.q, *rest, c.dout, [nk - hidden], c.real_scale)
+    within(c.dq, refs[0], tols[0], "dq")
+    within(c.dk[:, hidden:], refs[1], tols[1], "dk")
+    within(c.dv[:, hidden:], refs[2], tols[2], "dv")
+    assert not c.dk[:, :hidden].any() and not c.dv[:, :hidden].any()
+
+
 @pytest.mark.parametrize("heads,kv_heads,nq,nk,lens", [(4, 4, 2, 3, [3]), (2, 2, 300, 3, [3, 2]), (6, 2, 9, 128, [128, 4, 127]),
                                                        (3, 1, 40, 600, [2, 600, 33])])
 def test_gradients_of_few_keys_do_not_carry_the_rounding_of_out(heads, kv_heads, nq, nk, lens):
