@@ -33,6 +33,7 @@
 
 #include "block.h"
 #include "chained.cuh"
+#include "per_device.h"
 #include "softmax_tile.cuh"
 
 namespace sdv2 {
@@ -612,11 +613,18 @@ int backward_teams(int cols, bool aligned) { return std::max(1, std::min(15, kMa
 // Blocks of the backward kernel that an SM holds, by its registers.
 int backward_blocks(int cols, bool aligned) { return aligned && backward_team(cols, aligned).nv == 1 ? 2 : 1; }
 
+// Dynamic shared memory that every kernel may take.  One limit, set once: it is the kernel's, not the launch's, and a
+// call that set its own size would take it from a launch that another host thread is about to make.
+constexpr size_t kMaxShared = 220 * 1024;
+
 template <typename K>
-cudaError_t allow_shared(K kernel, size_t bytes)
+cudaError_t allow_shared(K kernel, PerDevice& allowed)
 {
-    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes))
-                             : cudaSuccess;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return allowed.run(dev, [&]() {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxShared));
+    });
 }
 
 template <int NV, Rows MODE, bool XF32, bool YF32>
@@ -629,11 +637,12 @@ cudaError_t forward(const NormParams& p, int threads, cudaStream_t s)
     const int teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(15, kMaxThreads / threads), spread)));
     const int block = teams * threads;
     // resident blocks: by shared memory, and by registers
-    const int fit = std::max(1, std::min(kBytes ? 220 * 1024 / (kBytes * block + 1024) : 8, 65536 / (forward_registers(NV, MODE) * block)));
+    const int fit = std::max(1, std::min(kBytes ? static_cast<int>(kMaxShared) / (kBytes * block + 1024) : 8, 65536 / (forward_registers(NV, MODE) * block)));
     const int64_t grid = std::min<int64_t>((p.rows + teams - 1) / teams, static_cast<int64_t>(kSms) * fit);
     const size_t smem = static_cast<size_t>(kBytes) * block;
     auto kernel = norm_forward_kernel<NV, MODE, XF32, YF32>;
-    const cudaError_t e = allow_shared(kernel, smem);
+    static PerDevice allowed;
+    const cudaError_t e = allow_shared(kernel, allowed);
     if (e != cudaSuccess) return e;
     return launch_chained(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)),
                           smem, s, p);
@@ -649,7 +658,8 @@ cudaError_t backward(const NormParams& p, int threads, cudaStream_t s)
     const size_t sums = teams > 1 ? static_cast<size_t>(teams) * 2 * p.cols * sizeof(float) : 0;
     const size_t smem = std::max(sums, static_cast<size_t>(kBytes) * threads * teams);
     auto kernel = norm_backward_kernel<NV, MODE, XF32, YF32>;
-    const cudaError_t e = allow_shared(kernel, smem);
+    static PerDevice allowed;
+    const cudaError_t e = allow_shared(kernel, allowed);
     if (e != cudaSuccess) return e;
     return launch_chained(kernel, dim3(static_cast<unsigned>(groups * p.slices)),
                           dim3(static_cast<unsigned>(threads), static_cast<unsigned>(teams)), smem, s, p);

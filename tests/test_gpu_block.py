@@ -815,6 +815,38 @@ def test_calls_from_several_host_threads():
         assert all(torch.equal(getattr(c, n), getattr(w, n)) for n in ("out", "lse", "dq", "dk", "dv"))
 
 
+def test_norms_of_several_widths_from_several_host_threads():
+    """Widths that run in one kernel with different amounts of shared memory, called at the same time, past the binding
+    so that the calls meet inside the library."""
+    L = sd.lib()
+    wide, narrow = (lambda i: Norm(152, 8192, xt="f32", yt="f32", seed=i)), (lambda i: Norm(1000, 512, xt="f32", yt="f32", seed=i))
+    cases = [(wide, narrow)[i % 2](i) for i in range(8)]
+    for n in cases:
+        n.forward()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    failed = []
+
+    def body(n, s):
+        cfg, ptr = ctypes.byref(n.cfg), [t.data_ptr() for t in (n.x, n.weight, n.bias, n.y, n.mean, n.rstd, n.dy, n.dx, n.dweight, n.dbias, n.ws)]
+        x, w, b, y, mean, rstd, dy, dx, dw, db, ws = ptr
+        for _ in range(3000):
+            for status in (L.sdv2_layer_norm(cfg, x, w, b, y, mean, rstd, s.cuda_stream),
+                           L.sdv2_layer_norm_backward(cfg, dy, x, w, mean, rstd, dx, dw, db, ws, s.cuda_stream)):
+                if status:
+                    failed.append(L.sdv2_last_error())
+    threads = [threading.Thread(target=body, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), failed[0])
+    for n in cases:
+        n.check_forward()
+        n.check_backward()
+
+
 def test_results_follow_what_other_streams_and_copies_bring():
     """The launches start early and wait for what is before them: a kernel, a copy, a fill, another stream's event;
     eagerly and captured.  The inputs change right in front of every call, and the outputs are read right behind."""
