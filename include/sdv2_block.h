@@ -8,8 +8,10 @@
  * (learned weight and bias), and attends to the prompt:
  *   sdv2_layer_norm            y = (x - mean) / sqrt(var + eps), times a weight, plus a bias;
  *   sdv2_cross_attention       the chunk's queries attend to each stream's prompt states.
- * sdv2_layer_norm_backward and sdv2_cross_attention_backward give their gradients, so that what
- * the prompt passes through (adapters, prompt states, norms) can be trained.
+ * sdv2_layer_norm_backward and sdv2_cross_attention_backward give the gradients of these two, so
+ * that what the prompt passes through (adapters, prompt states, norms) can be trained.  The library
+ * has no gradient of the chunk attention, of RoPE or of the projections: a loss that has to pass
+ * through those needs the caller's own.
  *
  * The conventions of sdv2.h hold: the caller owns all device memory, work is enqueued on the
  * caller's stream, arguments are checked on the host before anything is launched, host arrays are

@@ -2,7 +2,7 @@
 //
 // The keys and values have to be read and there is next to nothing to multiply them with, so what counts
 // is the time until the first product, and a tile of 128 rows is mostly empty (12 heads, 512 states: one
-// row 5.2 us, two 6.1 us, against 8.9 us on the tensor cores; at 20000 states the tensor cores' deeper
+// row 4.7 us, two 5.9 us, against 8.9 us on the tensor cores; at 20000 states the tensor cores' deeper
 // loads win by far, 46 against 139 us).
 //
 // out = sum_j softmax_j(scale q.k_j) v_j in one pass over the keys.  The heads that share a key head and their

@@ -36,6 +36,9 @@ __device__ __forceinline__ void mask_columns(uint32_t (&r)[32], int valid)
 // One step of the online softmax: reads the scores at tS, writes P as packed bf16 over their first 64
 // columns, and rescales the row's accumulator at tO (128 columns) when the running max has to follow;
 // `first` says that there is none yet.  m and l are the row's running max (log2 units) and sum.
+// P is rounded to bf16 (by 2^-8 of itself at most) because the tensor cores take both operands of P V in one type, and
+// V is bf16; the sum is taken of the probabilities before that.  Against 64 bits the output is off by 0.0022 in the
+// 2-norm (4680 x 12 x 512), 0.0017 of which is its own rounding.
 // Warp-collective.  The row is read twice, for its max and for the exponentials, in loops that are kept
 // short: a prompt has few key tiles, and code that runs a few times costs more to fetch than to execute.
 // (1.3B 480p chunk, 512 states: 20.7 us; one unrolled pass over 128 registers 25.8 us, unrolled quarters
