@@ -26,6 +26,23 @@ class LayerCache:
         sd.cache_reset(cfg, self.k, self.v, self.meta, stream)
 
 
+def _rows_of(t, name, groups, cols):
+    """A norm's parameters as [groups][cols] and the stride between rows (0 where there is one row or none)."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    if t.dim() != 2 or t.shape[0] != groups or t.shape[1] != cols:
+        if t.shape[-1:] != (cols,) or t.numel() != groups * cols:
+            raise ValueError("%s is %s, not [%d][%d]" % (name, tuple(t.shape), groups, cols))
+        try:
+            t = t.view(groups, cols)
+        except RuntimeError:
+            raise ValueError("%s (strides %s) has no stride between its rows" % (name, t.stride())) from None
+    stride = t.stride(0) if groups > 1 else 0
+    if groups > 1 and stride < cols:
+        raise ValueError("%s has a stride of %d between rows of %d" % (name, stride, cols))
+    return t, stride
+
+
 class StreamSession:
     def __init__(self, cfg: sd.StreamConfig, layers: int, start_frames, device="cuda", stream=None):
         self.cfg = cfg
@@ -38,6 +55,7 @@ class StreamSession:
         self.out = torch.empty((B, nq, H, D), dtype=torch.bfloat16, device=device)
         self.prompts = [None] * layers
         self.cross_ws = None
+        self.norms = {}                # norm_step's configurations, which follow from shapes, types and strides
 
     def layer_step(self, layer: int, chunk_index, q, k, v, out=None, lse=None, stream=None):
         """Causal-RoPE + cache append, then chunk attention, for one layer.  q, k, v: [B][Nq][H][D]."""
@@ -96,25 +114,15 @@ class StreamSession:
         C = x.shape[-1]
         rows = x.numel() // C
         groups = -(-rows // self.cfg.hw) if modulated else 1
-        strides = set()
-
-        def by_group(t, name):
-            if t is None or isinstance(t, int):
-                return t
-            if t.shape[-1:] != (C,) or t.numel() != groups * C:
-                raise ValueError("%s is %s, not [%d][%d]" % (name, tuple(t.shape), groups, C))
-            try:
-                t = t.view(groups, C)
-            except RuntimeError:
-                raise ValueError("%s (strides %s) has no stride between its rows" % (name, t.stride())) from None
-            if groups > 1:
-                strides.add(t.stride(0))
-            return t
-        weight, bias = by_group(weight, "weight"), by_group(bias, "bias")
-        if len(strides) > 1 or any(n < C for n in strides):
-            raise ValueError("weight and bias must have one stride between rows, of at least %d, not %s" % (C, sorted(strides)))
-        cfg = block.NormConfig.make(rows=rows, cols=C, x_dtype=kinds[x.dtype], y_dtype=kinds[out.dtype],
-                                    weight_plus_one=int(modulated), rows_per_group=self.cfg.hw if modulated else 0,
-                                    group_stride=strides.pop() if strides else 0, eps=eps)
+        weight, stride = _rows_of(weight, "weight", groups, C)
+        bias, bias_stride = _rows_of(bias, "bias", groups, C)
+        if stride and bias_stride and stride != bias_stride:
+            raise ValueError("weight and bias must have one stride between rows, not %d and %d" % (stride, bias_stride))
+        key = (rows, C, x.dtype, out.dtype, modulated, stride or bias_stride, eps)
+        cfg = self.norms.get(key)
+        if cfg is None:
+            cfg = self.norms[key] = block.NormConfig.make(
+                rows=rows, cols=C, x_dtype=kinds[x.dtype], y_dtype=kinds[out.dtype], weight_plus_one=int(modulated),
+                rows_per_group=self.cfg.hw if modulated else 0, group_stride=stride or bias_stride, eps=eps)
         block.layer_norm(cfg, x, out, weight=weight, bias=bias, stream=stream)
         return out

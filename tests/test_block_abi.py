@@ -285,6 +285,7 @@ def test_norm_step_takes_the_parameters_stride_and_refuses_other_shapes(monkeypa
     sess = sd.StreamSession.__new__(sd.StreamSession)        # its configuration only: nothing is allocated or launched
     sess.cfg = sd.StreamConfig.make(batch=2, heads=2, head_dim=128, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=4,
                                     grid_w=6, chunk_frames=3, sink_frames=3, window_frames=4, refresh_chunks=0, qkv_token_stride=0)
+    sess.norms = {}
     C, groups = 256, 6
     x = torch.zeros(2, sess.cfg.nq, C)
     y = torch.zeros(2, sess.cfg.nq, C, dtype=torch.bfloat16)
