@@ -47,4 +47,21 @@ from ._block import (  # noqa: F401
     layer_norm_backward,
     norm_workspace_bytes,
 )
+from ._project import (  # noqa: F401
+    GELU,
+    NO_ACTIVATION,
+    AxesRopeConfig,
+    Mx4Config,
+    Mx4ProductConfig,
+    RopeStrides,
+    axes_rope,
+    axes_rope_backward,
+    mx4_codes_bytes,
+    mx4_dequantize,
+    mx4_product,
+    mx4_quantize,
+    mx4_scales_bytes,
+    mx4_workspace_bytes,
+    mx4_workspace_init,
+)
 from .layer import LayerCache, StreamSession  # noqa: F401

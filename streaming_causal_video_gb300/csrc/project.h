@@ -1,0 +1,91 @@
+// Launch parameters and launchers of the operators in sdv2_project.h (not installed).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "../../include/sdv2_project.h"
+
+namespace sdv2 {
+
+// ---- microscaled 4-bit matrices -----------------------------------------------------------------
+
+constexpr int kMx4Block = 32;              // numbers that share a scale
+constexpr int kMx4Tile = 128;              // rows and columns of a scale tile: 512 bytes [row % 32][row / 32][block]
+constexpr int kMx4TileBytes = 64;          // bytes of a row's codes in a tile
+
+struct Mx4Params {
+    const void* x;                         // quantize: read; null otherwise
+    void* y;                               // dequantize: written
+    uint8_t* codes;                        // [rows][64 * tiles]
+    uint8_t* scales;                       // [row tiles][tiles][32][4][4]
+    int64_t rows, cols, stride;            // of the 4-bit matrix; elements between rows of x or y
+    int32_t tiles;                         // ceil(cols / 128)
+    int32_t f32;                           // x or y is fp32, else bf16
+    int32_t vectors;                       // rows of x or y begin on 16 bytes
+};
+
+cudaError_t launch_mx4_quantize(const Mx4Params& p, bool transposed, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const Mx4Params& p, cudaStream_t s);
+
+struct Mx4Product {
+    const uint8_t* a;                      // codes and scales of a: M rows, tiles * 128 columns
+    const uint8_t* as;
+    const uint8_t* b;                      // of b: N rows
+    const uint8_t* bs;
+    const float* bias;                     // [N] or null
+    void* out;
+    float* part;                           // partial sums [splits][M][part_stride], when the depth is split
+    int64_t M, N, out_stride;
+    int32_t tiles;                         // ceil(K / 128)
+    int32_t out_f32, gelu;
+    uint32_t* err;                         // device error word
+    uint64_t timeout_ns;
+    int64_t drop;                          // fault injection: 256-column step whose copies are left out, or -1
+};
+
+constexpr int kMx4FewRows = 8;             // rows of a that go to launch_mx4_rows
+
+// Few rows of a on the CUDA cores.
+cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s);
+
+// Parts that the depth of a product is cut into, and the elements between rows of their partial sums.
+int mx4_splits(int64_t M, int64_t N, int tiles);
+inline int64_t mx4_part_stride(int64_t N) { return (N + 3) / 4 * 4; }
+
+cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t s);
+
+// ---- rotary positions -----------------------------------------------------------------------------
+
+constexpr int kRopePairs = 128;            // head_dim 256
+
+struct RopePair {
+    uint64_t turn;                         // turns for a step of the position, as a 64-bit fraction of one
+    int16_t u, v;                          // dims of the pair
+    int16_t axis;                          // or -1: stays as it is
+    int16_t pad;
+};
+
+struct RopeTensor {
+    const void* in;
+    void* out;
+    sdv2_rope_strides is, os;
+};
+
+struct AxesRopeParams {
+    RopeTensor t[2];                       // q and k
+    const int32_t* positions;
+    int64_t tokens;
+    int32_t batch, heads, kv_heads, axes;
+    int32_t shared;                        // one row of positions for all of the batch
+    int32_t items;                         // threads for one row of heads
+    int32_t per;                           // heads (of q, then k) that a thread turns
+    RopePair pair[kRopePairs];
+};
+
+// The way a thread takes pairs: one vector of adjacent pairs, the vectors of the two halves, or one pair.
+enum class RopeLayout { adjacent, halves, single };
+
+cudaError_t launch_axes_rope(AxesRopeParams& p, RopeLayout layout, bool f32, int head_dim, cudaStream_t s);
+
+}  // namespace sdv2

@@ -1,0 +1,70 @@
+// Inline-PTX spellings for products of microscaled 4-bit matrices by CTA pairs.  Each function is one instruction, issued by
+// an elected lane of a converged warp where its name says so.
+#pragma once
+#include <cuda.h>
+#include <cstdint>
+
+namespace sdv2 {
+
+// Instruction descriptor of kind::mxf4: A and B e2m1 (1, at bits 7 and 10), scales ue8m0 (bit 23), N/8 at bit 17, M/128 at bit
+// 27; `half` selects the upper two of the four scale bytes that a tensor-memory cell holds (ids 0 or 2 at bits 4 and 29).
+__host__ __device__ constexpr uint32_t idesc_mx4(int M, int N, int half)
+{
+    return (static_cast<uint32_t>(2 * half) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(2 * half) << 29);
+}
+
+// Shared-memory descriptor of 128 rows' scales for 128 columns (512 bytes, no swizzle): 8 rows of 16 bytes lie 128 bytes
+// behind the 8 before them.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Copies those scales from each CTA's shared memory to four columns of its own tensor memory, for each of its four lane
+// quarters.  Products issued by the same thread behind it read what it wrote.
+__device__ __forceinline__ void scales_to_tmem_pair_warp(uint32_t taddr, uint64_t desc)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc)
+        : "memory");
+}
+
+// D (+)= A * B, 64 columns, over the pair; a_scales and b_scales are tensor-memory addresses in both CTAs.
+__device__ __forceinline__ void mma_mx4_pair_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t a_scales, uint32_t b_scales, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+}
+
+// Bytes that a barrier of this CTA was told to expect and that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, int32_t v)
+{
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// Box from shared memory to global memory; rows and columns past the tensor's end are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1, int32_t c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+}  // namespace sdv2

@@ -29,12 +29,18 @@ EncodeTiledFn encoder()
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                        const cuuint32_t* box)
 {
+    return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, map, base, rank, dims, strides, box);
+}
+
+bool encode_tensor_map_of(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, CUtensorMap* map, const void* base, int rank,
+                          const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box)
+{
     const EncodeTiledFn enc = encoder();
     if (!enc) return false;
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     auto attempt = [&]() {
-        return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
-                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
+                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (attempt()) return true;

@@ -1,4 +1,4 @@
-// Tensor maps of bf16 operands for TMA copies.
+// Tensor maps of operands for TMA copies.
 #pragma once
 #include <cuda.h>
 
@@ -8,5 +8,9 @@ namespace sdv2 {
 // all but the innermost in bytes, and the box that a copy brings.  Elements outside the tensor arrive as zeros.
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                        const cuuint32_t* box);
+
+// The same for elements of another type, with or without the swizzle.
+bool encode_tensor_map_of(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, CUtensorMap* map, const void* base, int rank,
+                          const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
 
 }  // namespace sdv2

@@ -1,0 +1,133 @@
+"""Plain implementations of 4-bit matrices, their products and rotary positions, with the error bounds that the kernels'
+roundings allow, for the tests of those operators.
+
+Bounds:
+* quantisation and values are exact: they are compared for equality;
+* a rounding is off by at most half a step, 2^-8 of the value for bf16 and 2^-24 for fp32;
+* products of 4-bit numbers are exact.  The tensor cores add 64 of them to a 32-bit sum at a time, each addend cut off at 2^-24
+  of the largest at the latest, so that a step is off by at most 65 * 2^-24 < 2^-17.9 of the sum of the magnitudes so far, and a
+  sum of K by ceil(K/64) steps of that.  (The CUDA cores' sums of 32 are exact and their 32-bit additions off by 2^-24 each.)  Parts
+  of the depth add one rounding each, at most 76 in all, which 2^-17 covers beside a part's fewer steps;
+* gelu's exponential and division add a few 2^-22 of the result, and as the argument of the exponential grows with y^3, an error of
+  its argument of 2^-22 relative to the 2u <= 100 for which the result is not zero: 2^-15; its slope is at most 1.13;
+* a sine or cosine is off by at most 2^-22 (its own error of 2 steps and its angle's of 2^-27 of a turn), and the rotation rounds
+  twice: 2^-21 of |u| + |v| in all.
+"""
+import math
+
+import numpy as np
+import torch
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+LEVELS = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+
+
+def quantized(x):
+    """Codes (0 to 15) [rows][cols] and scale bytes [rows][ceil(cols/32)] of a matrix, by comparisons in 64 bits with every
+    candidate: the scale is the first of all that is large enough, the code the nearest level.  On the CPU."""
+    x = x.detach().cpu().double()
+    rows, cols = x.shape
+    blocks = -(-cols // 32)
+    p = torch.zeros((rows, blocks * 32), dtype=torch.float64)
+    p[:, :cols] = x
+    p = p.view(rows, blocks, 32)
+    top = p.abs().amax(-1)
+    bad = ~torch.isfinite(p).all(-1)
+    powers = torch.tensor([2.0 ** (b - 127) for b in range(255)], dtype=torch.float64)
+    byte = torch.searchsorted(7.0 * powers, torch.where(bad, torch.zeros_like(top), top).contiguous())
+    unit = powers[byte]
+    v = torch.where(bad[..., None], torch.zeros_like(p), p) / unit[..., None]
+    middles = (LEVELS[1:] + LEVELS[:-1]) / 2
+    size = v.abs().contiguous()
+    low, high = torch.searchsorted(middles, size, right=False), torch.searchsorted(middles, size, right=True)
+    code = torch.where(low % 2 == 0, low, high)          # in the middle of two these differ: the even one
+    code = code + 8 * torch.signbit(v)
+    byte[bad] = 255
+    return code.view(rows, -1)[:, :cols], byte, bad
+
+
+def values(code, byte):
+    """64-bit values of codes and scale bytes."""
+    v = torch.cat([LEVELS, -LEVELS])[code]
+    scale = torch.exp2(byte.double() - 127)
+    scale[byte == 255] = math.nan
+    return v * scale.repeat_interleave(32, 1)[:, :v.shape[1]]
+
+
+def packed(code, byte, rows, cols):
+    """The documented bytes of codes and scales."""
+    tiles, row_tiles = -(-cols // 128), -(-rows // 128)
+    full = torch.zeros((rows, tiles * 128), dtype=torch.int64)
+    full[:, :cols] = code
+    codes = (full[:, 0::2] + 16 * full[:, 1::2]).to(torch.uint8)
+    grid = torch.zeros((row_tiles * 128, tiles * 4), dtype=torch.int64)
+    grid[:rows, :byte.shape[1]] = byte
+    scales = grid.view(row_tiles, 4, 32, tiles, 4).permute(0, 3, 2, 1, 4).contiguous().to(torch.uint8)
+    return codes, scales
+
+
+def special(x, gen):
+    """Writes into x (fp32, on the CPU) what a quantiser can get wrong, as far as it has room."""
+    rows, cols = x.shape
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0, -6.0])
+    row = ties.repeat(-(-cols // 16))[:cols]
+    tricks = [torch.zeros(cols), row, row * 2.0 ** -100, row * 1.0000001, row * 0.9999999, row * 2.0 ** 120,
+              torch.full((cols,), 7.0), torch.full((cols,), 7.0000005), torch.full((cols,), 3.3895e38),
+              torch.randn(cols, generator=gen) * 1e-40, torch.full((cols,), -1.17e-38), torch.full((cols,), -0.0)]
+    for i, t in enumerate(tricks):
+        if i + 1 < rows:
+            x[i + 1] = t
+    if rows > 14:
+        x[13, cols // 2] = math.nan
+        x[14, cols - 1] = -math.inf
+    return x
+
+
+def gelu(y):
+    return y / (1 + torch.exp(-math.sqrt(8 / math.pi) * (y + 0.044715 * y ** 3)))
+
+
+def product_reference(a, b, bias, with_gelu, out_dtype):
+    """act(a b^T + bias) of 64-bit matrices and its bound."""
+    y, size = a @ b.t(), a.abs() @ b.abs().t()
+    err = (-(-a.shape[1] // 64) * 2.0 ** -17.9 + 2.0 ** -17) * size
+    if bias is not None:
+        y = y + bias.double()
+        err = err + 2.0 ** -23 * (size + bias.double().abs())
+    if with_gelu:
+        err = 1.13 * err + 2.0 ** -15 * gelu(y).abs() + 2.0 ** -40
+        y = gelu(y)
+    return y, err + HALF[out_dtype] * (y.abs() + err)
+
+
+def rope_reference(x, positions, dims, base, scale, halves, backward=False):
+    """Rotated x [B][N][H][D] in 64 bits and its bound.  Angles by exact integer arithmetic where the frequency is a power of two
+    of a turn would need no more; here in long double."""
+    B, N, H, D = x.shape
+    y = x.double().clone()
+    tol = torch.zeros_like(y)
+    first = 0
+    for a, d in enumerate(dims):
+        j = np.arange(d // 2, dtype=np.longdouble)
+        freq = np.longdouble(scale[a] if scale else 1.0) * np.longdouble(base) ** (-2 * j / d)
+        angle = positions[..., a].cpu().numpy().astype(np.longdouble)[..., None] * freq
+        sign = -1.0 if backward else 1.0
+        turn = lambda f: torch.from_numpy(f(angle).astype(np.float64)).to(x.device).expand(B, N, d // 2)[:, :, None]
+        c, s = turn(np.cos), sign * turn(np.sin)
+        i = torch.arange(d // 2, device=x.device)
+        u, v = (first + i, first + d // 2 + i) if halves else (first + 2 * i, first + 2 * i + 1)
+        p, q = x[..., u].double(), x[..., v].double()
+        y[..., u], y[..., v] = p * c - q * s, p * s + q * c
+        tol[..., u] = tol[..., v] = 2.0 ** -21 * (p.abs() + q.abs())
+        first += d
+    return y, tol + HALF[x.dtype] * (y.abs() + tol)
+
+
+def within(got, ref, tol, what):
+    """|got - ref| <= tol everywhere."""
+    got = got.double()
+    bad = ~((got - ref).abs() <= tol) & ~(got == ref) & ~(got.isnan() & ref.isnan())
+    if bool(bad.any()):
+        i = tuple(int(j) for j in bad.nonzero()[0])
+        raise AssertionError("%s: %d of %d outside the bound, first at %s: %r, reference %r, bound %.3g" %
+                             (what, int(bad.sum()), bad.numel(), i, float(got[i]), float(ref[i]), float(tol[i])))
