@@ -3,7 +3,16 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace sdv2 {
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
 // The scale's byte of a block whose largest magnitude has the bits `amax` (as fp32): the least e with
 // amax <= 7 * 2^e, plus 127.  With amax = 1.m * 2^(E - 127) that is E - 2, and one more where 1.m > 1.75, which a carry out
@@ -54,12 +63,31 @@ __device__ __forceinline__ void mx4_numbers(uint32_t codes, __half2 (&x)[4])
     for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
-// y/2 * (1 + tanh(u)), u = sqrt(2/pi) * (y + 0.044715 y^3), as y / (1 + exp(-2u)).
+// y/2 * (1 + tanh(u)), u = sqrt(2/pi) * (y + 0.044715 y^3), as y / (1 + exp(-2u)), of two numbers.  One reciprocal serves both:
+// that of the product of the two divisors, which stays below 2^112 because y is taken to be at least -7.2 (the result there,
+// -2^-52, stands for all smaller ones).  Two exponentials and a reciprocal leave the MUFU pipe 1.5 operations a number.
+__device__ __forceinline__ uint64_t gelu2(uint64_t y)
+{
+    constexpr float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
+    float a, b;
+    f32x2_unpack(y, a, b);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-7.2f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-7.2f));
+    y = f32x2_pack(a, b);
+    const uint64_t z = mul2(y, ffma2(mul2(y, y), f32x2_pack(k * 0.044715f, k * 0.044715f), f32x2_pack(k, k)));
+    f32x2_unpack(z, a, b);
+    a = 1.0f + ex2_approx(a);
+    b = 1.0f + ex2_approx(b);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    return mul2(y, mul2(f32x2_pack(r, r), f32x2_pack(b, a)));
+}
+
 __device__ __forceinline__ float gelu(float y)
 {
-    constexpr float c = -2.0f * 0.7978845608028654f;
-    const float e = __expf(y * fmaf(c * 0.044715f, y * y, c));
-    return __fdividef(y, 1.0f + e);
+    float a, b;
+    f32x2_unpack(gelu2(f32x2_pack(y, 0.0f)), a, b);
+    return a;
 }
 
 }  // namespace sdv2

@@ -8,7 +8,7 @@
 // CTA's own 128 rows of a, and those of all 256 rows of b, which both CTAs read.
 //   warp 0: TMA producer (both CTAs load into their own shared memory and count the bytes on the leader's stage barrier, which
 //   the leader arms for both); warp 1: in the leader, scale copies and MMAs, whose commits arrive on the barriers of both CTAs;
-//   warps 2-9: epilogue, two per quarter of the tensor memory's lanes, thread = row of a; 128 bytes of a row at a time go
+//   warps 2-9: epilogue, two per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 128 bytes of a row at a time go
 //   through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
 // Where tiles are fewer than pairs, the depth is cut into parts; their sums go to the workspace in fp32 and a second kernel adds
 // them in order, so that results do not depend on which part ends first.
@@ -40,10 +40,12 @@ constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr uint32_t OUT_BYTES = 32 * 128;       // a warp's staging of its rows
-// tensor memory: sums, scales of a, scales of b
-constexpr uint32_t COL_AS = 256, COL_BS = COL_AS + 4 * STEP_TILES, TMEM_COLS = 512;
-constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 1, B_DONE = 2 * STAGES + 2,
-              NBARS = 2 * STAGES + 3;
+// Tensor memory: the sums of two tiles, the second's 256 columns beginning with the first's last 32, and behind them the scales of
+// a and of b.  The epilogue takes the shared columns of a tile first, and the next tile begins when they are free.
+constexpr uint32_t COL_SECOND = TN - 32, COL_AS = COL_SECOND + TN, COL_BS = COL_AS + 4 * STEP_TILES, TMEM_COLS = 512;
+static_assert(COL_BS + 8 * STEP_TILES <= TMEM_COLS, "tensor memory");
+constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 2, B_SHARED = 2 * STAGES + 4,
+              B_DONE = 2 * STAGES + 5, NBARS = 2 * STAGES + 6;
 constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;
 constexpr uint32_t BIAS_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
 constexpr uint32_t BAR_OFF = BIAS_OFF + EPI_WARPS * (TN / 2) * 4;
@@ -85,6 +87,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t pack2(uint64_t v)
+{
+    float lo, hi;
+    f32x2_unpack(v, lo, hi);
+    return pack2(lo, hi);
+}
+
+// Rows of out that TMA cannot write: a warp stores a row's 128 staged bytes number by number.
+template <bool F32>
+__device__ __noinline__ void store_rows(const ProductParams& p, const uint8_t* stage, int row0, int n)
+{
+    const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
+    constexpr int PER = F32 ? 4 : 8;
+    for (int r = 0; r < rows; ++r)
+        for (int j = lane; j < 8 * PER; j += 32) {
+            if (n + j >= p.N) continue;
+            const uint8_t* at = stage + r * 128 + (((j / PER) ^ (r & 7)) << 4);
+            const int64_t o = (row0 + r) * p.out_stride + n + j;
+            if constexpr (F32) static_cast<float*>(p.direct)[o] = reinterpret_cast<const float*>(at)[j % PER];
+            else static_cast<uint16_t*>(p.direct)[o] = reinterpret_cast<const uint16_t*>(at)[j % PER];
+        }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductParams p)
 {
@@ -106,8 +131,11 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * STAGES; ++i) mbar_init(bar(i), 1);
-        mbar_init(bar(B_ACC_FULL), 1);
-        mbar_init(bar(B_ACC_EMPTY), 2 * EPI_WARPS);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_ACC_FULL + i), 1);
+            mbar_init(bar(B_ACC_EMPTY + i), 2 * EPI_WARPS);
+        }
+        mbar_init(bar(B_SHARED), EPI_WARPS);       // half of the warps of each CTA
         mbar_init(bar(B_DONE), 1);
         *abort_flag = 0;
         *peer_steps = 0;
@@ -171,11 +199,15 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             int g = 0, li = 0;
             for (int u = pair; ok && u < units; u += pairs, ++li) {
                 const Unit t(p, u);
-                if (!wait(B_ACC_EMPTY, (static_cast<uint32_t>(li) & 1u) ^ 1u)) {
+                const int buf = li & 1;
+                // the tile before last has been read, and of the last one the columns that both use
+                if (!wait(B_ACC_EMPTY + buf, (static_cast<uint32_t>(li >> 1) & 1u) ^ 1u) ||
+                    (li > 0 && !wait(B_SHARED, static_cast<uint32_t>(li - 1) & 1u))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t acc = tmem + (buf ? COL_SECOND : 0u);
                 for (int k = t.first; k < t.last; ++k, ++g) {
                     const int st = g % STAGES;
                     if (!wait(B_FULL + st, static_cast<uint32_t>(g / STAGES) & 1u)) {
@@ -192,12 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma_mx4_pair_warp(tmem, dA + at + 2 * i, dB + at + 2 * i, (i & 1) ? idesc_mx4(TM, TN, 1) : idesc_mx4(TM, TN, 0),
+                        mma_mx4_pair_warp(acc, dA + at + 2 * i, dB + at + 2 * i, (i & 1) ? idesc_mx4(TM, TN, 1) : idesc_mx4(TM, TN, 0),
                                           tmem + COL_AS + 4 * (i >> 1), tmem + COL_BS + 8 * (i >> 1), (k > t.first || i > 0) ? 1u : 0u);
                     mma_commit_pair_warp(bar(B_EMPTY + st), kBothCtas);
                 }
                 if (!ok) break;
-                mma_commit_pair_warp(bar(B_ACC_FULL), kBothCtas);
+                mma_commit_pair_warp(bar(B_ACC_FULL + buf), kBothCtas);
             }
             if (!ok && lane == 0) give_up();
             mma_commit_pair_warp(bar(B_DONE), kBothCtas);            // tensor memory is freed only behind the last MMA
@@ -210,14 +242,16 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     } else {
         const int part = (warp - 2) >> 2, quarter = warp & 3;
         const int col0 = part * (TN / 2);
-        constexpr int CHUNK = F32 ? 32 : 64;                         // columns of 128 bytes
+        constexpr int PIECE = 32, PIECES = TN / 2 / PIECE;           // columns that a thread has at once
+        constexpr int TOGETHER = F32 ? 1 : 2;                        // pieces that make 128 bytes
         uint8_t* stage = smem + OUT_OFF + (warp - 2) * OUT_BYTES;
         float* bias = reinterpret_cast<float*>(smem + BIAS_OFF) + (warp - 2) * (TN / 2);
-        const uint32_t acc_empty_leader = map_to_rank(bar(B_ACC_EMPTY), 0);
+        const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), 0), shared_leader = map_to_rank(bar(B_SHARED), 0);
         const bool whole = p.splits == 1;                            // else partial sums
         int li = 0;
         for (int u = pair; u < units; u += pairs, ++li) {
             const Unit t(p, u);
+            const int buf = li & 1;
             const int row0 = t.m0 + rank * CM + quarter * 32;
 #pragma unroll
             for (int j = 0; j < TN / 2 / 32; ++j) {
@@ -225,66 +259,74 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 bias[j * 32 + lane] = whole && p.bias && n < p.N ? p.bias[n] : 0.0f;
             }
             __syncwarp();
-            const bool ok = mbar_wait_cluster_bounded(bar(B_ACC_FULL), static_cast<uint32_t>(li) & 1u, tmo, abort_flag) && !*abort_flag;
+            const bool ok = mbar_wait_cluster_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
             tc_fence_after();
-            const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(col0);
-#pragma unroll 1
-            for (int c = 0; c < TN / 2; c += CHUNK) {
-                float y[CHUNK];
+            const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(col0) + (buf ? COL_SECOND : 0u);
+            // the first buffer backwards: its last columns are the ones that the second shares
+            const int flip = buf ? 0 : PIECES - 1;
+            uint32_t raw[2][PIECE];
+            tmem_ld_x32_start(trow + (0 ^ flip) * PIECE, raw[0]);
 #pragma unroll
-                for (int h = 0; h < CHUNK; h += 32) tmem_ld_x32_sync(trow + c + h, reinterpret_cast<uint32_t(&)[32]>(y[h]));
+            for (int i = 0; i < PIECES; ++i) {
+                uint32_t(&y)[PIECE] = raw[i & 1];
+                tmem_ld_x32_finish(y);
+                if (i == 0 && part != buf) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(shared_leader);
+                }
+                if (i + 1 < PIECES) {
+                    tmem_ld_x32_start(trow + ((i + 1) ^ flip) * PIECE, raw[(i + 1) & 1]);
+                } else {                                             // all sums have been read; the arrival orders no memory
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader + 8u * static_cast<uint32_t>(buf));
+                }
+                const int c = (i ^ flip) * PIECE;
+                uint64_t v[PIECE / 2];
 #pragma unroll
-                for (int j = 0; j < CHUNK; j += 4) {
-                    const float4 b4 = *reinterpret_cast<const float4*>(bias + c + j);
-                    y[j] += b4.x, y[j + 1] += b4.y, y[j + 2] += b4.z, y[j + 3] += b4.w;
+                for (int j = 0; j < PIECE; j += 4) {
+                    const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bias + c + j);
+                    v[j / 2] = fadd2(f32x2_pack(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), b4.x);
+                    v[j / 2 + 1] = fadd2(f32x2_pack(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), b4.y);
                 }
                 if (whole && p.gelu) {
 #pragma unroll
-                    for (int j = 0; j < CHUNK; ++j) y[j] = gelu(y[j]);
+                    for (int j = 0; j < PIECE / 2; ++j) v[j] = gelu2(v[j]);
                 }
-                if (lane == 0) tma_store_wait_read();
-                __syncwarp();
+                if (i % TOGETHER == 0) {
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
+                }
+                // 16-byte vectors of a row of 128 bytes, swizzled as TMA takes them
 #pragma unroll
-                for (int v = 0; v < 8; ++v) {
+                for (int j = 0; j < 8 / TOGETHER; ++j) {
                     uint4 w;
-                    if constexpr (F32)
-                        w = make_uint4(__float_as_uint(y[4 * v]), __float_as_uint(y[4 * v + 1]), __float_as_uint(y[4 * v + 2]),
-                                       __float_as_uint(y[4 * v + 3]));
-                    else
-                        w = make_uint4(pack2(y[8 * v], y[8 * v + 1]), pack2(y[8 * v + 2], y[8 * v + 3]), pack2(y[8 * v + 4], y[8 * v + 5]),
-                                       pack2(y[8 * v + 6], y[8 * v + 7]));
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((v ^ (lane & 7)) << 4)) = w;
+                    if constexpr (F32) {
+                        w = make_uint4(static_cast<uint32_t>(v[2 * j]), static_cast<uint32_t>(v[2 * j] >> 32),
+                                       static_cast<uint32_t>(v[2 * j + 1]), static_cast<uint32_t>(v[2 * j + 1] >> 32));
+                    } else {
+                        w = make_uint4(pack2(v[4 * j]), pack2(v[4 * j + 1]), pack2(v[4 * j + 2]), pack2(v[4 * j + 3]));
+                    }
+                    const int at = F32 ? j : j + 4 * ((i ^ flip) & 1);
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((at ^ (lane & 7)) << 4)) = w;
                 }
-                const int n = t.n0 + col0 + c;
+                if (i % TOGETHER != TOGETHER - 1) continue;
+                const int n = t.n0 + col0 + (F32 ? c : c & ~63);
                 if (!p.direct) {
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M && n < p.N) tma_store_3d(&p.out, smem_u32(stage), n, row0, t.split);
                 } else {
                     __syncwarp();
-                    const int rows = min(32, p.M - row0);
-#pragma unroll 1
-                    for (int r = 0; r < rows; ++r)
-#pragma unroll
-                        for (int j = lane; j < CHUNK; j += 32) {
-                            if (n + j >= p.N) continue;
-                            constexpr int PER = F32 ? 4 : 8;
-                            const uint8_t* at = stage + r * 128 + (((j / PER) ^ (r & 7)) << 4);
-                            const int64_t o = (row0 + r) * p.out_stride + n + j;
-                            if constexpr (F32) static_cast<float*>(p.direct)[o] = reinterpret_cast<const float*>(at)[j % PER];
-                            else static_cast<uint16_t*>(p.direct)[o] = reinterpret_cast<const uint16_t*>(at)[j % PER];
-                        }
+                    store_rows<F32>(p, stage, row0, n);
                     __syncwarp();
                 }
             }
-            // the sums have been read: the MMA warp may go on; the arrival orders no memory
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader);
         }
         if (lane == 0) tma_store_wait();
         __syncwarp();

@@ -1,4 +1,11 @@
 // Matrices to and from microscaled 4-bit numbers.
+//
+// Both read and write every byte once, so that memory bounds them as long as the arithmetic of a number stays below about 20
+// instructions.  A block of 256 threads takes 16 rows, 16 threads a row; a thread has 8 neighbouring columns of a tile of 128 and
+// up to four tiles, all of whose loads are under way together, at addresses that differ by constants.  The 16 rows are 4
+// neighbours and those 32, 64 and 96 behind them, whose scales lie together (64 bytes a tile).
+// A row that is not whole vectors of 8 columns is read and written number by number, 16 neighbours at once, by way of shared
+// memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -10,119 +17,138 @@
 namespace sdv2 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;     // 16 threads take a tile of a row: 128 numbers, 8 each
+constexpr int kThreads = 256, kRows = 16;
+constexpr int kUnroll = 4;                 // tiles of a thread
 
-__device__ __forceinline__ int64_t scale_offset(int64_t row, int tile, int tiles)
-{
-    return ((row >> 7) * tiles + tile) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-}
-
-// Row and tile of a thread's units, which lie `step` units apart.
-struct Units {
+// A thread's row and first tile.
+struct Place {
     int64_t row;
-    int tile;
-    int tiles, step_rows, step_tiles;
-    __device__ __forceinline__ Units(int64_t first, int tiles_, int step) : tiles(tiles_)
+    int row_tile, in_tile, tile, tiles;
+    __device__ __forceinline__ Place(const Mx4Params& p, unsigned row_groups)
     {
-        row = first / tiles_;
-        tile = static_cast<int>(first - row * tiles_);
-        step_rows = step / tiles_;
-        step_tiles = step - step_rows * tiles_;
+        const unsigned chunk = blockIdx.x / row_groups, group = blockIdx.x - chunk * row_groups;
+        const int i = threadIdx.x >> 4;
+        row_tile = static_cast<int>(group >> 3);
+        in_tile = static_cast<int>(group & 7) * 4 + (i & 3) + 32 * (i >> 2);
+        row = static_cast<int64_t>(row_tile) * kMx4Tile + in_tile;
+        tile = static_cast<int>(chunk) * kUnroll;
+        tiles = min(kUnroll, p.tiles - tile);
     }
-    __device__ __forceinline__ void next()
+    __device__ __forceinline__ int64_t codes(const Mx4Params& p) const { return (row * p.tiles + tile) * kMx4TileBytes; }
+    __device__ __forceinline__ int64_t scales(const Mx4Params& p) const
     {
-        row += step_rows;
-        tile += step_tiles;
-        if (tile >= tiles) {
-            tile -= tiles;
-            ++row;
-        }
+        return (static_cast<int64_t>(row_tile) * p.tiles + tile) * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
     }
 };
 
-// Eight numbers from column c of a row of `cols` columns, zeros behind its end.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int64_t c, int64_t cols, bool vectors, float (&x)[8])
+__device__ __forceinline__ float bf16_at(const void* x, int64_t i)
 {
-    if (vectors && c + 8 <= cols) {
-        if constexpr (F32) {
-            const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-            const float4 a = v[0], b = v[1];
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float v = 0.0f;
-            if (c + i < cols) {
-                if constexpr (F32) v = static_cast<const float*>(row)[c + i];
-                else v = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[c + i]) << 16);
-            }
-            x[i] = v;
-        }
-    }
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x)[i]) << 16);
 }
 
 __device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Four threads hold a block of 32; each finds the block's scale with two exchanges.
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params p)
+template <bool F32, bool VECTORS>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params p, unsigned row_groups)
 {
-    constexpr int kUnits = 4;
+    __shared__ __align__(16) float staged[VECTORS ? 1 : kRows * kMx4Tile];
     wait_for_launch_before();
+    const Place at(p, row_groups);
     const int lane = threadIdx.x & 15;
-    const int64_t padded = (p.rows + kMx4Tile - 1) / kMx4Tile * kMx4Tile;
-    Units u(static_cast<int64_t>(blockIdx.x) * (kGroups * kUnits) + (threadIdx.x >> 4), p.tiles, kGroups);
-    const size_t size = F32 ? 4 : 2;
-    float x[kUnits][8];
-    int64_t row[kUnits];
-    int tile[kUnits];
+    const bool live = at.row < p.rows;
+    const int64_t c0 = static_cast<int64_t>(at.tile) * kMx4Tile;
+    const int64_t first = live ? at.row * p.stride + c0 : 0;
+    float x[kUnroll][8];
+    uint32_t top[kUnroll];
+    if constexpr (VECTORS) {
+        uint4 raw[kUnroll][F32 ? 2 : 1];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.x) + first * (F32 ? 4 : 2)) + lane * (F32 ? 2 : 1);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i, u.next()) {
-        row[i] = u.row;
-        tile[i] = u.tile;
-        const int64_t cols = u.row < p.rows ? p.cols : 0;
-        const unsigned char* src = static_cast<const unsigned char*>(p.x) + (cols ? u.row * p.stride * size : 0);
-        load8<F32>(src, static_cast<int64_t>(u.tile) * kMx4Tile + lane * 8, cols, p.vectors != 0, x[i]);
+        for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+            for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+                raw[i][h] = make_uint4(0, 0, 0, 0);
+                if (live && c0 + i * kMx4Tile + lane * 8 < p.cols) raw[i][h] = src[i * (F32 ? 32 : 16) + h];
+            }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint4 v = raw[i][0];
+            if constexpr (F32) {
+                const uint4 w = raw[i][1];
+                const uint32_t all[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+                top[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[i][j] = __uint_as_float(all[j]);
+                    top[i] = max(top[i], all[j] & 0x7FFFFFFFu);
+                }
+            } else {
+                const uint32_t all[4] = {v.x, v.y, v.z, v.w};
+                uint32_t two = 0;                        // the largest of the even and of the odd ones
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][2 * j] = __uint_as_float(all[j] << 16);
+                    x[i][2 * j + 1] = __uint_as_float(all[j] & 0xFFFF0000u);
+                    two = __vmaxu2(two, all[j] & 0x7FFF7FFFu);
+                }
+                top[i] = max(two << 16, two & 0xFFFF0000u);
+            }
+        }
+    } else {
+        float raw[kUnroll][8];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = i * kMx4Tile + j * 16 + lane;
+                raw[i][j] = 0.0f;
+                if (live && c0 + c < p.cols) raw[i][j] = F32 ? static_cast<const float*>(p.x)[first + c] : bf16_at(p.x, first + c);
+            }
+        float* mine = staged + (threadIdx.x >> 4) * kMx4Tile;
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mine[j * 16 + lane] = raw[i][j];
+            __syncwarp();
+            top[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[i][j] = mine[lane * 8 + j];
+                top[i] = max(top[i], size_bits(x[i][j]));
+            }
+        }
     }
+    uint8_t* codes = p.codes + at.codes(p) + lane * 4;
+    uint8_t* scales = p.scales + at.scales(p);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, size_bits(x[i][j]));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const uint32_t byte = mx4_scale_byte(top);
+    for (int i = 0; i < kUnroll; ++i) {
+        uint32_t t = top[i];                             // four threads hold a block of 32
+        t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+        t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+        const uint32_t byte = mx4_scale_byte(t);
         const float inverse = mx4_inverse(byte);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[i][j] *= inverse;
-        const uint32_t codes = mx4_codes(x[i]);
+        const uint32_t four_bits = mx4_codes(x[i]);
         uint32_t word = byte << (8 * (lane >> 2));       // the tile's four scales in one word
         word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
         word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-        if (row[i] < p.rows)
-            *reinterpret_cast<uint32_t*>(p.codes + (row[i] * p.tiles + tile[i]) * kMx4TileBytes + lane * 4) = codes;
-        if (lane == 0 && row[i] < padded) *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row[i], tile[i], p.tiles)) = word;
+        if (i < at.tiles) {
+            if (live) *reinterpret_cast<uint32_t*>(codes + i * kMx4TileBytes) = four_bits;
+            if (lane == 0) *reinterpret_cast<uint32_t*>(scales + i * 512) = word;
+        }
     }
 }
 
 // Rows of the 4-bit matrix are columns of x: a block takes 64 of them and a tile of 128 rows of x.  Each warp reads 32 rows
 // of x, a thread two neighbouring columns, so that blocks of 32 lie in its registers; codes and scales go out by way of
-// shared memory, a row's 64 bytes together.
+// shared memory, a row's 64 bytes together.  Places outside x are read at its nearest place and count as 0, so that all of a
+// thread's loads are under way together.
 constexpr int kTRows = 64, kTThreads = 128;
 constexpr int kTPitch = 80;                // bytes between rows of codes in shared memory: 16-byte stores of 8 rows do not collide
 
-template <bool F32>
+template <bool F32, bool PAIRS>
 __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx4Params p, unsigned row_blocks)
 {
     __shared__ __align__(16) uint8_t codes[kTRows * kTPitch];
@@ -135,31 +161,36 @@ __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx
     const int64_t k0 = static_cast<int64_t>(tile) * kMx4Tile + warp * 32;
     const int depth = static_cast<int>(max(int64_t(0), min(int64_t(32), p.cols - k0)));
     float x[2][32];
-    const bool pairs = (p.stride & 1) == 0 && r + 2 <= p.rows;
-    const size_t size = F32 ? 4 : 2;
-    const unsigned char* src = static_cast<const unsigned char*>(p.x) + (k0 * p.stride + r) * size;
+    if (depth == 32 && r0 + kTRows <= p.rows) {
+        const unsigned char* src = static_cast<const unsigned char*>(p.x) + (k0 * p.stride + r) * (F32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        x[0][i] = x[1][i] = 0.0f;
-        if (i < depth) {
-            const unsigned char* at = src + i * p.stride * size;
-            if (pairs) {
-                if constexpr (F32) {
-                    const float2 v = *reinterpret_cast<const float2*>(at);
-                    x[0][i] = v.x, x[1][i] = v.y;
-                } else {
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
-                    x[0][i] = __uint_as_float(v << 16), x[1][i] = __uint_as_float(v & 0xFFFF0000u);
-                }
+        for (int i = 0; i < 32; ++i) {
+            const unsigned char* from = src + i * p.stride * (F32 ? 4 : 2);
+            if constexpr (PAIRS && F32) {
+                const float2 v = *reinterpret_cast<const float2*>(from);
+                x[0][i] = v.x, x[1][i] = v.y;
+            } else if constexpr (PAIRS) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(from);
+                x[0][i] = __uint_as_float(v << 16), x[1][i] = __uint_as_float(v & 0xFFFF0000u);
+            } else if constexpr (F32) {
+                x[0][i] = reinterpret_cast<const float*>(from)[0], x[1][i] = reinterpret_cast<const float*>(from)[1];
             } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (r + h < p.rows) {
-                        if constexpr (F32) x[h][i] = reinterpret_cast<const float*>(at)[h];
-                        else x[h][i] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[h]) << 16);
-                    }
+                x[0][i] = bf16_at(from, 0), x[1][i] = bf16_at(from, 1);
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t o = min(k0 + i, p.cols - 1) * p.stride + min(r + h, p.rows - 1);
+                x[h][i] = F32 ? static_cast<const float*>(p.x)[o] : bf16_at(p.x, o);
+            }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (i >= depth || r + h >= p.rows) x[h][i] = 0.0f;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -187,101 +218,108 @@ __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx
             *reinterpret_cast<uint4*>(p.codes + ((r0 + row) * p.tiles + tile) * kMx4TileBytes + part * 16) =
                 *reinterpret_cast<const uint4*>(codes + row * kTPitch + part * 16);
     }
-    if (threadIdx.x < kTRows)
-        *reinterpret_cast<uint32_t*>(p.scales + scale_offset(r0 + threadIdx.x, tile, p.tiles)) =
+    if (threadIdx.x < kTRows) {
+        const int64_t row = r0 + threadIdx.x;
+        *reinterpret_cast<uint32_t*>(p.scales + ((row >> 7) * p.tiles + tile) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4) =
             *reinterpret_cast<const uint32_t*>(scales + 4 * threadIdx.x);
+    }
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const Mx4Params p)
+template <bool F32, bool VECTORS>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const Mx4Params p, unsigned row_groups)
 {
-    constexpr int kUnits = 4;
+    __shared__ __align__(16) float staged[VECTORS ? 1 : kRows * kMx4Tile];
     wait_for_launch_before();
+    const Place at(p, row_groups);
     const int lane = threadIdx.x & 15;
-    Units u(static_cast<int64_t>(blockIdx.x) * (kGroups * kUnits) + (threadIdx.x >> 4), p.tiles, kGroups);
-    uint32_t codes[kUnits], byte[kUnits];
-    int64_t row[kUnits];
-    int tile[kUnits];
+    const bool live = at.row < p.rows;
+    const uint8_t* codes = p.codes + at.codes(p) + lane * 4;
+    const uint8_t* scales = p.scales + at.scales(p);
+    uint32_t four_bits[kUnroll] = {}, word[kUnroll] = {};
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i, u.next()) {
-        row[i] = u.row;
-        tile[i] = u.tile;
-        codes[i] = byte[i] = 0;
-        if (u.row < p.rows) {
-            codes[i] = *reinterpret_cast<const uint32_t*>(p.codes + (u.row * p.tiles + u.tile) * kMx4TileBytes + lane * 4);
-            byte[i] = p.scales[scale_offset(u.row, u.tile, p.tiles) + (lane >> 2)];
+    for (int i = 0; i < kUnroll; ++i)
+        if (live && i < at.tiles) {
+            four_bits[i] = *reinterpret_cast<const uint32_t*>(codes + i * kMx4TileBytes);
+            word[i] = *reinterpret_cast<const uint32_t*>(scales + i * 512);
         }
-    }
+    const int64_t c0 = static_cast<int64_t>(at.tile) * kMx4Tile;
+    const int64_t first = at.row * p.stride + c0;
+    float* mine = VECTORS ? staged : staged + (threadIdx.x >> 4) * kMx4Tile;
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        if (row[i] >= p.rows) continue;
-        const float scale = mx4_scale(byte[i]);
+    for (int i = 0; i < kUnroll; ++i) {
+        const float scale = mx4_scale((word[i] >> (8 * (lane >> 2))) & 255u);
         __half2 n[4];
-        mx4_numbers(codes[i], n);
+        mx4_numbers(four_bits[i], n);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 v = __half22float2(n[j]);
             y[2 * j] = v.x * scale, y[2 * j + 1] = v.y * scale;
         }
-        const int64_t c = static_cast<int64_t>(tile[i]) * kMx4Tile + lane * 8;
-        const int64_t at = row[i] * p.stride + c;
-        const bool whole = p.vectors && c + 8 <= p.cols;
-        if constexpr (F32) {
-            float* out = static_cast<float*>(p.y) + at;
-            if (whole) {
-                reinterpret_cast<float4*>(out)[0] = make_float4(y[0], y[1], y[2], y[3]);
-                reinterpret_cast<float4*>(out)[1] = make_float4(y[4], y[5], y[6], y[7]);
+        if constexpr (VECTORS) {
+            if (!live || c0 + i * kMx4Tile + lane * 8 >= p.cols) continue;
+            const int64_t o = first + i * kMx4Tile + lane * 8;
+            if constexpr (F32) {
+                float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.y) + o);
+                out[0] = make_float4(y[0], y[1], y[2], y[3]);
+                out[1] = make_float4(y[4], y[5], y[6], y[7]);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < p.cols) out[j] = y[j];
-            }
-        } else {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.y) + at;
-            if (whole) {
                 __nv_bfloat162 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-                *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(v);
-            } else {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + o) = *reinterpret_cast<uint4*>(v);
+            }
+        } else {
+            __syncwarp();
+            *reinterpret_cast<float4*>(mine + lane * 8) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(mine + lane * 8 + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < p.cols) out[j] = __float2bfloat16_rn(y[j]);
+            for (int j = 0; j < 8; ++j) {
+                const int c = i * kMx4Tile + j * 16 + lane;
+                if (!live || c0 + c >= p.cols) continue;
+                if constexpr (F32) static_cast<float*>(p.y)[first + c] = mine[j * 16 + lane];
+                else static_cast<__nv_bfloat16*>(p.y)[first + c] = __float2bfloat16_rn(mine[j * 16 + lane]);
             }
         }
     }
 }
 
-// Blocks for so many units, or 0 if there are more than a grid holds.
-unsigned blocks_for(int64_t units, int per)
+// Blocks of 16 rows and kUnroll tiles; false if there are more than a grid holds.
+bool blocks_of(const Mx4Params& p, unsigned* grid, unsigned* row_groups)
 {
-    const int64_t n = (units + per - 1) / per;
-    return n <= INT32_MAX ? static_cast<unsigned>(n) : 0;
+    const int64_t groups = (p.rows + kMx4Tile - 1) / kMx4Tile * (kMx4Tile / kRows);
+    const int64_t n = groups * ((p.tiles + kUnroll - 1) / kUnroll);
+    *grid = static_cast<unsigned>(n);
+    *row_groups = static_cast<unsigned>(groups);
+    return n <= INT32_MAX;
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4Params& p, bool transposed, cudaStream_t s)
 {
-    const int64_t padded = (p.rows + kMx4Tile - 1) / kMx4Tile * kMx4Tile;
+    unsigned grid, row_groups;
     if (transposed) {
-        const unsigned row_blocks = static_cast<unsigned>(padded / kTRows);
-        const unsigned grid = blocks_for(static_cast<int64_t>(row_blocks) * p.tiles, 1);
-        if (!grid) return cudaErrorInvalidConfiguration;
-        return launch_chained(p.f32 ? quantize_transposed_kernel<true> : quantize_transposed_kernel<false>, grid, kTThreads, 0, s, p,
-                              row_blocks);
+        const int64_t row_blocks = (p.rows + kMx4Tile - 1) / kMx4Tile * (kMx4Tile / kTRows);
+        if (row_blocks * p.tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+        auto kernel = p.stride & 1 ? (p.f32 ? quantize_transposed_kernel<true, false> : quantize_transposed_kernel<false, false>)
+                                   : (p.f32 ? quantize_transposed_kernel<true, true> : quantize_transposed_kernel<false, true>);
+        return launch_chained(kernel, static_cast<unsigned>(row_blocks * p.tiles), kTThreads, 0, s, p, static_cast<unsigned>(row_blocks));
     }
-    const unsigned grid = blocks_for(padded * p.tiles, kGroups * 4);
-    if (!grid) return cudaErrorInvalidConfiguration;
-    return launch_chained(p.f32 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>, grid, kThreads, 0, s, p);
+    if (!blocks_of(p, &grid, &row_groups)) return cudaErrorInvalidConfiguration;
+    auto kernel = p.vectors ? (p.f32 ? quantize_rows_kernel<true, true> : quantize_rows_kernel<false, true>)
+                            : (p.f32 ? quantize_rows_kernel<true, false> : quantize_rows_kernel<false, false>);
+    return launch_chained(kernel, grid, kThreads, 0, s, p, row_groups);
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4Params& p, cudaStream_t s)
 {
-    const unsigned grid = blocks_for(p.rows * p.tiles, kGroups * 4);
-    if (!grid) return cudaErrorInvalidConfiguration;
-    return launch_chained(p.f32 ? dequantize_kernel<true> : dequantize_kernel<false>, grid, kThreads, 0, s, p);
+    unsigned grid, row_groups;
+    if (!blocks_of(p, &grid, &row_groups)) return cudaErrorInvalidConfiguration;
+    auto kernel = p.vectors ? (p.f32 ? dequantize_kernel<true, true> : dequantize_kernel<false, true>)
+                            : (p.f32 ? dequantize_kernel<true, false> : dequantize_kernel<false, false>);
+    return launch_chained(kernel, grid, kThreads, 0, s, p, row_groups);
 }
 
 }  // namespace sdv2

@@ -1,11 +1,12 @@
-// Products of a few rows with a 4-bit matrix, on the CUDA cores.
+// Products of a few rows with a 4-bit matrix: out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]) for at most 32 rows of a.
 //
-// out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]) for at most eight rows of a.  Every byte of b is read once and takes part
-// in few operations, so that reading b, or at small sizes the latency of a launch, bounds this.  A block owns the four rows
-// n = 128 t + r + 32 i of b whose scales share 16 bytes; each lane of its warps takes a block of 32 columns, which has one
-// scale for each of them: 16 bytes of codes of every row in one load.
-// The sum of a block's 32 products is exact: products of two e2m1 numbers are multiples of 1/4 up to 36, so that 8 of them
-// in a lane of a half2 stay below 2^11 quarters.  It is scaled and added up in fp32.
+// Every byte of b is read once and takes part in few operations, so that reading b bounds this, and at small sizes the latency of
+// a launch.  tcgen05's tiles would leave most SMs idle at the depths and widths of a layer; here a block takes 16 rows of b, whose
+// warps share out the depth, and multiplies with mma.sync m16n8k16: rows of b by up to 8, 16 or 32 rows of a, both decoded to fp16,
+// which holds every e2m1 number.  A thread's four bytes of a row are 8 columns, and any order of the columns will do as long as
+// both operands have it: two MMAs take a block of 32, whose sum is exact (products are multiples of 1/4 up to 36).  It is scaled
+// by the power of two of its row and its column and added up in fp32.
+// The 16 rows are 4 neighbours and those 32, 64 and 96 behind them: their scales lie together, 64 bytes a tile of 128 columns.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -18,128 +19,136 @@ namespace sdv2 {
 namespace {
 
 constexpr int kMaxWarps = 8;
+constexpr int kTogether = 2;               // tiles of a warp whose loads are under way together
 
-__device__ __forceinline__ void numbers32(uint4 codes, __half2 (&x)[16])
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __half2 h[4];
-        mx4_numbers(w[i], h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * i + j] = h[j];
-    }
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// V values of every lane to the sums over the warp: lane l is left with that of value (l >> (5 - log2 V)), in v[0].
-template <int V>
-__device__ __forceinline__ void sum_lanes(float (&v)[V])
+__device__ __forceinline__ void decode(uint32_t codes, uint32_t (&x)[4])
 {
-    const int lane = threadIdx.x & 31;
-    int have = V;
+    __half2 h[4];
+    mx4_numbers(codes, h);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        if (have > 1) {
-            have >>= 1;
-            const bool upper = (lane & d) != 0;
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i)
-                if (i < have) {
-                    const float give = upper ? v[i] : v[i + have];
-                    const float keep = upper ? v[i + have] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, d);
-                }
-        } else {
-            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
-        }
-    }
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<uint32_t*>(&h[i]);
 }
 
-// R: rows of a that a thread has accumulators for, M <= R.
-template <int R>
+__device__ __forceinline__ int byte_of(uint32_t word, int i) { return static_cast<int>((word >> (8 * i)) & 255u); }
+
+// NT: groups of 8 rows of a
+template <int NT>
 __global__ void __launch_bounds__(32 * kMaxWarps) rows_kernel(const Mx4Product p)
 {
-    constexpr int V = 4 * R;
-    __shared__ float sums[kMaxWarps][V];
+    constexpr int COLS = 8 * NT;
+    __shared__ float sums[kMaxWarps][16 * COLS];
     wait_for_launch_before();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x >> 5) * 128 + (blockIdx.x & 31);     // rows n0 + 32 i of b
-    const uint8_t* bs = p.bs + static_cast<int64_t>(blockIdx.x >> 5) * p.tiles * 512 + (blockIdx.x & 31) * 16;
+    const int g = lane >> 2, t = lane & 3, M = static_cast<int>(p.M);
+    const int64_t row_tile = blockIdx.x >> 3;
+    const int q0 = static_cast<int>(blockIdx.x & 7) * 4;
     const int64_t pitch = static_cast<int64_t>(p.tiles) * kMx4TileBytes;
-    const int blocks = p.tiles * 4, M = static_cast<int>(p.M);
-    float acc[V];
+    // rows g and g + 8 of the block's
+    const uint8_t* b[2];
+    const uint8_t* bs[2];
+    bool have[2];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    for (int kb = warp * 32 + lane; kb < blocks; kb += warps * 32) {
-        const int at = kb & 3;
-        const uint4 scale4 = *reinterpret_cast<const uint4*>(bs + static_cast<int64_t>(kb >> 2) * 512);
-        const uint32_t scales[4] = {scale4.x, scale4.y, scale4.z, scale4.w};
-        uint4 bc[4], ac[R];
-        uint32_t ab[R];
+    for (int h = 0; h < 2; ++h) {
+        const int i = g + 8 * h, in_tile = q0 + (i & 3) + 32 * (i >> 2);
+        const int64_t n = row_tile * kMx4Tile + in_tile;
+        have[h] = n < p.N;
+        b[h] = p.b + (have[h] ? n : 0) * pitch + t * 4;
+        bs[h] = p.bs + row_tile * p.tiles * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+    }
+    float acc[NT][4] = {};
+    bool nan_b[2] = {}, nan_a[NT][2] = {};
+    for (int k0 = warp; k0 < p.tiles; k0 += kTogether * warps) {
+        uint32_t bc[kTogether][2][4], bw[kTogether][2], ac[kTogether][NT][4], aw[kTogether][NT][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            bc[i] = n0 + 32 * i < p.N ? *reinterpret_cast<const uint4*>(p.b + (n0 + 32 * i) * pitch + kb * int64_t(16)) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < kTogether; ++u) {
+            const int k = k0 + u * warps;
+            const bool in = k < p.tiles;
+            const int64_t at = static_cast<int64_t>(k) * kMx4TileBytes, scale_at = static_cast<int64_t>(k) * 512;
 #pragma unroll
-        for (int m = 0; m < R; ++m) {
-            ac[m] = make_uint4(0, 0, 0, 0);
-            ab[m] = 0;
-            if (m < M) {
-                ac[m] = *reinterpret_cast<const uint4*>(p.a + m * pitch + kb * int64_t(16));
-                ab[m] = p.as[static_cast<int64_t>(kb >> 2) * 512 + m * 16 + at];
+            for (int h = 0; h < 2; ++h) {
+                bw[u][h] = in && have[h] ? *reinterpret_cast<const uint32_t*>(bs[h] + scale_at) : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bc[u][h][j] = in && have[h] ? *reinterpret_cast<const uint32_t*>(b[h] + at + j * 16) : 0;
+            }
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int m = 8 * c + 2 * t + h;
+                    aw[u][c][h] = in && m < M ? *reinterpret_cast<const uint32_t*>(p.as + scale_at + m * 16) : 0;
+                }
+                const int m = 8 * c + g;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    ac[u][c][j] = in && m < M ? *reinterpret_cast<const uint32_t*>(p.a + m * pitch + at + t * 4 + j * 16) : 0;
             }
         }
-        __half2 b[4][16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) numbers32(bc[i], b[i]);
+        for (int u = 0; u < kTogether; ++u) {
 #pragma unroll
-        for (int m = 0; m < R; ++m) {
-            if (m >= M) break;
-            __half2 a[16];
-            numbers32(ac[m], a);
+            for (int h = 0; h < 2; ++h) {
+                nan_b[h] |= __vcmpeq4(bw[u][h], 0xFFFFFFFFu) != 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t bb = (scales[i] >> (8 * at)) & 255u;
-                __half2 s0 = __hmul2(a[0], b[i][0]), s1 = __hmul2(a[8], b[i][8]);
+                for (int c = 0; c < NT; ++c) nan_a[c][h] |= __vcmpeq4(aw[u][c][h], 0xFFFFFFFFu) != 0;
+            }
 #pragma unroll
-                for (int j = 1; j < 8; ++j) {
-                    s0 = __hfma2(a[j], b[i][j], s0);
-                    s1 = __hfma2(a[j + 8], b[i][j + 8], s1);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t x0[4], x1[4];
+                decode(bc[u][0][j], x0);
+                decode(bc[u][1][j], x1);
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    uint32_t y[4];
+                    decode(ac[u][c][j], y);
+                    float s[4] = {};
+                    mma_16x8x16(s, x0[0], x1[0], x0[1], x1[1], y[0], y[1]);
+                    mma_16x8x16(s, x0[2], x1[2], x0[3], x1[3], y[2], y[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // 2^(eb + ea), 0 below fp32's normal numbers and 2^127 above them
+                        const int e = byte_of(bw[u][i >> 1], j) + byte_of(aw[u][c][i & 1], j) - 127;
+                        acc[c][i] = fmaf(s[i], __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23), acc[c][i]);
+                    }
                 }
-                const float2 f0 = __half22float2(s0), f1 = __half22float2(s1);
-                const float dot = (f0.x + f0.y) + (f1.x + f1.y);
-                // 2^(ea + eb) as two factors, neither of which leaves fp32's range before the product does
-                const int e = static_cast<int>(ab[m] + bb) - 254;
-                const int half = e >> 1;
-                float scaled = dot * __uint_as_float(static_cast<uint32_t>(max(half + 127, 1)) << 23) *
-                               __uint_as_float(static_cast<uint32_t>(max(e - half + 127, 1)) << 23);
-                if (max(ab[m], bb) == 255u) scaled = __uint_as_float(0x7FC00000u);
-                acc[4 * m + i] += scaled;
             }
         }
     }
-    sum_lanes<V>(acc);
-    if ((lane & (32 / V - 1)) == 0) sums[warp][lane / (32 / V)] = acc[0];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool bad = nan_b[i >> 1] || nan_a[c][i & 1];
+            sums[warp][(g + 8 * (i >> 1)) * COLS + 8 * c + 2 * t + (i & 1)] = bad ? __uint_as_float(0x7FC00000u) : acc[c][i];
+        }
     __syncthreads();
-    const int m = threadIdx.x >> 2;
-    const int64_t n = n0 + 32 * (threadIdx.x & 3);
-    if (m >= M || n >= p.N) return;
-    float y = sums[0][threadIdx.x];
-    for (int w = 1; w < warps; ++w) y += sums[w][threadIdx.x];
-    if (p.bias) y += p.bias[n];
-    if (p.gelu) y = gelu(y);
-    const int64_t o = m * p.out_stride + n;
-    if (p.out_f32) static_cast<float*>(p.out)[o] = y;
-    else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+    for (int o = threadIdx.x; o < 16 * M; o += blockDim.x) {
+        const int m = o >> 4, i = o & 15;
+        const int64_t n = row_tile * kMx4Tile + q0 + (i & 3) + 32 * (i >> 2);
+        if (n >= p.N) continue;
+        float y = sums[0][i * COLS + m];
+        for (int w = 1; w < warps; ++w) y += sums[w][i * COLS + m];
+        if (p.bias) y += p.bias[n];
+        if (p.gelu) y = gelu(y);
+        const int64_t at = m * p.out_stride + n;
+        if (p.out_f32) static_cast<float*>(p.out)[at] = y;
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s)
 {
-    // a warp for every 32 blocks of columns, so that a block's loads are all under way at once
-    const int warps = std::min(kMaxWarps, (p.tiles * 4 + 31) / 32);
-    const unsigned grid = static_cast<unsigned>((p.N + 127) / 128 * 32);
-    auto kernel = p.M == 1 ? rows_kernel<1> : p.M == 2 ? rows_kernel<2> : p.M <= 4 ? rows_kernel<4> : rows_kernel<8>;
+    const int warps = std::min(kMaxWarps, (p.tiles + kTogether - 1) / kTogether);
+    const unsigned grid = static_cast<unsigned>((p.N + kMx4Tile - 1) / kMx4Tile * 8);
+    auto kernel = p.M <= 8 ? rows_kernel<1> : p.M <= 16 ? rows_kernel<2> : rows_kernel<4>;
     return launch_chained(kernel, grid, 32 * warps, 0, s, p);
 }
 

@@ -22,7 +22,7 @@ struct Mx4Params {
     int64_t rows, cols, stride;            // of the 4-bit matrix; elements between rows of x or y
     int32_t tiles;                         // ceil(cols / 128)
     int32_t f32;                           // x or y is fp32, else bf16
-    int32_t vectors;                       // rows of x or y begin on 16 bytes
+    int32_t vectors;                       // rows of x or y begin on 16 bytes and are whole groups of 8 columns
 };
 
 cudaError_t launch_mx4_quantize(const Mx4Params& p, bool transposed, cudaStream_t s);

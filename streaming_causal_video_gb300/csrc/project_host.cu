@@ -38,7 +38,7 @@ Mx4Params mx4_params(const sdv2_mx4_cfg* c)
     p.stride = c->x_row_stride ? c->x_row_stride : c->transposed ? c->rows : c->cols;
     p.tiles = tiles_of(c->cols);
     p.f32 = c->x_dtype == SDV2_F32;
-    p.vectors = (p.stride & (p.f32 ? 3 : 7)) == 0;
+    p.vectors = (p.stride % (p.f32 ? 4 : 8) | p.cols % 8) == 0;
     return p;
 }
 
