@@ -4,7 +4,7 @@ import ctypes
 import torch
 
 from . import _binding as _b
-from ._block import _FP, _TYPE, _U8, _Config, _Operands, _stream
+from ._block import _FP, _TYPE, _U8, _Config, _current_device, _Operands, _stream
 
 NO_ACTIVATION, GELU = 0, 1     # sdv2_activation
 
@@ -80,6 +80,30 @@ class AxesRopeConfig(_Config):
                 operand(self.kv_heads, self.k_out), places * max(self.axes, 0) * 4)
 
 
+def _here(t):
+    """The current device if t is a tensor on it, else a number that is no tensor's device."""
+    if t.__class__ is torch.Tensor and t.is_cuda:
+        d = t.get_device()
+        if d == _current_device():
+            return d
+    return -2
+
+
+def _buffer(t, name, dtype, nbytes, device):
+    """Pointer of a dense tensor of at least nbytes bytes.  What is as it should be is seen at once; anything else goes to
+    the checks that say what is wrong with it (or find that nothing is)."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.nbytes >= nbytes and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    return _Operands()(t, name, dtype, nbytes, True)
+
+
+def _view(t, name, kind, shape, strides, nbytes, device):
+    """The same for a view of a configuration's shape and strides."""
+    if t.__class__ is torch.Tensor and t.dtype is kind and t.shape == shape and t.stride() == strides and t.get_device() == device:
+        return t.data_ptr()
+    return _Operands().view(t, name, kind, shape, strides, nbytes)
+
+
 _LIB = None
 
 
@@ -124,20 +148,20 @@ def mx4_workspace_init(cfg, ws, stream=None):
 def mx4_quantize(cfg, x, codes, scales, stream=None):
     """x: [rows][cols] (transposed: [cols][rows]) of cfg.x_dtype; codes, scales: uint8, of mx4_codes_bytes(cfg) and
     mx4_scales_bytes(cfg) bytes."""
-    op = _Operands()
-    nc, ns, (kind, shape, strides, span) = cfg.derived()
-    status = _lib().sdv2_mx4_quantize(ctypes.byref(cfg), op.view(x, "x", kind, shape, strides, span),
-                                      op(codes, "codes", _U8, nc, True), op(scales, "scales", _U8, ns, True), _stream(stream))
+    dev = _here(x)
+    nc, ns, plan = cfg.derived()
+    status = _lib().sdv2_mx4_quantize(cfg, _view(x, "x", *plan, dev), _buffer(codes, "codes", _U8, nc, dev),
+                                      _buffer(scales, "scales", _U8, ns, dev), _stream(stream))
     if status:
         _b._check(status, "sdv2_mx4_quantize")
 
 
 def mx4_dequantize(cfg, codes, scales, y, stream=None):
     """y: [rows][cols] of cfg.x_dtype, the values that codes and scales stand for."""
-    op = _Operands()
-    nc, ns, (kind, shape, strides, span) = cfg.derived()
-    status = _lib().sdv2_mx4_dequantize(ctypes.byref(cfg), op(codes, "codes", _U8, nc, True), op(scales, "scales", _U8, ns, True),
-                                        op.view(y, "y", kind, shape, strides, span), _stream(stream))
+    dev = _here(y)
+    nc, ns, plan = cfg.derived()
+    status = _lib().sdv2_mx4_dequantize(cfg, _buffer(codes, "codes", _U8, nc, dev), _buffer(scales, "scales", _U8, ns, dev),
+                                        _view(y, "y", *plan, dev), _stream(stream))
     if status:
         _b._check(status, "sdv2_mx4_dequantize")
 
@@ -145,37 +169,39 @@ def mx4_dequantize(cfg, codes, scales, y, stream=None):
 def mx4_product(cfg, a_codes, a_scales, b_codes, b_scales, out, ws, bias=None, stream=None):
     """out [rows][cols] = act(a b^T + bias) of matrices that mx4_quantize wrote: a of `rows` and b of `cols` rows, both of
     `depth` columns; bias: fp32 [cols]; ws: mx4_workspace_bytes(cfg) bytes."""
-    op = _Operands()
-    ac, asc, bc, bsc, nb, nw, (kind, shape, strides, span) = cfg.derived()
-    status = _lib().sdv2_mx4_product(ctypes.byref(cfg), op(a_codes, "a_codes", _U8, ac, True), op(a_scales, "a_scales", _U8, asc, True),
-                                     op(b_codes, "b_codes", _U8, bc, True), op(b_scales, "b_scales", _U8, bsc, True),
-                                     op(bias, "bias", _FP, nb, True), op.view(out, "out", kind, shape, strides, span),
-                                     op(ws, "ws", _U8, nw, True), _stream(stream))
+    dev = _here(out)
+    ac, asc, bc, bsc, nb, nw, plan = cfg.derived()
+    status = _lib().sdv2_mx4_product(cfg, _buffer(a_codes, "a_codes", _U8, ac, dev), _buffer(a_scales, "a_scales", _U8, asc, dev),
+                                     _buffer(b_codes, "b_codes", _U8, bc, dev), _buffer(b_scales, "b_scales", _U8, bsc, dev),
+                                     None if bias is None else _buffer(bias, "bias", _FP, nb, dev), _view(out, "out", *plan, dev),
+                                     _buffer(ws, "ws", _U8, nw, dev), _stream(stream))
     if status:
         _b._check(status, "sdv2_mx4_product")
 
 
-def _turn(name, cfg, positions, q, q_new, k, k_new, backward, stream):
-    op = _Operands()
+def _turn(cfg, positions, q, q_new, k, k_new, backward, stream):
+    dev = _here(q)
     kind, q_in, q_out, k_in, k_out, np = cfg.derived()
     if backward:
         q_in, q_out, k_in, k_out = q_out, q_in, k_out, k_in
-    names = ("dq_out", "dq", "dk_out", "dk") if backward else ("q", "q_out", "k", "k_out")
-    if not cfg.kv_heads:
-        k = k_new = None
-    status = getattr(_lib(), name)(ctypes.byref(cfg), op(positions, "positions", torch.int32, np, True),
-                                   op.view(q, names[0], kind, *q_in), op.view(q_new, names[1], kind, *q_out),
-                                   op.view(k, names[2], kind, *k_in), op.view(k_new, names[3], kind, *k_out), _stream(stream))
+        names, call = ("dq_out", "dq", "dk_out", "dk"), _lib().sdv2_axes_rope_backward
+    else:
+        names, call = ("q", "q_out", "k", "k_out"), _lib().sdv2_axes_rope
+    pk = pk_new = None
+    if cfg.kv_heads:
+        pk, pk_new = _view(k, names[2], kind, *k_in, dev), _view(k_new, names[3], kind, *k_out, dev)
+    status = call(cfg, _buffer(positions, "positions", torch.int32, np, dev), _view(q, names[0], kind, *q_in, dev),
+                  _view(q_new, names[1], kind, *q_out, dev), pk, pk_new, _stream(stream))
     if status:
-        _b._check(status, name)
+        _b._check(status, "sdv2_axes_rope_backward" if backward else "sdv2_axes_rope")
 
 
 def axes_rope(cfg, positions, q, q_out, k=None, k_out=None, stream=None):
     """q, q_out: [batch][tokens][heads][head_dim], k, k_out: [batch][tokens][kv_heads][head_dim] with cfg's strides;
     positions: int32 [batch][tokens][axes], or [tokens][axes] shared by the batch."""
-    _turn("sdv2_axes_rope", cfg, positions, q, q_out, k, k_out, False, stream)
+    _turn(cfg, positions, q, q_out, k, k_out, False, stream)
 
 
 def axes_rope_backward(cfg, positions, dq_out, dq, dk_out=None, dk=None, stream=None):
     """Gradients dq (cfg.q_in's strides) and dk (cfg.k_in's) from those of axes_rope's results."""
-    _turn("sdv2_axes_rope_backward", cfg, positions, dq_out, dq, dk_out, dk, True, stream)
+    _turn(cfg, positions, dq_out, dq, dk_out, dk, True, stream)

@@ -1,11 +1,12 @@
 // Rotary positions of several axes, forward and backward (the rotation by the negative angle).
 //
 // Every element is read and written once, so that memory bounds this.  A thread owns the same pairs of dims in many heads of a
-// token: it finds their sines and cosines once and then only loads, turns and stores.
+// token: it finds their sines and cosines once and then only loads, turns and stores, four heads' loads under way together.  Pairs
+// of neighbours lie in one vector of 16 bytes; pairs half a segment apart in two, as wide as every half segment is whole vectors of.
 // An angle in turns is position * scale * base^(-2j/d) / 2pi.  Its frequency is held as a 64-bit fraction of a turn (whole
 // turns of it change nothing), so that the 64-bit product with the position, which wraps around, is the fraction of a turn that
 // is left: off by 2^-64 of a turn per position.  The nearest quarter turn is taken off before the rest, at most an eighth, goes
-// to fp32, where it is off by 2^-28 of a turn at most.
+// to fp32, where it is off by 2^-28 of a turn at most; sine and cosine of that are sums of their Taylor series.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -16,154 +17,152 @@
 namespace sdv2 {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;              // of a block, at most: whole rows of items
 constexpr int kBatch = 4;                  // heads whose loads are under way together
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turn)
 {
     const uint32_t t = static_cast<uint32_t>(turn >> 32);
     const uint32_t quarter = (t + 0x20000000u) >> 30;
-    const float rest = static_cast<float>(static_cast<int32_t>(t - (quarter << 30))) * 0x1p-31f;   // half turns, at most a quarter
-    float s, c;
-    sincospif(rest, &s, &c);
-    float2 r;
-    r.x = quarter & 1 ? s : c;
-    r.y = quarter & 1 ? c : s;
-    if (quarter == 1 || quarter == 2) r.x = -r.x;
-    if (quarter & 2) r.y = -r.y;
-    return r;
+    const float a = static_cast<float>(static_cast<int32_t>(t - (quarter << 30))) * (6.2831853071795865f * 0x1p-32f);
+    const float a2 = a * a;
+    // terms up to a^9/9! and a^10/10!: at a = pi/4 the next are 2^-29 and 2^-33
+    float s = fmaf(a2, 1.0f / 362880, -1.0f / 5040);
+    s = fmaf(a2, s, 1.0f / 120);
+    s = fmaf(a2, s, -1.0f / 6);
+    s = fmaf(a * a2, s, a);
+    float c = fmaf(a2, -1.0f / 3628800, 1.0f / 40320);
+    c = fmaf(a2, c, -1.0f / 720);
+    c = fmaf(a2, c, 1.0f / 24);
+    c = fmaf(a2, c, -0.5f);
+    c = fmaf(a2, c, 1.0f);
+    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+    // a quarter turn takes (c, s) to (-s, c)
+    return make_float2(__uint_as_float(__float_as_uint(x) ^ ((quarter + 1) << 30 & 0x80000000u)),
+                       __uint_as_float(__float_as_uint(y) ^ (quarter << 30 & 0x80000000u)));
 }
 
-template <typename T>
-__device__ __forceinline__ float widen(T x) { return static_cast<float>(x); }
-template <>
-__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T narrow(float x) { return static_cast<T>(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// 16 bytes as elements.
-template <typename T>
-struct Vec {
-    static constexpr int n = 16 / sizeof(T);
-    union {
-        uint4 bits;
-        T e[16 / sizeof(T)];
-    };
-    __device__ __forceinline__ Vec() {}
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Pack {
+    T e[N];
 };
 
-template <typename T>
-__device__ __forceinline__ void turn_pair(T& u, T& v, float2 cs, bool turns)
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <int N>
+__device__ __forceinline__ void narrow(Pack<float, N>& p, const float (&x)[N])
 {
-    if (!turns) return;
-    const float a = widen<T>(u), b = widen<T>(v);
-    u = narrow<T>(fmaf(a, cs.x, -(b * cs.y)));
-    v = narrow<T>(fmaf(a, cs.y, b * cs.x));
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.e[i] = x[i];
 }
 
-template <typename T, RopeLayout L>
+template <int N>
+__device__ __forceinline__ void narrow(Pack<__nv_bfloat16, N>& p, const float (&x)[N])
+{
+    if constexpr (N == 1) {
+        p.e[0] = __float2bfloat16_rn(x[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(x[i], x[i + 1]);
+            p.e[i] = two.x;
+            p.e[i + 1] = two.y;
+        }
+    }
+}
+
+// N: elements of a vector; ADJACENT: one of pairs of neighbours, else two of their first and second elements; ALL: every dim turns.
+template <typename T, int N, bool ADJACENT, bool ALL>
 __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_constant__ AxesRopeParams p)
 {
-    constexpr int VE = Vec<T>::n;
-    constexpr int P = L == RopeLayout::adjacent ? VE / 2 : L == RopeLayout::halves ? VE : 1;   // pairs of a thread
-    wait_for_launch_before();
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t place = g / p.items;                       // b * tokens + n
-    if (place >= p.batch * p.tokens) return;
-    const int item = static_cast<int>(g - place * p.items);
-    const int64_t b = place / p.tokens, n = place - b * p.tokens;
-    const int32_t* pos = p.positions + (p.shared ? n : place) * p.axes;
-    float2 cs[P];
-    bool turns[P];
-    const int u0 = p.pair[item * P].u, v0 = p.pair[item * P].v;
+    constexpr int P = ADJACENT ? N / 2 : N, V = ADJACENT ? 1 : 2;
+    const int place = threadIdx.x / p.items, item = threadIdx.x - place * p.items;
+    const int together = blockDim.x / p.items;               // tokens of a block
+    const bool second = blockIdx.y >= p.q_parts;
+    const RopeTensor& t = p.t[second];
+    const int h0 = (second ? blockIdx.y - p.q_parts : blockIdx.y) * p.per;
+    const int heads = min(p.per, (second ? p.kv_heads : p.heads) - h0);
+    uint64_t turn[P];
+    int axis[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const RopePair& r = p.pair[item * P + i];
-        turns[i] = r.axis >= 0;
-        cs[i] = make_float2(1.0f, 0.0f);
-        if (turns[i]) cs[i] = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos[r.axis])) * r.turn);
+        turn[i] = p.pair[item * P + i].turn;
+        axis[i] = p.pair[item * P + i].axis;
     }
-    const int all = p.heads + p.kv_heads;
-    const int last = min(all, static_cast<int>(blockIdx.y + 1) * p.per);
-    for (int h0 = blockIdx.y * p.per; h0 < last; h0 += kBatch) {
-        const T* in[kBatch];
-        T* out[kBatch];
+    const int u0 = p.pair[item * P].u, v0 = p.pair[item * P].v;
+    const T* const in0 = static_cast<const T*>(t.in) + blockIdx.z * t.is.batch_stride + h0 * t.is.head_stride + u0;
+    T* const out0 = static_cast<T*>(t.out) + blockIdx.z * t.os.batch_stride + h0 * t.os.head_stride + u0;
+    const int32_t* const pos0 = p.positions + (p.shared ? 0 : blockIdx.z * p.tokens * p.axes);
+    wait_for_launch_before();
+    for (int64_t n = static_cast<int64_t>(blockIdx.x) * together + place; n < p.tokens; n += static_cast<int64_t>(gridDim.x) * together) {
+        float2 cs[P];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int h = min(h0 + i, last - 1);
-            const RopeTensor& t = p.t[h >= p.heads];
-            const int64_t hh = h >= p.heads ? h - p.heads : h;
-            in[i] = static_cast<const T*>(t.in) + b * t.is.batch_stride + n * t.is.token_stride + hh * t.is.head_stride;
-            out[i] = static_cast<T*>(t.out) + b * t.os.batch_stride + n * t.os.token_stride + hh * t.os.head_stride;
-        }
-        if constexpr (L == RopeLayout::single) {
-            T u[kBatch], v[kBatch];
+        for (int i = 0; i < P; ++i) cs[i] = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos0[n * p.axes + max(axis[i], 0)])) * turn[i]);
+        const T* in = in0 + n * t.is.token_stride;
+        T* out = out0 + n * t.os.token_stride;
+        for (int h = 0; h < heads; h += kBatch) {
+            Pack<T, N> x[kBatch][V];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) u[i] = in[i][u0], v[i] = in[i][v0];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (h0 + i < last) {
-                    turn_pair<T>(u[i], v[i], cs[0], turns[0]);
-                    out[i][u0] = u[i];
-                    out[i][v0] = v[i];
-                }
-        } else if constexpr (L == RopeLayout::adjacent) {
-            Vec<T> x[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) x[i].bits = *reinterpret_cast<const uint4*>(in[i] + u0);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (h0 + i < last) {
-#pragma unroll
-                    for (int j = 0; j < P; ++j) turn_pair<T>(x[i].e[2 * j], x[i].e[2 * j + 1], cs[j], turns[j]);
-                    *reinterpret_cast<uint4*>(out[i] + u0) = x[i].bits;
-                }
-        } else {
-            Vec<T> u[kBatch], v[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                u[i].bits = *reinterpret_cast<const uint4*>(in[i] + u0);
-                v[i].bits = *reinterpret_cast<const uint4*>(in[i] + v0);
+            for (int b = 0; b < kBatch; ++b) {
+                const T* from = in + min(b, heads - 1 - h) * t.is.head_stride;
+                x[b][0] = *reinterpret_cast<const Pack<T, N>*>(from);
+                if constexpr (!ADJACENT) x[b][1] = *reinterpret_cast<const Pack<T, N>*>(from + (v0 - u0));
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (h0 + i < last) {
+            for (int b = 0; b < kBatch; ++b) {
+                if (h + b >= heads) break;
+                float y[V][N];
 #pragma unroll
-                    for (int j = 0; j < P; ++j) turn_pair<T>(u[i].e[j], v[i].e[j], cs[j], turns[j]);
-                    *reinterpret_cast<uint4*>(out[i] + u0) = u[i].bits;
-                    *reinterpret_cast<uint4*>(out[i] + v0) = v[i].bits;
+                for (int i = 0; i < P; ++i) {
+                    const float u = widen(ADJACENT ? x[b][0].e[2 * i] : x[b][0].e[i]);
+                    const float v = widen(ADJACENT ? x[b][0].e[2 * i + 1] : x[b][V - 1].e[i]);
+                    float a = fmaf(u, cs[i].x, -(v * cs[i].y)), c = fmaf(u, cs[i].y, v * cs[i].x);
+                    if constexpr (!ALL)
+                        if (axis[i] < 0) a = u, c = v;
+                    y[0][ADJACENT ? 2 * i : i] = a;
+                    y[V - 1][ADJACENT ? 2 * i + 1 : i] = c;
                 }
+                T* to = out + b * t.os.head_stride;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    Pack<T, N> w;
+                    narrow(w, y[i]);
+                    *reinterpret_cast<Pack<T, N>*>(to + (i ? v0 - u0 : 0)) = w;
+                }
+            }
+            in += kBatch * t.is.head_stride;
+            out += kBatch * t.os.head_stride;
         }
     }
 }
 
-template <typename T>
-cudaError_t launch(const AxesRopeParams& p, RopeLayout layout, dim3 grid, cudaStream_t s)
+template <typename T, int N, bool ADJACENT>
+cudaError_t launch(AxesRopeParams& p, bool all, int head_dim, cudaStream_t s)
 {
-    auto kernel = layout == RopeLayout::adjacent ? axes_rope_kernel<T, RopeLayout::adjacent>
-                : layout == RopeLayout::halves   ? axes_rope_kernel<T, RopeLayout::halves>
-                                                 : axes_rope_kernel<T, RopeLayout::single>;
-    return launch_chained(kernel, grid, kThreads, 0, s, p);
+    p.items = head_dim / (ADJACENT ? N : 2 * N);
+    const int together = std::max(1, kThreads / p.items);
+    const int64_t places = (p.tokens + together - 1) / together;
+    // Heads of a thread: all of a tensor's, unless that leaves SMs without work; a part of them costs its sines and cosines again.
+    constexpr int64_t kFull = 152 * 12;
+    const int heads = std::max(p.heads, p.kv_heads), tensors = p.kv_heads ? 2 : 1;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((heads + kBatch - 1) / kBatch, kFull / std::max<int64_t>(1, places * p.batch * tensors)));
+    p.per = static_cast<int>((heads + parts - 1) / parts + kBatch - 1) / kBatch * kBatch;
+    p.q_parts = (p.heads + p.per - 1) / p.per;
+    const int all_parts = p.q_parts + (p.kv_heads + p.per - 1) / p.per;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(places, INT32_MAX)), static_cast<unsigned>(all_parts), static_cast<unsigned>(p.batch));
+    return launch_chained(all ? axes_rope_kernel<T, N, ADJACENT, true> : axes_rope_kernel<T, N, ADJACENT, false>, grid, together * p.items, 0, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_axes_rope(AxesRopeParams& p, RopeLayout layout, bool f32, int head_dim, cudaStream_t s)
+cudaError_t launch_axes_rope(AxesRopeParams& p, bool adjacent, int width, bool all, bool f32, int head_dim, cudaStream_t s)
 {
-    const int lane = f32 ? 4 : 8;
-    p.items = layout == RopeLayout::adjacent ? head_dim / lane : layout == RopeLayout::halves ? head_dim / lane / 2 : head_dim / 2;
-    const int64_t threads = p.batch * p.tokens * p.items;
-    const int64_t blocks = (threads + kThreads - 1) / kThreads;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    // Heads of a thread: all, unless that leaves SMs without work; a part of them costs its sines and cosines again.
-    const int all = p.heads + p.kv_heads;
-    constexpr int64_t kFull = 152 * 8;
-    const int64_t parts = std::min<int64_t>({(all + kBatch - 1) / kBatch, std::max<int64_t>(1, kFull / blocks), 65535});
-    p.per = static_cast<int>((all + parts - 1) / parts + kBatch - 1) / kBatch * kBatch;
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((all + p.per - 1) / p.per));
-    return f32 ? launch<float>(p, layout, grid, s) : launch<__nv_bfloat16>(p, layout, grid, s);
+    if (adjacent) return f32 ? launch<float, 4, true>(p, all, head_dim, s) : launch<__nv_bfloat16, 8, true>(p, all, head_dim, s);
+    if (f32) return width == 4 ? launch<float, 4, false>(p, all, head_dim, s) : width == 2 ? launch<float, 2, false>(p, all, head_dim, s)
+                                                                                         : launch<float, 1, false>(p, all, head_dim, s);
+    return width == 8 ? launch<__nv_bfloat16, 8, false>(p, all, head_dim, s)
+         : width == 2 ? launch<__nv_bfloat16, 2, false>(p, all, head_dim, s) : launch<__nv_bfloat16, 1, false>(p, all, head_dim, s);
 }
 
 }  // namespace sdv2

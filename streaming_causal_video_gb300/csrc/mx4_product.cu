@@ -8,8 +8,8 @@
 // CTA's own 128 rows of a, and those of all 256 rows of b, which both CTAs read.
 //   warp 0: TMA producer (both CTAs load into their own shared memory and count the bytes on the leader's stage barrier, which
 //   the leader arms for both); warp 1: in the leader, scale copies and MMAs, whose commits arrive on the barriers of both CTAs;
-//   warps 2-9: epilogue, two per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 128 bytes of a row at a time go
-//   through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
+//   warps 2-17: epilogue, four per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 64
+//   bytes of a row at a time go through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
 // Where tiles are fewer than pairs, the depth is cut into parts; their sums go to the workspace in fp32 and a second kernel adds
 // them in order, so that results do not depend on which part ends first.
 #include <cuda_bf16.h>
@@ -30,29 +30,41 @@
 namespace sdv2 {
 namespace {
 
-constexpr int TM = 256, TN = 256;              // rows of a and of b in a pair tile
-constexpr int CM = TM / 2, CN = TN / 2;        // and in each CTA
+constexpr int TM = 256, CM = TM / 2;           // rows of a in a pair tile and in each CTA
 constexpr int STEP_TILES = 2;                  // scale tiles (128 columns) of a stage
-constexpr int STAGES = 5;
-constexpr uint32_t A_BYTES = CM * 128, B_BYTES = CN * 128;
-constexpr uint32_t AS_BYTES = STEP_TILES * 512, BS_BYTES = 2 * STEP_TILES * 512;
-constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
-constexpr uint32_t OUT_BYTES = 32 * 128;       // a warp's staging of its rows
-// Tensor memory: the sums of two tiles, the second's 256 columns beginning with the first's last 32, and behind them the scales of
-// a and of b.  The epilogue takes the shared columns of a tile first, and the next tile begins when they are free.
-constexpr uint32_t COL_SECOND = TN - 32, COL_AS = COL_SECOND + TN, COL_BS = COL_AS + 4 * STEP_TILES, TMEM_COLS = 512;
-static_assert(COL_BS + 8 * STEP_TILES <= TMEM_COLS, "tensor memory");
-constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 2, B_SHARED = 2 * STAGES + 4,
-              B_DONE = 2 * STAGES + 5, NBARS = 2 * STAGES + 6;
-constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;
-constexpr uint32_t BIAS_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
-constexpr uint32_t BAR_OFF = BIAS_OFF + EPI_WARPS * (TN / 2) * 4;
-constexpr uint32_t SMEM_BYTES = BAR_OFF + 256 + 1024;
 constexpr uint16_t kBothCtas = 3;
-static_assert(STAGE_BYTES % 1024 == 0 && A_BYTES % 1024 == 0 && OUT_OFF % 1024 == 0, "128-byte swizzle");
-static_assert(NBARS * 8 + 16 <= 256 && SMEM_BYTES <= 232448, "shared memory");
+
+// What depends on the rows of b in a pair tile.
+template <int TN>
+struct Tile {
+    static constexpr int CN = TN / 2;                                  // rows of b in each CTA
+    static constexpr int STAGES = TN == 256 ? 5 : 6;
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 2, B_SHARED = 2 * STAGES + 4,
+                         B_DONE = 2 * STAGES + 5, NBARS = 2 * STAGES + 6;
+    static constexpr uint32_t A_BYTES = CM * 128, B_BYTES = CN * 128;
+    static constexpr uint32_t AS_BYTES = STEP_TILES * 512, BS_BYTES = 2 * STEP_TILES * 512;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
+    static constexpr uint32_t STAGE_PITCH = (STAGE_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t OUT_BYTES = 32 * 64;                     // a warp's staging of its rows
+    static constexpr uint32_t OUT_OFF = STAGES * STAGE_PITCH;
+    static constexpr uint32_t BIAS_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
+    static constexpr uint32_t BAR_OFF = BIAS_OFF + EPI_WARPS * 64 * 4;
+    static constexpr uint32_t SMEM_BYTES = BAR_OFF + 256 + 1024;
+    // Tensor memory: the sums of two tiles, and behind them the scales of a and of b of a step.  Two tiles of 256 columns do
+    // not fit beside the scales: the second begins with the first's last 32.  The epilogue takes the shared columns of a tile
+    // first, and the next tile begins when they are free, about 1300 cycles behind the last one's end; tiles of 192 columns
+    // follow at once.
+    static constexpr bool SHARES = TN == 256;
+    static constexpr uint32_t COL_SECOND = SHARES ? TN - 32 : TN;
+    static constexpr uint32_t COL_AS = COL_SECOND + TN, COL_BS = COL_AS + 4 * STEP_TILES;
+    static_assert(TN == 256 || TN == 192, "rows of b from a multiple of 64 on, in two scale tiles");
+    static_assert(COL_AS + 12 * STEP_TILES <= 512, "tensor memory");
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && OUT_OFF % 1024 == 0, "128-byte swizzle");
+    static_assert(NBARS * 8 + 16 <= 256 && SMEM_BYTES <= 232448, "shared memory");
+};
+constexpr uint32_t TMEM_COLS = 512;
 
 struct ProductParams {
     CUtensorMap a, as, b, bs, out;             // out: the result, or partial sums
@@ -62,22 +74,49 @@ struct ProductParams {
     uint32_t* err;
     uint64_t timeout_ns;
     int64_t drop;
-    int32_t M, N, mtiles, ntiles, steps, splits;
-    int32_t m_fastest, gelu;
+    int32_t M, N, steps, splits, units;
+    int32_t m_fastest, inner;                  // whether the tiles of a vary fastest, and how many there are
+    int32_t step_i, step_j;                    // the grid's pairs in whole rows of them and the rest
+    int32_t gelu;
 };
 
+// A pair's tiles and parts of the depth, one after the other.
 struct Unit {
-    int m0, n0, split, first, last;            // tile's first rows, part of the depth and its steps
-    __device__ __forceinline__ Unit(const ProductParams& p, int u)
+    int u, i, j;                               // place in the grid's inner and outer direction
+    int m0, n0, split, first, last;            // the tile's first rows, the part of the depth and its steps
+    __device__ __forceinline__ Unit(const ProductParams& p, int u_, int tn) : u(u_) { find(p, tn); }
+    // The unit `pairs` places on: without divisions where the depth is whole, as these are in the way of the next MMAs.
+    __device__ __forceinline__ void next(const ProductParams& p, int pairs, int tn)
+    {
+        u += pairs;
+        if (p.splits == 1) {
+            i += p.step_i;
+            j += p.step_j;
+            if (i >= p.inner) {
+                i -= p.inner;
+                ++j;
+            }
+            place(p, tn);
+        } else {
+            find(p, tn);
+        }
+    }
+
+private:
+    __device__ __forceinline__ void find(const ProductParams& p, int tn)
     {
         const int t = u / p.splits;
         split = u - t * p.splits;
-        first = static_cast<int>(static_cast<int64_t>(p.steps) * split / p.splits);
-        last = static_cast<int>(static_cast<int64_t>(p.steps) * (split + 1) / p.splits);
-        const int j = t / (p.m_fastest ? p.mtiles : p.ntiles);
-        const int i = t - j * (p.m_fastest ? p.mtiles : p.ntiles);
+        first = p.steps / p.splits * split + min(split, p.steps % p.splits);
+        last = first + p.steps / p.splits + (split < p.steps % p.splits);
+        j = t / p.inner;
+        i = t - j * p.inner;
+        place(p, tn);
+    }
+    __device__ __forceinline__ void place(const ProductParams& p, int tn)
+    {
         m0 = (p.m_fastest ? i : j) * TM;
-        n0 = (p.m_fastest ? j : i) * TN;
+        n0 = (p.m_fastest ? j : i) * tn;
     }
 };
 
@@ -94,39 +133,53 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v)
     return pack2(lo, hi);
 }
 
-// Rows of out that TMA cannot write: a warp stores a row's 128 staged bytes number by number.
+__device__ __forceinline__ void tmem_ld_sync(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32_sync(taddr, r); }
+__device__ __forceinline__ void tmem_ld_sync(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16_sync(taddr, r); }
+
+// Rows of out that TMA cannot write: a warp stores the 64 staged bytes of its rows number by number, a row (bf16) or two (fp32) at
+// a time, with eight of them under way.
 template <bool F32>
-__device__ __noinline__ void store_rows(const ProductParams& p, const uint8_t* stage, int row0, int n)
+__device__ __forceinline__ void store_rows(const ProductParams& p, const uint8_t* stage, int row0, int n)
 {
-    const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
-    constexpr int PER = F32 ? 4 : 8;
-    for (int r = 0; r < rows; ++r)
-        for (int j = lane; j < 8 * PER; j += 32) {
-            if (n + j >= p.N) continue;
-            const uint8_t* at = stage + r * 128 + (((j / PER) ^ (r & 7)) << 4);
-            const int64_t o = (row0 + r) * p.out_stride + n + j;
-            if constexpr (F32) static_cast<float*>(p.direct)[o] = reinterpret_cast<const float*>(at)[j % PER];
-            else static_cast<uint16_t*>(p.direct)[o] = reinterpret_cast<const uint16_t*>(at)[j % PER];
-        }
+    constexpr int COLS = F32 ? 16 : 32, ROWS = 32 / COLS, PER = F32 ? 4 : 8;
+    const int lane = threadIdx.x & 31, j = lane % COLS, first = lane / COLS;
+    if (n + j >= p.N) return;
+    const int rows = min(32, p.M - row0);
+    const int64_t at = (row0 + first) * p.out_stride + n + j;
+#pragma unroll 8
+    for (int i = 0; i < 32 / ROWS; ++i) {
+        const int r = first + i * ROWS;
+        if (r >= rows) break;
+        const uint8_t* from = stage + r * 64 + (((j / PER) ^ ((r >> 1) & 3)) << 4);
+        const int64_t o = at + i * ROWS * p.out_stride;
+        if constexpr (F32) static_cast<float*>(p.direct)[o] = reinterpret_cast<const float*>(from)[j % PER];
+        else static_cast<uint16_t*>(p.direct)[o] = reinterpret_cast<const uint16_t*>(from)[j % PER];
+    }
 }
 
-template <bool F32>
+template <int TN, bool F32>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductParams p)
 {
+    using T = Tile<TN>;
+    constexpr uint32_t A_BYTES = T::A_BYTES, B_BYTES = T::B_BYTES, AS_BYTES = T::AS_BYTES, STAGE_BYTES = T::STAGE_BYTES;
+    constexpr uint32_t COL_AS = T::COL_AS, COL_BS = T::COL_BS;
+    constexpr int STAGES = T::STAGES, B_FULL = T::B_FULL, B_EMPTY = T::B_EMPTY, B_ACC_FULL = T::B_ACC_FULL,
+                  B_ACC_EMPTY = T::B_ACC_EMPTY, B_SHARED = T::B_SHARED, B_DONE = T::B_DONE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::BAR_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + T::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* peer_steps = abort_flag + 1;
+    volatile int* peer_abort = abort_flag + 1;
+    volatile int* peer_steps = abort_flag + 2;
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());            // 0: the leader, which issues the MMAs
     const int pair = static_cast<int>(cluster_id_x()), pairs = static_cast<int>(cluster_count_x());
-    const int units = p.mtiles * p.ntiles * p.splits;
+    const int units = p.units;
     const uint64_t tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -135,9 +188,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             mbar_init(bar(B_ACC_FULL + i), 1);
             mbar_init(bar(B_ACC_EMPTY + i), 2 * EPI_WARPS);
         }
-        mbar_init(bar(B_SHARED), EPI_WARPS);       // half of the warps of each CTA
+        mbar_init(bar(B_SHARED), EPI_WARPS / 2);   // a quarter of the warps of each CTA
         mbar_init(bar(B_DONE), 1);
         *abort_flag = 0;
+        *peer_abort = 0;
         *peer_steps = 0;
         fence_mbar_init();
     }
@@ -163,17 +217,16 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             tma_prefetch_desc(&p.b);
             const uint32_t full_leader = map_to_rank(bar(B_FULL), 0);
             bool ok = true;
-            for (int u = pair; ok && u < units; u += pairs) {
-                const Unit t(p, u);
-                const int m0 = t.m0 + rank * CM, n0 = t.n0 + rank * CN;
+            for (Unit t(p, pair, TN); ok && t.u < units; t.next(p, pairs, TN)) {
+                const int m0 = t.m0 + rank * CM, n0 = t.n0 + rank * T::CN;
                 for (int k = t.first; k < t.last; ++k) {
                     const int st = issued % STAGES;
-                    if (!mbar_wait_cluster_bounded(bar(B_EMPTY + st), (static_cast<uint32_t>(issued / STAGES) & 1u) ^ 1u, tmo, abort_flag)) {
+                    if (!mbar_wait_bounded(bar(B_EMPTY + st), (static_cast<uint32_t>(issued / STAGES) & 1u) ^ 1u, tmo, abort_flag)) {
                         give_up();
                         ok = false;
                         break;
                     }
-                    const uint32_t sa = s0 + st * STAGE_BYTES, fb = full_leader + 8u * static_cast<uint32_t>(st);
+                    const uint32_t sa = s0 + st * T::STAGE_PITCH, fb = full_leader + 8u * static_cast<uint32_t>(st);
                     if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2 * STAGE_BYTES);
                     ++issued;
                     if (k == p.drop) continue;
@@ -193,40 +246,36 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             const uint64_t dAS = sdesc_scales(s0 + A_BYTES + B_BYTES);
             const uint64_t dBS = sdesc_scales(s0 + A_BYTES + B_BYTES + AS_BYTES);
             auto wait = [&](int i, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar(i), parity, tmo, abort_flag));
+                return __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity, tmo, abort_flag));
             };
             bool ok = true;
-            int g = 0, li = 0;
-            for (int u = pair; ok && u < units; u += pairs, ++li) {
-                const Unit t(p, u);
+            int li = 0, st = 0;                                      // tiles so far; the ring's stage, its phase and its offset
+            uint32_t phase = 0;
+            uint64_t at = 0;
+            for (Unit t(p, pair, TN); ok && t.u < units; t.next(p, pairs, TN), ++li) {
                 const int buf = li & 1;
                 // the tile before last has been read, and of the last one the columns that both use
-                if (!wait(B_ACC_EMPTY + buf, (static_cast<uint32_t>(li >> 1) & 1u) ^ 1u) ||
-                    (li > 0 && !wait(B_SHARED, static_cast<uint32_t>(li - 1) & 1u))) {
-                    ok = false;
-                    break;
-                }
+                ok = wait(B_ACC_EMPTY + buf, (static_cast<uint32_t>(li >> 1) & 1u) ^ 1u) &&
+                     (!T::SHARES || li == 0 || wait(B_SHARED, static_cast<uint32_t>(li - 1) & 1u));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + (buf ? COL_SECOND : 0u);
-                for (int k = t.first; k < t.last; ++k, ++g) {
-                    const int st = g % STAGES;
-                    if (!wait(B_FULL + st, static_cast<uint32_t>(g / STAGES) & 1u)) {
+                const uint32_t acc = tmem + (buf ? T::COL_SECOND : 0u);
+                const uint32_t b_scales = tmem + COL_BS + static_cast<uint32_t>(t.n0 / 32 % 4);    // of the tile's first row
+                for (int k = t.first; k < t.last; ++k) {
+                    if (!wait(B_FULL + st, phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t at = static_cast<uint64_t>(st) * (STAGE_BYTES >> 4);
-#pragma unroll
-                    for (int c = 0; c < STEP_TILES; ++c) {
-                        scales_to_tmem_pair_warp(tmem + COL_AS + 4 * c, dAS + at + c * 32);
-                        scales_to_tmem_pair_warp(tmem + COL_BS + 8 * c, dBS + at + c * 32);
-                        scales_to_tmem_pair_warp(tmem + COL_BS + 8 * c + 4, dBS + at + (STEP_TILES + c) * 32);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_mx4_pair_warp(acc, dA + at + 2 * i, dB + at + 2 * i, (i & 1) ? idesc_mx4(TM, TN, 1) : idesc_mx4(TM, TN, 0),
-                                          tmem + COL_AS + 4 * (i >> 1), tmem + COL_BS + 8 * (i >> 1), (k > t.first || i > 0) ? 1u : 0u);
+                    mx4_stage_pair_warp(acc, dA + at, dB + at, dAS + at, dBS + at, tmem + COL_AS, tmem + COL_BS, b_scales, idesc_mx4(TM, TN, 0),
+                                        idesc_mx4(TM, TN, 1), k > t.first ? 1u : 0u);
                     mma_commit_pair_warp(bar(B_EMPTY + st), kBothCtas);
+                    at += T::STAGE_PITCH >> 4;
+                    if (++st == STAGES) {
+                        st = 0;
+                        at = 0;
+                        phase ^= 1u;
+                    }
                 }
                 if (!ok) break;
                 mma_commit_pair_warp(bar(B_ACC_FULL + buf), kBothCtas);
@@ -240,53 +289,52 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         }
         __syncwarp();
     } else {
-        const int part = (warp - 2) >> 2, quarter = warp & 3;
-        const int col0 = part * (TN / 2);
-        constexpr int PIECE = 32, PIECES = TN / 2 / PIECE;           // columns that a thread has at once
-        constexpr int TOGETHER = F32 ? 1 : 2;                        // pieces that make 128 bytes
-        uint8_t* stage = smem + OUT_OFF + (warp - 2) * OUT_BYTES;
-        float* bias = reinterpret_cast<float*>(smem + BIAS_OFF) + (warp - 2) * (TN / 2);
+        // Four warps per quarter, 64 columns each; of 192 columns another one has none in each tile.
+        const int group = (warp - 2) >> 2, quarter = warp & 3;
+        constexpr int PIECE = F32 ? 16 : 32, PIECES = 64 / PIECE;    // columns that a thread has at once: 64 bytes of a row
+        uint8_t* stage = smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES;
+        float* bias = reinterpret_cast<float*>(smem + T::BIAS_OFF) + (warp - 2) * 64;
         const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), 0), shared_leader = map_to_rank(bar(B_SHARED), 0);
         const bool whole = p.splits == 1;                            // else partial sums
         int li = 0;
-        for (int u = pair; u < units; u += pairs, ++li) {
-            const Unit t(p, u);
+        for (Unit t(p, pair, TN); t.u < units; t.next(p, pairs, TN), ++li) {
             const int buf = li & 1;
-            const int row0 = t.m0 + rank * CM + quarter * 32;
-#pragma unroll
-            for (int j = 0; j < TN / 2 / 32; ++j) {
-                const int n = t.n0 + col0 + j * 32 + lane;
-                bias[j * 32 + lane] = whole && p.bias && n < p.N ? p.bias[n] : 0.0f;
+            const int place = T::SHARES ? group : (group + li) & 3;
+            const int row0 = t.m0 + rank * CM + quarter * 32, n0 = t.n0 + place * 64;
+            const bool mine = (T::SHARES || place < 3) && row0 < p.M && n0 < p.N;
+            if (mine) {
+                bias[lane] = whole && p.bias && n0 + lane < p.N ? p.bias[n0 + lane] : 0.0f;
+                bias[32 + lane] = whole && p.bias && n0 + 32 + lane < p.N ? p.bias[n0 + 32 + lane] : 0.0f;
             }
             __syncwarp();
-            const bool ok = mbar_wait_cluster_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
+            const bool ok = mbar_wait_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
             tc_fence_after();
-            const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(col0) + (buf ? COL_SECOND : 0u);
-            // the first buffer backwards: its last columns are the ones that the second shares
-            const int flip = buf ? 0 : PIECES - 1;
-            uint32_t raw[2][PIECE];
-            tmem_ld_x32_start(trow + (0 ^ flip) * PIECE, raw[0]);
+            // the arrivals order no memory but the loads of tensor memory before them
+            auto arrive = [&](uint32_t at) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(at);
+            };
+            // the first buffer's last columns and the second's first are the ones that both use
+            const bool shared = T::SHARES && place == (buf ? 0 : 3);
+            if (!mine) {
+                if (shared) arrive(shared_leader);
+                arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
+                continue;
+            }
+            const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (buf ? T::COL_SECOND : 0u) + static_cast<uint32_t>(place * 64);
+            const int flip = T::SHARES && buf == 0 ? PIECES - 1 : 0;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                uint32_t(&y)[PIECE] = raw[i & 1];
-                tmem_ld_x32_finish(y);
-                if (i == 0 && part != buf) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(shared_leader);
-                }
-                if (i + 1 < PIECES) {
-                    tmem_ld_x32_start(trow + ((i + 1) ^ flip) * PIECE, raw[(i + 1) & 1]);
-                } else {                                             // all sums have been read; the arrival orders no memory
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(empty_leader + 8u * static_cast<uint32_t>(buf));
-                }
                 const int c = (i ^ flip) * PIECE;
+                uint32_t y[PIECE];
+                tmem_ld_sync(trow + c, y);
+                if (shared && (i + 1) * PIECE == 32) arrive(shared_leader);
+                if (i == PIECES - 1) arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
                 uint64_t v[PIECE / 2];
 #pragma unroll
                 for (int j = 0; j < PIECE; j += 4) {
@@ -298,13 +346,11 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 #pragma unroll
                     for (int j = 0; j < PIECE / 2; ++j) v[j] = gelu2(v[j]);
                 }
-                if (i % TOGETHER == 0) {
-                    if (lane == 0) tma_store_wait_read();
-                    __syncwarp();
-                }
-                // 16-byte vectors of a row of 128 bytes, swizzled as TMA takes them
+                if (lane == 0) tma_store_wait_read();
+                __syncwarp();
+                // 16-byte vectors of a row's 64 bytes, swizzled as TMA takes them
 #pragma unroll
-                for (int j = 0; j < 8 / TOGETHER; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     uint4 w;
                     if constexpr (F32) {
                         w = make_uint4(static_cast<uint32_t>(v[2 * j]), static_cast<uint32_t>(v[2 * j] >> 32),
@@ -312,18 +358,15 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     } else {
                         w = make_uint4(pack2(v[4 * j]), pack2(v[4 * j + 1]), pack2(v[4 * j + 2]), pack2(v[4 * j + 3]));
                     }
-                    const int at = F32 ? j : j + 4 * ((i ^ flip) & 1);
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((at ^ (lane & 7)) << 4)) = w;
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
                 }
-                if (i % TOGETHER != TOGETHER - 1) continue;
-                const int n = t.n0 + col0 + (F32 ? c : c & ~63);
                 if (!p.direct) {
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0 && row0 < p.M && n < p.N) tma_store_3d(&p.out, smem_u32(stage), n, row0, t.split);
+                    if (lane == 0 && n0 + c < p.N) tma_store_3d(&p.out, smem_u32(stage), n0 + c, row0, t.split);
                 } else {
                     __syncwarp();
-                    store_rows<F32>(p, stage, row0, n);
+                    store_rows<F32>(p, stage, row0, n0 + c);
                     __syncwarp();
                 }
             }
@@ -333,20 +376,23 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_abort)), static_cast<uint32_t>(rank ^ 1)), 1);
     cluster_sync_all();          // no CTA leaves while the other may still signal or read it
-    if (threadIdx.x == 0 && rank == 0 && *abort_flag) {
+    if (*abort_flag || *peer_abort) {
         // The ring's copies land before the pair may go.  A step that only one of the two CTAs issued is squared up: armed for the
         // peer's copies alone, or told that the peer's do not come.
-        const int mine = issued, peer = *peer_steps;
-        for (int g = mine; g < peer; ++g) mbar_arrive_expect_tx(bar(B_FULL + g % STAGES), STAGE_BYTES);
-        for (int g = peer; g < mine; ++g) mbar_complete_tx(bar(B_FULL + g % STAGES), STAGE_BYTES);
-        const int end = max(mine, peer);
-        volatile int no_abort = 0;
-        for (int g = max(0, end - STAGES); g < end; ++g)
-            mbar_wait_cluster_bounded(bar(B_FULL + g % STAGES), static_cast<uint32_t>(g / STAGES) & 1u, tmo, &no_abort);
+        if (threadIdx.x == 0 && rank == 0) {
+            const int mine = issued, peer = *peer_steps;
+            for (int g = mine; g < peer; ++g) mbar_arrive_expect_tx(bar(B_FULL + g % STAGES), STAGE_BYTES);
+            for (int g = peer; g < mine; ++g) mbar_complete_tx(bar(B_FULL + g % STAGES), STAGE_BYTES);
+            const int end = max(mine, peer);
+            volatile int no_abort = 0;
+            for (int g = max(0, end - STAGES); g < end; ++g)
+                mbar_wait_cluster_bounded(bar(B_FULL + g % STAGES), static_cast<uint32_t>(g / STAGES) & 1u, tmo, &no_abort);
+        }
+        __syncthreads();
+        cluster_sync_all();
     }
-    __syncthreads();
-    cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, TMEM_COLS);
@@ -394,12 +440,12 @@ __global__ void __launch_bounds__(256) join_kernel(const float* part, const floa
 
 constexpr int kPairs = 76;                     // a pair for each TPC's two SMs
 
-// Codes: boxes of 128 bytes x 128 rows.
-bool codes_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles)
+// Codes: boxes of 128 bytes x `box_rows` rows.
+bool codes_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, int box_rows)
 {
     const cuuint64_t pitch = static_cast<cuuint64_t>(tiles) * kMx4TileBytes;
     const cuuint64_t dims[3] = {pitch, static_cast<cuuint64_t>(rows), 1}, strides[2] = {pitch, pitch * static_cast<cuuint64_t>(rows)};
-    const cuuint32_t box[3] = {128, 128, 1};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
     return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, map, base, 3, dims, strides, box);
 }
 
@@ -412,20 +458,22 @@ bool scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, 
     return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, map, base, 3, dims, strides, box);
 }
 
-// Results or partial sums: boxes of 128 bytes x 32 rows.
+// Results or partial sums: boxes of 64 bytes x 32 rows.
 bool out_map(CUtensorMap* map, const void* base, bool f32, int64_t M, int64_t N, int64_t stride, int splits)
 {
     const cuuint64_t pitch = static_cast<cuuint64_t>(stride) * (f32 ? 4 : 2);
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(splits)};
     const cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(M)};
-    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
-    return encode_tensor_map_of(f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint32_t box[3] = {f32 ? 16u : 32u, 32, 1};
+    return encode_tensor_map_of(f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B,
                                 map, base, 3, dims, strides, box);
 }
 
-template <bool F32>
-cudaError_t launch(const ProductParams& p, cudaStream_t s)
+template <int TN, bool F32>
+cudaError_t launch(ProductParams& p, cudaStream_t s)
 {
+    constexpr uint32_t SMEM_BYTES = Tile<TN>::SMEM_BYTES;
+    auto kernel = product_kernel<TN, F32>;
     cudaLaunchAttribute attr[2] = {chained_attribute(), {}};
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
@@ -443,35 +491,64 @@ cudaError_t launch(const ProductParams& p, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = once.run(dev, [&]() -> cudaError_t {
-        cudaError_t err = cudaFuncSetAttribute(product_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-        if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(&resident[dev & 63], product_kernel<F32>, &cfg);
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+        if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(&resident[dev & 63], kernel, &cfg);
         return err != cudaSuccess ? err : resident[dev & 63] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
     });
     if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.splits;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, resident[dev & 63])));
-    return cudaLaunchKernelEx(&cfg, product_kernel<F32>, p);
+    const int pairs = std::min(p.units, resident[dev & 63]);
+    p.step_j = pairs / p.inner;
+    p.step_i = pairs % p.inner;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
-int mx4_splits(int64_t M, int64_t N, int tiles)
+namespace {
+
+struct Plan {
+    int tn, splits;
+};
+
+// Rows of b in a tile, and parts of the depth, by an estimate of the time in nanoseconds: what a step and a tile were measured to
+// take with every pair at work.  Tiles of 192 rows read more for the same work (4680 x 5120, depth 20480: 132.6 us with 256 rows,
+// 171.4 with 192), but their tiles follow one another closer and fill the pairs evenly at other sizes (4680 x 1536, depth 1536: 10.8
+// and 10.0 us).
+Plan plan_of(int64_t M, int64_t N, int tiles)
 {
-    const int64_t units = ((M + TM - 1) / TM) * ((N + TN - 1) / TN);
+    const int64_t mtiles = (M + TM - 1) / TM;
     const int steps = (tiles + STEP_TILES - 1) / STEP_TILES;
+    Plan best{256, 1};
+    double least = 0;
+    for (int tn : {256, 192}) {
+        const int64_t units = mtiles * ((N + tn - 1) / tn);
+        const int64_t waves = (units + kPairs - 1) / kPairs;
+        const double time = static_cast<double>(waves) * (tn == 256 ? 315.0 * steps + 1090 : 291.0 * steps + 650);
+        if (least == 0 || time < least) {
+            least = time;
+            best.tn = tn;
+        }
+    }
+    const int64_t units = mtiles * ((N + best.tn - 1) / best.tn);
     const int s = static_cast<int>(std::min<int64_t>(kPairs / std::min<int64_t>(units, kPairs), std::max(1, steps / 2)));
-    return steps - steps / s >= 12 ? s : 1;
+    if (steps - steps / s >= 12) best.splits = s;
+    return best;
 }
+
+}  // namespace
+
+int mx4_splits(int64_t M, int64_t N, int tiles) { return plan_of(M, N, tiles).splits; }
 
 cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
 {
     ProductParams p{};
     p.M = static_cast<int32_t>(q.M);
     p.N = static_cast<int32_t>(q.N);
-    p.mtiles = static_cast<int32_t>((q.M + TM - 1) / TM);
-    p.ntiles = static_cast<int32_t>((q.N + TN - 1) / TN);
+    const Plan plan = plan_of(q.M, q.N, q.tiles);
+    const int32_t mtiles = static_cast<int32_t>((q.M + TM - 1) / TM), ntiles = static_cast<int32_t>((q.N + plan.tn - 1) / plan.tn);
     p.steps = (q.tiles + STEP_TILES - 1) / STEP_TILES;
-    p.splits = mx4_splits(q.M, q.N, q.tiles);
+    p.splits = plan.splits;
     p.bias = q.bias;
     p.gelu = q.gelu;
     p.err = q.err;
@@ -480,9 +557,11 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     p.out_stride = q.out_stride;
     // the operand with the fewer bytes is read again for every tile of the other
     p.m_fastest = q.N > q.M;
+    p.inner = p.m_fastest ? mtiles : ntiles;
+    p.units = mtiles * ntiles * p.splits;
     const bool parts = p.splits > 1;
     const bool f32 = parts || q.out_f32;
-    if (!codes_map(&p.a, q.a, q.M, q.tiles) || !codes_map(&p.b, q.b, q.N, q.tiles) || !scales_map(&p.as, q.as, q.M, q.tiles, 1) ||
+    if (!codes_map(&p.a, q.a, q.M, q.tiles, CM) || !codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) || !scales_map(&p.as, q.as, q.M, q.tiles, 1) ||
         !scales_map(&p.bs, q.bs, q.N, q.tiles, 2))
         return cudaErrorInvalidValue;
     const int64_t stride = parts ? mx4_part_stride(q.N) : q.out_stride;
@@ -492,7 +571,8 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     const bool boxes = (pitch | width * (f32 ? 4 : 2)) % 16 == 0 && pitch <= (int64_t(1) << 39) / q.M;
     if (!boxes) p.direct = q.out;
     else if (!out_map(&p.out, parts ? q.part : q.out, f32, q.M, width, stride, p.splits)) return cudaErrorInvalidValue;
-    cudaError_t e = f32 ? launch<true>(p, s) : launch<false>(p, s);
+    cudaError_t e = plan.tn == 256 ? (f32 ? launch<256, true>(p, s) : launch<256, false>(p, s))
+                                   : (f32 ? launch<192, true>(p, s) : launch<192, false>(p, s));
     if (e != cudaSuccess || !parts) return e;
     const int64_t blocks = (q.M * (stride / 4) + 255) / 256;
     const int vectors = q.out_stride % 4 == 0;

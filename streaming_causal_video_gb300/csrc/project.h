@@ -62,7 +62,7 @@ constexpr int kRopePairs = 128;            // head_dim 256
 struct RopePair {
     uint64_t turn;                         // turns for a step of the position, as a 64-bit fraction of one
     int16_t u, v;                          // dims of the pair
-    int16_t axis;                          // or -1: stays as it is
+    int16_t axis;                          // or -1: stays as it is (its turn is 0)
     int16_t pad;
 };
 
@@ -79,13 +79,13 @@ struct AxesRopeParams {
     int32_t batch, heads, kv_heads, axes;
     int32_t shared;                        // one row of positions for all of the batch
     int32_t items;                         // threads for one row of heads
-    int32_t per;                           // heads (of q, then k) that a thread turns
+    int32_t per;                           // heads that a thread turns
+    int32_t q_parts;                       // blocks in y for the heads of q; those of k follow
     RopePair pair[kRopePairs];
 };
 
-// The way a thread takes pairs: one vector of adjacent pairs, the vectors of the two halves, or one pair.
-enum class RopeLayout { adjacent, halves, single };
-
-cudaError_t launch_axes_rope(AxesRopeParams& p, RopeLayout layout, bool f32, int head_dim, cudaStream_t s);
+// adjacent: pairs of neighbours; else of two half segments, all of which are whole vectors of `width` elements (16 bytes, 2 or 1);
+// all: every dim turns.
+cudaError_t launch_axes_rope(AxesRopeParams& p, bool adjacent, int width, bool all, bool f32, int head_dim, cudaStream_t s);
 
 }  // namespace sdv2

@@ -144,16 +144,16 @@ uint64_t turn_fraction(Twofold turns)
     return f + static_cast<uint64_t>(std::llrint(std::ldexp(turns.lo, 64)));
 }
 
-// The pairs of a head and how threads take them.
-RopeLayout rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
+// The pairs of a head; the elements of a vector that every half segment is whole ones of.
+int rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
 {
     constexpr Twofold kTurns{0.15915494309189535, -9.839338337591243e-18};      // 1 / 2pi
     const int lane = c->dtype == SDV2_F32 ? 4 : 8;       // elements of a vector
-    int n = 0, first = 0;
-    bool whole = true;                                   // every half segment is whole vectors
+    int n = 0, first = 0, width = lane;
+    auto fits = [&](int half) { width = half % width == 0 ? width : half % 2 == 0 ? 2 : 1; };
     for (int a = 0; a < c->axes; ++a) {
         const int d = c->dims[a];
-        whole = whole && d / 2 % lane == 0;
+        fits(d / 2);
         const double scale = c->scale[a] == 0.0 ? 1.0 : c->scale[a];
         const bool negative = (scale < 0) != backward;
         const Twofold ratio = frequency_ratio(c->base, d);
@@ -169,7 +169,7 @@ RopeLayout rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams
         first += d;
     }
     const int rest = c->head_dim - first;
-    whole = whole && rest / 2 % lane == 0;
+    fits(rest / 2);
     for (int j = 0; j < rest / 2; ++j) {
         RopePair& q = p->pair[n++];
         q = RopePair{};
@@ -177,7 +177,7 @@ RopeLayout rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams
         q.v = static_cast<int16_t>(c->halves ? first + j + rest / 2 : first + 2 * j + 1);
         q.axis = -1;
     }
-    return !c->halves ? RopeLayout::adjacent : whole ? RopeLayout::halves : RopeLayout::single;
+    return width;
 }
 
 sdv2_status rope_call(const sdv2_axes_rope_cfg* c, const int32_t* positions, const void* q, void* q_new, const void* k,
@@ -208,8 +208,10 @@ sdv2_status rope_call(const sdv2_axes_rope_cfg* c, const int32_t* positions, con
     p.kv_heads = c->kv_heads;
     p.axes = c->axes;
     p.shared = c->shared_positions;
-    const RopeLayout layout = rope_pairs(c, backward, &p);
-    return launched(launch_axes_rope(p, layout, c->dtype == SDV2_F32, c->head_dim, static_cast<cudaStream_t>(stream)), "axes rope launch");
+    const int width = rope_pairs(c, backward, &p);
+    const bool all = p.pair[c->head_dim / 2 - 1].axis >= 0;
+    return launched(launch_axes_rope(p, !c->halves, width, all, c->dtype == SDV2_F32, c->head_dim, static_cast<cudaStream_t>(stream)),
+                    "axes rope launch");
 }
 
 }  // namespace

@@ -21,28 +21,47 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
-// Copies those scales from each CTA's shared memory to four columns of its own tensor memory, for each of its four lane
-// quarters.  Products issued by the same thread behind it read what it wrote.
-__device__ __forceinline__ void scales_to_tmem_pair_warp(uint32_t taddr, uint64_t desc)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-        "l"(desc)
-        : "memory");
-}
-
-// D (+)= A * B, 64 columns, over the pair; a_scales and b_scales are tensor-memory addresses in both CTAs.
-__device__ __forceinline__ void mma_mx4_pair_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t a_scales, uint32_t b_scales, uint32_t accumulate)
+// One ring stage, 256 columns, issued by one elected lane: the scales of both scale tiles of a and of the two by two of b go from each
+// CTA's shared memory to its own tensor memory (a: 4 columns a tile; b: 8), and four MMAs over the pair add 64 columns each to
+// the sums.  One block of instructions, because what bounds these products is how fast a single thread issues them: with an
+// election, a predicate and descriptors computed for each, a stage took 540 cycles, whatever its MMAs were.
+//   a, b: descriptors of the codes, a row's 64 columns 32 bytes apart; as, bs: of the scales, tiles 512 bytes apart, b's second
+//   row tile 1024; i0, i1: instruction descriptors for the first and the second half of a scale tile
+__device__ __forceinline__ void mx4_stage_pair_warp(uint32_t sums, uint64_t a, uint64_t b, uint64_t as, uint64_t bs, uint32_t a_scales,
+                                                    uint32_t b_scales, uint32_t b_first, uint32_t i0, uint32_t i1, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
+        ".reg .b64 x, y;\n\t"
+        ".reg .b32 t, u;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        "setp.ne.b32 p, %10, 0;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %3;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %4;\n\t"
+        "add.s32 t, %6, 4;\n\t"
+        "add.s64 x, %4, 64;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+        "add.s32 t, %5, 4;\n\t"
+        "add.s64 x, %3, 32;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+        "add.s32 u, %6, 8;\n\t"
+        "add.s64 x, %4, 32;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
+        "add.s32 u, %6, 12;\n\t"
+        "add.s64 x, %4, 96;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %8, [%5], [%7], p;\n\t"
+        "add.s64 x, %1, 2;\n\t"
+        "add.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [%5], [%7], 1;\n\t"
+        "add.s64 x, %1, 4;\n\t"
+        "add.s64 y, %2, 4;\n\t"
+        "add.s32 u, %7, 8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [t], [u], 1;\n\t"
+        "add.s64 x, %1, 6;\n\t"
+        "add.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [t], [u], 1;\n\t}" ::"r"(sums),
+        "l"(a), "l"(b), "l"(as), "l"(bs), "r"(a_scales), "r"(b_scales), "r"(b_first), "r"(i0), "r"(i1), "r"(accumulate)
         : "memory");
 }
 
