@@ -1,7 +1,7 @@
 // Rotary positions of several axes, forward and backward (the rotation by the negative angle).
 //
 // Every element is read and written once, so that memory bounds this.  A thread owns the same pairs of dims in many heads of a
-// token: it finds their sines and cosines once and then only loads, turns and stores, four heads' loads under way together.  Pairs
+// token: it finds their sines and cosines once and then only loads, turns and stores, six heads' loads under way together.  Pairs
 // of neighbours lie in one vector of 16 bytes; pairs half a segment apart in two, as wide as every half segment is whole vectors of.
 // An angle in turns is position * scale * base^(-2j/d) / 2pi.  Its frequency is held as a 64-bit fraction of a turn (whole
 // turns of it change nothing), so that the 64-bit product with the position, which wraps around, is the fraction of a turn that
@@ -18,7 +18,7 @@ namespace sdv2 {
 namespace {
 
 constexpr int kThreads = 128;              // of a block, at most: whole rows of items
-constexpr int kBatch = 4;                  // heads whose loads are under way together
+constexpr int kBatch = 6;                  // heads whose loads are under way together
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turn)
 {
@@ -96,9 +96,10 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
     const int32_t* const pos0 = p.positions + (p.shared ? 0 : blockIdx.z * p.tokens * p.axes);
     wait_for_launch_before();
     for (int64_t n = static_cast<int64_t>(blockIdx.x) * together + place; n < p.tokens; n += static_cast<int64_t>(gridDim.x) * together) {
-        float2 cs[P];
+        int32_t pos[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) cs[i] = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos0[n * p.axes + max(axis[i], 0)])) * turn[i]);
+        for (int i = 0; i < P; ++i) pos[i] = pos0[n * p.axes + max(axis[i], 0)];
+        float2 cs[P];
         const T* in = in0 + n * t.is.token_stride;
         T* out = out0 + n * t.os.token_stride;
         for (int h = 0; h < heads; h += kBatch) {
@@ -108,6 +109,10 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
                 const T* from = in + min(b, heads - 1 - h) * t.is.head_stride;
                 x[b][0] = *reinterpret_cast<const Pack<T, N>*>(from);
                 if constexpr (!ADJACENT) x[b][1] = *reinterpret_cast<const Pack<T, N>*>(from + (v0 - u0));
+            }
+            if (h == 0) {                                    // while the first heads are on their way
+#pragma unroll
+                for (int i = 0; i < P; ++i) cs[i] = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos[i])) * turn[i]);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
