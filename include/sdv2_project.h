@@ -84,13 +84,12 @@ typedef struct {
     int64_t out_row_stride;    /* elements between rows of out; 0 = cols                        */
 } sdv2_mx4_product_cfg;
 
-/* Bytes of the workspace of products with this configuration: the device error word (256 bytes) and,
- * where the depth is split over the GPU, partial sums.  It holds nothing from one call to the next
- * but the error word; calls that use it must not overlap on the GPU.  0 on an invalid configuration. */
+/* Bytes of the workspace of products with this configuration: the device error word (256 bytes).
+ * 0 on an invalid configuration. */
 size_t sdv2_mx4_workspace_bytes(const sdv2_mx4_product_cfg* cfg);
 
-/* Zeroes the error word and enqueues nothing else; one workspace serves every configuration that it
- * is large enough for.  Waits on the device are bounded by sdv2_set_wait_timeout_ns;
+/* Zeroes the error word and enqueues nothing else; one workspace serves every configuration, and calls
+ * that overlap on the GPU.  Waits on the device are bounded by sdv2_set_wait_timeout_ns;
  * sdv2_check_device_error(ws, stream) reads the word.  With sdv2_debug_drop_kv_tile set, a product of
  * more than 8 rows leaves out the copy of the 256 columns of a and b with this number. */
 sdv2_status sdv2_mx4_workspace_init(const sdv2_mx4_product_cfg* cfg, void* ws, void* stream);

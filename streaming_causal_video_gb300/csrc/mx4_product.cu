@@ -10,8 +10,9 @@
 //   the leader arms for both); warp 1: in the leader, scale copies and MMAs, whose commits arrive on the barriers of both CTAs;
 //   warps 2-17: epilogue, four per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 64
 //   bytes of a row at a time go through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
-// Where tiles are fewer than pairs, the depth is cut into parts; their sums go to the workspace in fp32 and a second kernel adds
-// them in order, so that results do not depend on which part ends first.
+// Where tiles are fewer than pairs, the depth is cut into two or four parts, one for each pair of a larger cluster.  Their sums are
+// exchanged through shared memory when the ring is free, and each pair adds up and writes its share of the columns, in the order of
+// the parts, so that results do not depend on which part ends first.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -34,7 +35,6 @@ constexpr int TM = 256, CM = TM / 2;           // rows of a in a pair tile and i
 constexpr int STEP_TILES = 2;                  // scale tiles (128 columns) of a stage
 constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
-constexpr uint16_t kBothCtas = 3;
 
 // What depends on the rows of b in a pair tile.
 template <int TN>
@@ -49,8 +49,7 @@ struct Tile {
     static constexpr uint32_t STAGE_PITCH = (STAGE_BYTES + 1023) / 1024 * 1024;
     static constexpr uint32_t OUT_BYTES = 32 * 64;                     // a warp's staging of its rows
     static constexpr uint32_t OUT_OFF = STAGES * STAGE_PITCH;
-    static constexpr uint32_t BIAS_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
-    static constexpr uint32_t BAR_OFF = BIAS_OFF + EPI_WARPS * 64 * 4;
+    static constexpr uint32_t BAR_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
     static constexpr uint32_t SMEM_BYTES = BAR_OFF + 256 + 1024;
     // Tensor memory: the sums of two tiles, and behind them the scales of a and of b of a step.  Two tiles of 256 columns do
     // not fit beside the scales: the second begins with the first's last 32.  The epilogue takes the shared columns of a tile
@@ -67,7 +66,7 @@ struct Tile {
 constexpr uint32_t TMEM_COLS = 512;
 
 struct ProductParams {
-    CUtensorMap a, as, b, bs, out;             // out: the result, or partial sums
+    CUtensorMap a, as, b, bs, out;
     const float* bias;
     void* direct;                              // out, where rows are not whole 16 bytes, else null
     int64_t out_stride;
@@ -157,7 +156,73 @@ __device__ __forceinline__ void store_rows(const ProductParams& p, const uint8_t
     }
 }
 
-template <int TN, bool F32>
+// A warp's way to out: PIECE columns of its 32 rows at a time, 64 bytes of a row, thread = row.
+template <bool F32>
+struct Epilogue {
+    static constexpr int PIECE = F32 ? 16 : 32;
+    const ProductParams& p;
+    uint8_t* stage;                            // 2 KB, swizzled as TMA takes 64-byte rows
+
+    __device__ __forceinline__ Epilogue(const ProductParams& p_, uint8_t* stage_) : p(p_), stage(stage_) {}
+
+    // Columns n to n + PIECE of rows row0 to row0 + 32, of which there is one at least.
+    __device__ __forceinline__ void write(const uint32_t (&y)[PIECE], int row0, int n)
+    {
+        const int lane = threadIdx.x & 31;
+        uint64_t v[PIECE / 2];
+#pragma unroll
+        for (int j = 0; j < PIECE / 2; ++j) v[j] = f32x2_pack(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
+        if (p.bias) {
+            if (n + PIECE <= p.N) {                              // the same addresses in all lanes
+                const ulonglong2* b = reinterpret_cast<const ulonglong2*>(p.bias + n);
+#pragma unroll
+                for (int j = 0; j < PIECE / 4; ++j) {
+                    const ulonglong2 b4 = b[j];
+                    v[2 * j] = fadd2(v[2 * j], b4.x);
+                    v[2 * j + 1] = fadd2(v[2 * j + 1], b4.y);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < PIECE / 2; ++j)
+                    v[j] = fadd2(v[j], f32x2_pack(n + 2 * j < p.N ? p.bias[n + 2 * j] : 0.0f, n + 2 * j + 1 < p.N ? p.bias[n + 2 * j + 1] : 0.0f));
+            }
+        }
+        if (p.gelu) {
+#pragma unroll
+            for (int j = 0; j < PIECE / 2; ++j) v[j] = gelu2(v[j]);
+        }
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 w;
+            if constexpr (F32)
+                w = make_uint4(static_cast<uint32_t>(v[2 * j]), static_cast<uint32_t>(v[2 * j] >> 32), static_cast<uint32_t>(v[2 * j + 1]),
+                               static_cast<uint32_t>(v[2 * j + 1] >> 32));
+            else
+                w = make_uint4(pack2(v[4 * j]), pack2(v[4 * j + 1]), pack2(v[4 * j + 2]), pack2(v[4 * j + 3]));
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+        }
+        if (!p.direct) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&p.out, smem_u32(stage), n, row0, 0);
+        } else {
+            __syncwarp();
+            store_rows<F32>(p, stage, row0, n);
+            __syncwarp();
+        }
+    }
+
+    __device__ __forceinline__ void finish()
+    {
+        if ((threadIdx.x & 31) == 0) tma_store_wait();
+        __syncwarp();
+    }
+};
+
+// SPLIT: a cluster is p.splits pairs, which take the parts of the depth of one tile.
+template <int TN, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ ProductParams p)
 {
     using T = Tile<TN>;
@@ -171,17 +236,27 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::BAR_OFF);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + T::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* peer_abort = abort_flag + 1;
+    volatile int* peer_abort = abort_flag + 1;          // a CTA of the cluster gave up
     volatile int* peer_steps = abort_flag + 2;
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
     const int lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_ctarank());            // 0: the leader, which issues the MMAs
-    const int pair = static_cast<int>(cluster_id_x()), pairs = static_cast<int>(cluster_count_x());
+    const int in_cluster = static_cast<int>(cluster_ctarank());
+    const int rank = in_cluster & 1;                                 // 0: the pair's leader, which issues the MMAs
+    const uint32_t leader = SPLIT ? static_cast<uint32_t>(in_cluster & ~1) : 0u;
+    const uint16_t both = static_cast<uint16_t>(3u << leader);       // the pair's CTAs
     const int units = p.units;
+    const int pair = SPLIT ? static_cast<int>(cluster_id_x()) * p.splits + (in_cluster >> 1) : static_cast<int>(cluster_id_x());
+    const int pairs = SPLIT ? units : static_cast<int>(cluster_count_x());
     const uint64_t tmo = p.timeout_ns;
 
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&p.a);
+        tma_prefetch_desc(&p.b);
+        tma_prefetch_desc(&p.as);
+        tma_prefetch_desc(&p.bs);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * STAGES; ++i) mbar_init(bar(i), 1);
         for (int i = 0; i < 2; ++i) {
@@ -213,9 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     int issued = 0;              // the producer's steps
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&p.a);
-            tma_prefetch_desc(&p.b);
-            const uint32_t full_leader = map_to_rank(bar(B_FULL), 0);
+            const uint32_t full_leader = map_to_rank(bar(B_FULL), leader);
             bool ok = true;
             for (Unit t(p, pair, TN); ok && t.u < units; t.next(p, pairs, TN)) {
                 const int m0 = t.m0 + rank * CM, n0 = t.n0 + rank * T::CN;
@@ -236,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     tma_load_3d_pair(sa + A_BYTES + B_BYTES + AS_BYTES, &p.bs, fb, 0, k * STEP_TILES, t.n0 / 128);
                 }
             }
-            if (rank == 1) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_steps)), 0), issued);
+            if (rank == 1) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_steps)), leader), issued);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -269,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     tc_fence_after();
                     mx4_stage_pair_warp(acc, dA + at, dB + at, dAS + at, dBS + at, tmem + COL_AS, tmem + COL_BS, b_scales, idesc_mx4(TM, TN, 0),
                                         idesc_mx4(TM, TN, 1), k > t.first ? 1u : 0u);
-                    mma_commit_pair_warp(bar(B_EMPTY + st), kBothCtas);
+                    mma_commit_pair_warp(bar(B_EMPTY + st), both);
                     at += T::STAGE_PITCH >> 4;
                     if (++st == STAGES) {
                         st = 0;
@@ -278,10 +351,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                     }
                 }
                 if (!ok) break;
-                mma_commit_pair_warp(bar(B_ACC_FULL + buf), kBothCtas);
+                mma_commit_pair_warp(bar(B_ACC_FULL + buf), both);
             }
             if (!ok && lane == 0) give_up();
-            mma_commit_pair_warp(bar(B_DONE), kBothCtas);            // tensor memory is freed only behind the last MMA
+            mma_commit_pair_warp(bar(B_DONE), both);            // tensor memory is freed only behind the last MMA
         }
         if (lane == 0) {
             volatile int no_abort = 0;
@@ -291,28 +364,23 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     } else {
         // Four warps per quarter, 64 columns each; of 192 columns another one has none in each tile.
         const int group = (warp - 2) >> 2, quarter = warp & 3;
-        constexpr int PIECE = F32 ? 16 : 32, PIECES = 64 / PIECE;    // columns that a thread has at once: 64 bytes of a row
-        uint8_t* stage = smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES;
-        float* bias = reinterpret_cast<float*>(smem + T::BIAS_OFF) + (warp - 2) * 64;
-        const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), 0), shared_leader = map_to_rank(bar(B_SHARED), 0);
-        const bool whole = p.splits == 1;                            // else partial sums
+        constexpr int PIECE = Epilogue<F32>::PIECE, PIECES = 64 / PIECE;
+        Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES);
+        const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), leader), shared_leader = map_to_rank(bar(B_SHARED), leader);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int li = 0;
         for (Unit t(p, pair, TN); t.u < units; t.next(p, pairs, TN), ++li) {
             const int buf = li & 1;
             const int place = T::SHARES ? group : (group + li) & 3;
             const int row0 = t.m0 + rank * CM + quarter * 32, n0 = t.n0 + place * 64;
             const bool mine = (T::SHARES || place < 3) && row0 < p.M && n0 < p.N;
-            if (mine) {
-                bias[lane] = whole && p.bias && n0 + lane < p.N ? p.bias[n0 + lane] : 0.0f;
-                bias[32 + lane] = whole && p.bias && n0 + 32 + lane < p.N ? p.bias[n0 + 32 + lane] : 0.0f;
-            }
-            __syncwarp();
             const bool ok = mbar_wait_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
             tc_fence_after();
+            if constexpr (SPLIT) continue;                           // the sums of the parts are added below
             // the arrivals order no memory but the loads of tensor memory before them
             auto arrive = [&](uint32_t at) {
                 tc_fence_before();
@@ -326,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
                 continue;
             }
-            const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (buf ? T::COL_SECOND : 0u) + static_cast<uint32_t>(place * 64);
+            const uint32_t trow = lanes + (buf ? T::COL_SECOND : 0u) + static_cast<uint32_t>(place * 64);
             const int flip = T::SHARES && buf == 0 ? PIECES - 1 : 0;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
@@ -335,50 +403,74 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 tmem_ld_sync(trow + c, y);
                 if (shared && (i + 1) * PIECE == 32) arrive(shared_leader);
                 if (i == PIECES - 1) arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
-                uint64_t v[PIECE / 2];
+                out.write(y, row0, n0 + c);
+            }
+        }
+        if constexpr (!SPLIT) out.finish();
+    }
+    if constexpr (SPLIT) {
+        // The parts' sums change hands through shared memory: pair s of the cluster adds up, in the order of the parts, and writes
+        // the s-th of equal ranges of the tile's columns.  The ring is free when every pair's MMAs are done.
+        tc_fence_before();
+        __syncthreads();
+        cluster_sync_all();
+        tc_fence_after();
+        const int parts = p.splits, own = in_cluster >> 1, width = TN / parts;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t my_row = static_cast<uint32_t>(quarter * 32 + lane) * 16;
+        const bool sound = !*abort_flag;
+        if (warp >= 2 && sound) {
+            const Unit t(p, pair, TN);
+            const int owner = group * 64 / width;
+            if (owner != own && t.m0 + rank * CM + quarter * 32 < p.M && t.n0 + group * 64 < p.N) {
+                // [part][four columns][row][column]: a warp stores 512 bytes together
+                const uint32_t to = map_to_rank(s0, static_cast<uint32_t>(2 * owner + rank)) +
+                                    static_cast<uint32_t>((own < owner ? own : own - 1) * width + group * 64 % width) * (CM * 4) + my_row;
 #pragma unroll
-                for (int j = 0; j < PIECE; j += 4) {
-                    const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bias + c + j);
-                    v[j / 2] = fadd2(f32x2_pack(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), b4.x);
-                    v[j / 2 + 1] = fadd2(f32x2_pack(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), b4.y);
-                }
-                if (whole && p.gelu) {
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld_x32_sync(lanes + group * 64 + c, y);
 #pragma unroll
-                    for (int j = 0; j < PIECE / 2; ++j) v[j] = gelu2(v[j]);
-                }
-                if (lane == 0) tma_store_wait_read();
-                __syncwarp();
-                // 16-byte vectors of a row's 64 bytes, swizzled as TMA takes them
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 w;
-                    if constexpr (F32) {
-                        w = make_uint4(static_cast<uint32_t>(v[2 * j]), static_cast<uint32_t>(v[2 * j] >> 32),
-                                       static_cast<uint32_t>(v[2 * j + 1]), static_cast<uint32_t>(v[2 * j + 1] >> 32));
-                    } else {
-                        w = make_uint4(pack2(v[4 * j]), pack2(v[4 * j + 1]), pack2(v[4 * j + 2]), pack2(v[4 * j + 3]));
-                    }
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
-                }
-                if (!p.direct) {
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0 && n0 + c < p.N) tma_store_3d(&p.out, smem_u32(stage), n0 + c, row0, t.split);
-                } else {
-                    __syncwarp();
-                    store_rows<F32>(p, stage, row0, n0 + c);
-                    __syncwarp();
+                    for (int j = 0; j < 32; j += 4) st_cluster_v4(to + static_cast<uint32_t>(c + j) * (CM * 4), y[j], y[j + 1], y[j + 2], y[j + 3]);
                 }
             }
         }
-        if (lane == 0) tma_store_wait();
-        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && sound) {
+            constexpr int PIECE = Epilogue<F32>::PIECE;
+            Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES);
+            const Unit t(p, pair, TN);
+            const int row0 = t.m0 + rank * CM + quarter * 32;
+            for (int c = group * PIECE; c < width; c += 4 * PIECE) {
+                const int n = t.n0 + own * width + c;
+                if (row0 >= p.M || n >= p.N) continue;
+                uint32_t mine[PIECE];
+                tmem_ld_sync(lanes + own * width + c, mine);
+                uint32_t y[PIECE] = {};
+                for (int part = 0; part < parts; ++part) {
+                    const uint8_t* from = smem + ((part < own ? part : part - 1) * width + c) * (CM * 4) + my_row;
+#pragma unroll
+                    for (int j = 0; j < PIECE; j += 4) {
+                        uint4 v = make_uint4(mine[j], mine[j + 1], mine[j + 2], mine[j + 3]);
+                        if (part != own) v = *reinterpret_cast<const uint4*>(from + j * (CM * 4));
+                        y[j] = __float_as_uint(__uint_as_float(y[j]) + __uint_as_float(v.x));
+                        y[j + 1] = __float_as_uint(__uint_as_float(y[j + 1]) + __uint_as_float(v.y));
+                        y[j + 2] = __float_as_uint(__uint_as_float(y[j + 2]) + __uint_as_float(v.z));
+                        y[j + 3] = __float_as_uint(__uint_as_float(y[j + 3]) + __uint_as_float(v.w));
+                    }
+                }
+                out.write(y, row0, n);
+            }
+            out.finish();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_abort)), static_cast<uint32_t>(rank ^ 1)), 1);
+    if (threadIdx.x == 0 && *abort_flag)
+        for (int c = 0; c < (SPLIT ? 2 * p.splits : 2); ++c) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_abort)), static_cast<uint32_t>(c)), 1);
     cluster_sync_all();          // no CTA leaves while the other may still signal or read it
-    if (*abort_flag || *peer_abort) {
+    if (*peer_abort) {
         // The ring's copies land before the pair may go.  A step that only one of the two CTAs issued is squared up: armed for the
         // peer's copies alone, or told that the peer's do not come.
         if (threadIdx.x == 0 && rank == 0) {
@@ -396,45 +488,6 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, TMEM_COLS);
-    }
-}
-
-// Adds the parts of the depth in order, then bias, activation and the rounding of out.
-template <bool F32>
-__global__ void __launch_bounds__(256) join_kernel(const float* part, const float* bias, void* out, int64_t M, int N, int64_t stride,
-                                                   int64_t part_stride, int splits, int gelu_too, int vectors)
-{
-    wait_for_launch_before();
-    const int64_t quads = part_stride / 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= M * quads) return;
-    const int64_t m = i / quads;
-    const int n = static_cast<int>(i - m * quads) * 4;
-    const float4* src = reinterpret_cast<const float4*>(part + m * part_stride + n);
-    const int64_t step = M * quads;
-    float y[4] = {};
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-        const float4 v = src[s * step];
-        y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (n + j >= N) continue;
-        if (bias) y[j] += bias[n + j];
-        if (gelu_too) y[j] = gelu(y[j]);
-    }
-    const int64_t o = m * stride + n;
-    if (vectors && n + 4 <= N) {
-        if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(y[0], y[1], y[2], y[3]);
-        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (n + j >= N) continue;
-        if constexpr (F32) static_cast<float*>(out)[o + j] = y[j];
-        else static_cast<__nv_bfloat16*>(out)[o + j] = __float2bfloat16_rn(y[j]);
     }
 }
 
@@ -458,25 +511,25 @@ bool scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, 
     return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, map, base, 3, dims, strides, box);
 }
 
-// Results or partial sums: boxes of 64 bytes x 32 rows.
-bool out_map(CUtensorMap* map, const void* base, bool f32, int64_t M, int64_t N, int64_t stride, int splits)
+// Results: boxes of 64 bytes x 32 rows.
+bool out_map(CUtensorMap* map, const void* base, bool f32, int64_t M, int64_t N, int64_t stride)
 {
     const cuuint64_t pitch = static_cast<cuuint64_t>(stride) * (f32 ? 4 : 2);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(splits)};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), 1};
     const cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(M)};
     const cuuint32_t box[3] = {f32 ? 16u : 32u, 32, 1};
     return encode_tensor_map_of(f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B,
                                 map, base, 3, dims, strides, box);
 }
 
-template <int TN, bool F32>
+template <int TN, bool F32, bool SPLIT>
 cudaError_t launch(ProductParams& p, cudaStream_t s)
 {
     constexpr uint32_t SMEM_BYTES = Tile<TN>::SMEM_BYTES;
-    auto kernel = product_kernel<TN, F32>;
+    auto kernel = product_kernel<TN, F32, SPLIT>;
     cudaLaunchAttribute attr[2] = {chained_attribute(), {}};
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = SPLIT ? 2 * p.splits : 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2);
@@ -492,11 +545,11 @@ cudaError_t launch(ProductParams& p, cudaStream_t s)
     if (e != cudaSuccess) return e;
     e = once.run(dev, [&]() -> cudaError_t {
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-        if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(&resident[dev & 63], kernel, &cfg);
-        return err != cudaSuccess ? err : resident[dev & 63] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+        if (err == cudaSuccess && !SPLIT) err = cudaOccupancyMaxActiveClusters(&resident[dev & 63], kernel, &cfg);
+        return err != cudaSuccess ? err : SPLIT || resident[dev & 63] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
     });
     if (e != cudaSuccess) return e;
-    const int pairs = std::min(p.units, resident[dev & 63]);
+    const int pairs = SPLIT ? p.units : std::min(p.units, resident[dev & 63]);
     p.step_j = pairs / p.inner;
     p.step_i = pairs % p.inner;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
@@ -514,31 +567,33 @@ struct Plan {
 // Rows of b in a tile, and parts of the depth, by an estimate of the time in nanoseconds: what a step and a tile were measured to
 // take with every pair at work.  Tiles of 192 rows read more for the same work (4680 x 5120, depth 20480: 132.6 us with 256 rows,
 // 171.4 with 192), but their tiles follow one another closer and fill the pairs evenly at other sizes (4680 x 1536, depth 1536: 10.8
-// and 10.0 us).
+// and 10.0 us).  Where tiles of 256 rows are few, two or four pairs may share the depth of each (the GPU holds 36 clusters of four CTAs
+// and 15 of eight at once), if that saves more than the exchange of their sums from SM to SM costs.
 Plan plan_of(int64_t M, int64_t N, int tiles)
 {
     const int64_t mtiles = (M + TM - 1) / TM;
     const int steps = (tiles + STEP_TILES - 1) / STEP_TILES;
     Plan best{256, 1};
     double least = 0;
+    auto offer = [&](int tn, int splits, double time) {
+        if (least == 0 || time < least) {
+            least = time;
+            best = {tn, splits};
+        }
+    };
     for (int tn : {256, 192}) {
         const int64_t units = mtiles * ((N + tn - 1) / tn);
         const int64_t waves = (units + kPairs - 1) / kPairs;
-        const double time = static_cast<double>(waves) * (tn == 256 ? 315.0 * steps + 1090 : 291.0 * steps + 650);
-        if (least == 0 || time < least) {
-            least = time;
-            best.tn = tn;
-        }
+        offer(tn, 1, static_cast<double>(waves) * (tn == 256 ? 315.0 * steps + 1090 : 291.0 * steps + 650));
     }
-    const int64_t units = mtiles * ((N + best.tn - 1) / best.tn);
-    const int s = static_cast<int>(std::min<int64_t>(kPairs / std::min<int64_t>(units, kPairs), std::max(1, steps / 2)));
-    if (steps - steps / s >= 12) best.splits = s;
+    const int64_t units = mtiles * ((N + 255) / 256);
+    const double exchange = static_cast<double>(std::min<int64_t>(M, CM) * 256 * 4) / 25;     // of all sums, at 25 bytes a nanosecond
+    if (units <= 36 && steps >= 2) offer(256, 2, 315.0 * ((steps + 1) / 2) + 1090 + 700 + exchange / 2);
+    if (units <= 15 && steps >= 4) offer(256, 4, 315.0 * ((steps + 3) / 4) + 1090 + 700 + exchange * 3 / 4);
     return best;
 }
 
 }  // namespace
-
-int mx4_splits(int64_t M, int64_t N, int tiles) { return plan_of(M, N, tiles).splits; }
 
 cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
 {
@@ -559,26 +614,16 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     p.m_fastest = q.N > q.M;
     p.inner = p.m_fastest ? mtiles : ntiles;
     p.units = mtiles * ntiles * p.splits;
-    const bool parts = p.splits > 1;
-    const bool f32 = parts || q.out_f32;
     if (!codes_map(&p.a, q.a, q.M, q.tiles, CM) || !codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) || !scales_map(&p.as, q.as, q.M, q.tiles, 1) ||
         !scales_map(&p.bs, q.bs, q.N, q.tiles, 2))
         return cudaErrorInvalidValue;
-    const int64_t stride = parts ? mx4_part_stride(q.N) : q.out_stride;
-    const int64_t pitch = stride * (f32 ? 4 : 2);
-    const int64_t width = parts ? stride : q.N;
+    const int64_t size = q.out_f32 ? 4 : 2, pitch = q.out_stride * size;
     // (a store's last 16 bytes of a row are written whole)
-    const bool boxes = (pitch | width * (f32 ? 4 : 2)) % 16 == 0 && pitch <= (int64_t(1) << 39) / q.M;
-    if (!boxes) p.direct = q.out;
-    else if (!out_map(&p.out, parts ? q.part : q.out, f32, q.M, width, stride, p.splits)) return cudaErrorInvalidValue;
-    cudaError_t e = plan.tn == 256 ? (f32 ? launch<256, true>(p, s) : launch<256, false>(p, s))
-                                   : (f32 ? launch<192, true>(p, s) : launch<192, false>(p, s));
-    if (e != cudaSuccess || !parts) return e;
-    const int64_t blocks = (q.M * (stride / 4) + 255) / 256;
-    const int vectors = q.out_stride % 4 == 0;
-    return launch_chained(q.out_f32 ? join_kernel<true> : join_kernel<false>, static_cast<unsigned>(blocks), 256, 0, s,
-                          static_cast<const float*>(q.part), q.bias, q.out, q.M, static_cast<int>(q.N), q.out_stride, stride, p.splits, q.gelu,
-                          vectors);
+    if ((pitch | q.N * size) % 16 != 0 || pitch > (int64_t(1) << 39) / q.M) p.direct = q.out;
+    else if (!out_map(&p.out, q.out, q.out_f32, q.M, q.N, q.out_stride)) return cudaErrorInvalidValue;
+    if (p.splits > 1) return q.out_f32 ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+    if (plan.tn == 256) return q.out_f32 ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
+    return q.out_f32 ? launch<192, true, false>(p, s) : launch<192, false, false>(p, s);
 }
 
 }  // namespace sdv2

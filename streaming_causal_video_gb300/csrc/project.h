@@ -35,7 +35,6 @@ struct Mx4Product {
     const uint8_t* bs;
     const float* bias;                     // [N] or null
     void* out;
-    float* part;                           // partial sums [splits][M][part_stride], when the depth is split
     int64_t M, N, out_stride;
     int32_t tiles;                         // ceil(K / 128)
     int32_t out_f32, gelu;
@@ -48,10 +47,6 @@ constexpr int kMx4FewRows = 8;             // rows of a that go to launch_mx4_ro
 
 // Few rows of a on the CUDA cores.
 cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s);
-
-// Parts that the depth of a product is cut into, and the elements between rows of their partial sums.
-int mx4_splits(int64_t M, int64_t N, int tiles);
-inline int64_t mx4_part_stride(int64_t N) { return (N + 3) / 4 * 4; }
 
 cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t s);
 

@@ -262,9 +262,7 @@ sdv2_status sdv2_mx4_dequantize(const sdv2_mx4_cfg* c, const void* codes, const 
 
 size_t sdv2_mx4_workspace_bytes(const sdv2_mx4_product_cfg* c)
 {
-    if (check_product(c) != SDV2_OK) return 0;
-    const int splits = c->rows <= kMx4FewRows ? 1 : mx4_splits(c->rows, c->cols, tiles_of(c->depth));
-    return kHeaderBytes + (splits > 1 ? static_cast<size_t>(splits) * c->rows * mx4_part_stride(c->cols) * sizeof(float) : 0);
+    return check_product(c) == SDV2_OK ? kHeaderBytes : 0;
 }
 
 sdv2_status sdv2_mx4_workspace_init(const sdv2_mx4_product_cfg* c, void* ws, void* stream)
@@ -292,7 +290,6 @@ sdv2_status sdv2_mx4_product(const sdv2_mx4_product_cfg* c, const void* a_codes,
     p.bs = static_cast<const uint8_t*>(b_scales);
     p.bias = bias;
     p.out = out;
-    p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kHeaderBytes);
     p.M = c->rows;
     p.N = c->cols;
     p.out_stride = c->out_row_stride ? c->out_row_stride : c->cols;
