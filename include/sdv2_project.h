@@ -90,8 +90,8 @@ size_t sdv2_mx4_workspace_bytes(const sdv2_mx4_product_cfg* cfg);
 
 /* Zeroes the error word and enqueues nothing else; one workspace serves every configuration, and calls
  * that overlap on the GPU.  Waits on the device are bounded by sdv2_set_wait_timeout_ns;
- * sdv2_check_device_error(ws, stream) reads the word.  With sdv2_debug_drop_kv_tile set, a product of
- * more than 8 rows leaves out the copy of the 256 columns of a and b with this number. */
+ * sdv2_check_device_error(ws, stream) reads the word.  With sdv2_debug_drop_kv_tile set, a product
+ * leaves out the copy of the 256 columns of a and b with this number. */
 sdv2_status sdv2_mx4_workspace_init(const sdv2_mx4_product_cfg* cfg, void* ws, void* stream);
 
 /*

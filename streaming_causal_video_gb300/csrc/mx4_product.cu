@@ -21,6 +21,7 @@
 #include "cross_tma.cuh"
 #include "internal.h"
 #include "mx4.cuh"
+#include "mx4_maps.h"
 #include "per_device.h"
 #include "project.h"
 #include "ptx.cuh"
@@ -131,9 +132,6 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v)
     f32x2_unpack(v, lo, hi);
     return pack2(lo, hi);
 }
-
-__device__ __forceinline__ void tmem_ld_sync(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32_sync(taddr, r); }
-__device__ __forceinline__ void tmem_ld_sync(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16_sync(taddr, r); }
 
 // Rows of out that TMA cannot write: a warp stores the 64 staged bytes of its rows number by number, a row (bf16) or two (fp32) at
 // a time, with eight of them under way.
@@ -400,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             for (int i = 0; i < PIECES; ++i) {
                 const int c = (i ^ flip) * PIECE;
                 uint32_t y[PIECE];
-                tmem_ld_sync(trow + c, y);
+                tmem_ld_cols(trow + c, y);
                 if (shared && (i + 1) * PIECE == 32) arrive(shared_leader);
                 if (i == PIECES - 1) arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
                 out.write(y, row0, n0 + c);
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 const int n = t.n0 + own * width + c;
                 if (row0 >= p.M || n >= p.N) continue;
                 uint32_t mine[PIECE];
-                tmem_ld_sync(lanes + own * width + c, mine);
+                tmem_ld_cols(lanes + own * width + c, mine);
                 uint32_t y[PIECE] = {};
                 for (int part = 0; part < parts; ++part) {
                     const uint8_t* from = smem + ((part < own ? part : part - 1) * width + c) * (CM * 4) + my_row;
@@ -492,24 +490,6 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
 }
 
 constexpr int kPairs = 76;                     // a pair for each TPC's two SMs
-
-// Codes: boxes of 128 bytes x `box_rows` rows.
-bool codes_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, int box_rows)
-{
-    const cuuint64_t pitch = static_cast<cuuint64_t>(tiles) * kMx4TileBytes;
-    const cuuint64_t dims[3] = {pitch, static_cast<cuuint64_t>(rows), 1}, strides[2] = {pitch, pitch * static_cast<cuuint64_t>(rows)};
-    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
-    return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, map, base, 3, dims, strides, box);
-}
-
-// Scales: boxes of a tile's 128 words x two tiles x `row_tiles`; tiles past the matrix's arrive as zeros.
-bool scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, int row_tiles)
-{
-    const cuuint64_t n = static_cast<cuuint64_t>((rows + kMx4Tile - 1) / kMx4Tile);
-    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(tiles), n}, strides[2] = {512, static_cast<cuuint64_t>(tiles) * 512};
-    const cuuint32_t box[3] = {128, STEP_TILES, static_cast<cuuint32_t>(row_tiles)};
-    return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, map, base, 3, dims, strides, box);
-}
 
 // Results: boxes of 64 bytes x 32 rows.
 bool out_map(CUtensorMap* map, const void* base, bool f32, int64_t M, int64_t N, int64_t stride)
@@ -557,6 +537,22 @@ cudaError_t launch(ProductParams& p, cudaStream_t s)
 }
 
 }  // namespace
+
+bool mx4_codes_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, int box_rows)
+{
+    const cuuint64_t pitch = static_cast<cuuint64_t>(tiles) * kMx4TileBytes;
+    const cuuint64_t dims[3] = {pitch, static_cast<cuuint64_t>(rows), 1}, strides[2] = {pitch, pitch * static_cast<cuuint64_t>(rows)};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+    return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, map, base, 3, dims, strides, box);
+}
+
+bool mx4_scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int tiles, int box_tiles, int box_row_tiles)
+{
+    const cuuint64_t n = static_cast<cuuint64_t>((rows + kMx4Tile - 1) / kMx4Tile);
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(tiles), n}, strides[2] = {512, static_cast<cuuint64_t>(tiles) * 512};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_tiles), static_cast<cuuint32_t>(box_row_tiles)};
+    return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, map, base, 3, dims, strides, box);
+}
 
 namespace {
 
@@ -614,8 +610,8 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     p.m_fastest = q.N > q.M;
     p.inner = p.m_fastest ? mtiles : ntiles;
     p.units = mtiles * ntiles * p.splits;
-    if (!codes_map(&p.a, q.a, q.M, q.tiles, CM) || !codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) || !scales_map(&p.as, q.as, q.M, q.tiles, 1) ||
-        !scales_map(&p.bs, q.bs, q.N, q.tiles, 2))
+    if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, CM) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) ||
+        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, 2))
         return cudaErrorInvalidValue;
     const int64_t size = q.out_f32 ? 4 : 2, pitch = q.out_stride * size;
     // (a store's last 16 bytes of a row are written whole)

@@ -1,155 +1,271 @@
-// Products of a few rows with a 4-bit matrix: out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]) for at most 32 rows of a.
+// Products of a few rows with a 4-bit matrix: out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]) for at most 64 rows of a.
 //
 // Every byte of b is read once and takes part in few operations, so that reading b bounds this, and at small sizes the latency of
-// a launch.  tcgen05's tiles would leave most SMs idle at the depths and widths of a layer; here a block takes 16 rows of b, whose
-// warps share out the depth, and multiplies with mma.sync m16n8k16: rows of b by up to 8, 16 or 32 rows of a, both decoded to fp16,
-// which holds every e2m1 number.  A thread's four bytes of a row are 8 columns, and any order of the columns will do as long as
-// both operands have it: two MMAs take a block of 32, whose sum is exact (products are multiples of 1/4 up to 36).  It is scaled
-// by the power of two of its row and its column and added up in fp32.
-// The 16 rows are 4 neighbours and those 32, 64 and 96 behind them: their scales lie together, 64 bytes a tile of 128 columns.
+// a launch.  The operands change places: 128 rows of b are the rows of a tcgen05 MMA (kind::mxf4, M = 128), and the rows of a its
+// 16, 32 or 64 columns, so that an MMA takes a fraction of the time that its rows of b take to come.  (Decoding b on the CUDA cores
+// for mma.sync was bound by that: 3 rows at 5120 x 20480 took 30 us.)  A CTA has four stages of 256 columns, 16 KB of b each, and two
+// CTAs fit an SM.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
+// shared memory, and each adds up, in the order of the parts, and writes its share of the rows of a.
+//   warps 0-3: epilogue, thread = row of b: its sums lie in its lane of tensor memory, and a warp's stores of a row of out are
+//   neighbours; warp 4: TMA producer; warp 5: scale copies and MMAs.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "chained.cuh"
+#include "internal.h"
 #include "mx4.cuh"
+#include "mx4_maps.h"
+#include "per_device.h"
 #include "project.h"
+#include "ptx.cuh"
+#include "ptx_mx4.cuh"
+#include "ptx_pair.cuh"
 
 namespace sdv2 {
 namespace {
 
-constexpr int kMaxWarps = 8;
-constexpr int kTogether = 2;               // tiles of a warp whose loads are under way together
+constexpr int ROWS = 128;                      // of b, of a CTA
+constexpr int STEP_TILES = 2;                  // scale tiles (128 columns) of a stage
+constexpr int STAGES = 4;
+constexpr int B_FULL = 0, B_EMPTY = STAGES, B_DONE = 2 * STAGES, NBARS = 2 * STAGES + 1;
+constexpr uint32_t COL_BS = 64, COL_AS = COL_BS + 4 * STEP_TILES, TMEM_COLS = 128;    // of tensor memory, behind the sums
+constexpr int THREADS = 6 * 32;
+constexpr uint32_t B_BYTES = ROWS * 128, SCALE_BYTES = STEP_TILES * 512;
+constexpr int kMaxParts = 8;
 
-__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+// What depends on the columns of the MMA, as many rows of a.
+template <int COLS>
+struct Stage {
+    static constexpr uint32_t A_BYTES = COLS * 128;
+    static constexpr uint32_t BYTES = B_BYTES + A_BYTES + 2 * SCALE_BYTES;
+    static constexpr uint32_t BAR_OFF = STAGES * BYTES;
+    static constexpr uint32_t SMEM_BYTES = BAR_OFF + 128 + 1024;
+    static_assert(BYTES % 1024 == 0 && NBARS * 8 + 8 <= 128, "128-byte swizzle; barriers");
+    static_assert(ROWS * COLS * 4 <= STAGES * BYTES && 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "sums of the other parts; two CTAs an SM");
+};
+
+struct RowsParams {
+    CUtensorMap a, as, b, bs;
+    const float* bias;
+    void* out;
+    int64_t out_stride;
+    uint32_t* err;
+    uint64_t timeout_ns;
+    int64_t drop;
+    int32_t M, N, steps, parts, out_f32, gelu;
+};
+
+template <int COLS>
+__global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant__ RowsParams p)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+    using S = Stage<COLS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s0 = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t bar0 = smem_u32(bars);
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const int part = static_cast<int>(cluster_ctarank());
+    const int n0 = static_cast<int>(cluster_id_x()) * ROWS;
+    const int steps = p.steps / p.parts + (part < p.steps % p.parts);
+    const int first = p.steps / p.parts * part + min(part, p.steps % p.parts);
+    const uint64_t tmo = p.timeout_ns;
 
-__device__ __forceinline__ void decode(uint32_t codes, uint32_t (&x)[4])
-{
-    __half2 h[4];
-    mx4_numbers(codes, h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<uint32_t*>(&h[i]);
-}
-
-__device__ __forceinline__ int byte_of(uint32_t word, int i) { return static_cast<int>((word >> (8 * i)) & 255u); }
-
-// NT: groups of 8 rows of a
-template <int NT>
-__global__ void __launch_bounds__(32 * kMaxWarps) rows_kernel(const Mx4Product p)
-{
-    constexpr int COLS = 8 * NT;
-    __shared__ float sums[kMaxWarps][16 * COLS];
-    wait_for_launch_before();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int g = lane >> 2, t = lane & 3, M = static_cast<int>(p.M);
-    const int64_t row_tile = blockIdx.x >> 3;
-    const int q0 = static_cast<int>(blockIdx.x & 7) * 4;
-    const int64_t pitch = static_cast<int64_t>(p.tiles) * kMx4TileBytes;
-    // rows g and g + 8 of the block's
-    const uint8_t* b[2];
-    const uint8_t* bs[2];
-    bool have[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int i = g + 8 * h, in_tile = q0 + (i & 3) + 32 * (i >> 2);
-        const int64_t n = row_tile * kMx4Tile + in_tile;
-        have[h] = n < p.N;
-        b[h] = p.b + (have[h] ? n : 0) * pitch + t * 4;
-        bs[h] = p.bs + row_tile * p.tiles * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NBARS; ++i) mbar_init(bar(i), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
     }
-    float acc[NT][4] = {};
-    bool nan_b[2] = {}, nan_a[NT][2] = {};
-    for (int k0 = warp; k0 < p.tiles; k0 += kTogether * warps) {
-        uint32_t bc[kTogether][2][4], bw[kTogether][2], ac[kTogether][NT][4], aw[kTogether][NT][2];
-#pragma unroll
-        for (int u = 0; u < kTogether; ++u) {
-            const int k = k0 + u * warps;
-            const bool in = k < p.tiles;
-            const int64_t at = static_cast<int64_t>(k) * kMx4TileBytes, scale_at = static_cast<int64_t>(k) * 512;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                bw[u][h] = in && have[h] ? *reinterpret_cast<const uint32_t*>(bs[h] + scale_at) : 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) bc[u][h][j] = in && have[h] ? *reinterpret_cast<const uint32_t*>(b[h] + at + j * 16) : 0;
-            }
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int m = 8 * c + 2 * t + h;
-                    aw[u][c][h] = in && m < M ? *reinterpret_cast<const uint32_t*>(p.as + scale_at + m * 16) : 0;
-                }
-                const int m = 8 * c + g;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    ac[u][c][j] = in && m < M ? *reinterpret_cast<const uint32_t*>(p.a + m * pitch + at + t * 4 + j * 16) : 0;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kTogether; ++u) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                nan_b[h] |= __vcmpeq4(bw[u][h], 0xFFFFFFFFu) != 0;
-#pragma unroll
-                for (int c = 0; c < NT; ++c) nan_a[c][h] |= __vcmpeq4(aw[u][c][h], 0xFFFFFFFFu) != 0;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t x0[4], x1[4];
-                decode(bc[u][0][j], x0);
-                decode(bc[u][1][j], x1);
-#pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    uint32_t y[4];
-                    decode(ac[u][c][j], y);
-                    float s[4] = {};
-                    mma_16x8x16(s, x0[0], x1[0], x0[1], x1[1], y[0], y[1]);
-                    mma_16x8x16(s, x0[2], x1[2], x0[3], x1[3], y[2], y[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // 2^(eb + ea), 0 below fp32's normal numbers and 2^127 above them
-                        const int e = byte_of(bw[u][i >> 1], j) + byte_of(aw[u][c][i & 1], j) - 127;
-                        acc[c][i] = fmaf(s[i], __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23), acc[c][i]);
-                    }
-                }
-            }
-        }
+    if (threadIdx.x == 128) {
+        tma_prefetch_desc(&p.b);
+        tma_prefetch_desc(&p.bs);
+        tma_prefetch_desc(&p.a);
+        tma_prefetch_desc(&p.as);
     }
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool bad = nan_b[i >> 1] || nan_a[c][i & 1];
-            sums[warp][(g + 8 * (i >> 1)) * COLS + 8 * c + 2 * t + (i & 1)] = bad ? __uint_as_float(0x7FC00000u) : acc[c][i];
-        }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    for (int o = threadIdx.x; o < 16 * M; o += blockDim.x) {
-        const int m = o >> 4, i = o & 15;
-        const int64_t n = row_tile * kMx4Tile + q0 + (i & 3) + 32 * (i >> 2);
-        if (n >= p.N) continue;
-        float y = sums[0][i * COLS + m];
-        for (int w = 1; w < warps; ++w) y += sums[w][i * COLS + m];
-        if (p.bias) y += p.bias[n];
-        if (p.gelu) y = gelu(y);
-        const int64_t at = m * p.out_stride + n;
-        if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    wait_for_launch_before();
+
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+    };
+    if (warp == 4) {
+        if (lane == 0) {
+            int issued = 0;
+            for (; issued < steps; ++issued) {
+                const int st = issued % STAGES, k = first + issued;
+                if (!mbar_wait_bounded(bar(B_EMPTY + st), (static_cast<uint32_t>(issued / STAGES) & 1u) ^ 1u, tmo, abort_flag)) {
+                    give_up();
+                    break;
+                }
+                const uint32_t sb = s0 + st * S::BYTES, full = bar(B_FULL + st);
+                mbar_arrive_expect_tx(full, S::BYTES);
+                if (k == p.drop) continue;
+                tma_load_3d(sb, &p.b, full, k * 128, n0, 0);
+                tma_load_3d(sb + B_BYTES, &p.a, full, k * 128, 0, 0);
+                tma_load_3d(sb + B_BYTES + S::A_BYTES, &p.bs, full, 0, k * STEP_TILES, n0 / 128);
+                tma_load_3d(sb + B_BYTES + S::A_BYTES + SCALE_BYTES, &p.as, full, 0, k * STEP_TILES, 0);
+            }
+            // the last copies land before their memory is used again or left
+            volatile int no_abort = 0;
+            for (int g = max(0, issued - STAGES); g < issued; ++g)
+                mbar_wait_bounded(bar(B_FULL + g % STAGES), static_cast<uint32_t>(g / STAGES) & 1u, tmo, &no_abort);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        const uint64_t dB = sdesc_sw128(s0, 16, 1024), dA = sdesc_sw128(s0 + B_BYTES, 16, 1024);
+        const uint64_t dBS = sdesc_scales(s0 + B_BYTES + S::A_BYTES), dAS = sdesc_scales(s0 + B_BYTES + S::A_BYTES + SCALE_BYTES);
+        int st = 0;
+        uint32_t phase = 0;
+        uint64_t at = 0;
+        for (int i = 0; i < steps; ++i) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_FULL + st), phase, tmo, abort_flag))) {
+                if (lane == 0) give_up();
+                break;
+            }
+            tc_fence_after();
+            mx4_stage_warp(tmem, dB + at, dA + at, dBS + at, dAS + at, tmem + COL_BS, tmem + COL_AS, idesc_mx4(ROWS, COLS, 0), idesc_mx4(ROWS, COLS, 1),
+                           i > 0 ? 1u : 0u);
+            mma_commit_warp(bar(B_EMPTY + st));
+            at += S::BYTES >> 4;
+            if (++st == STAGES) {
+                st = 0;
+                at = 0;
+                phase ^= 1u;
+            }
+        }
+        mma_commit_warp(bar(B_DONE));
+        if (lane == 0) {
+            volatile int no_abort = 0;
+            mbar_wait_bounded(bar(B_DONE), 0, tmo, &no_abort);
+        }
+        __syncwarp();
+    } else {
+        const bool ok = mbar_wait_bounded(bar(B_DONE), 0, tmo, abort_flag);
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) give_up();
     }
+    __syncthreads();
+    const bool sound = !*abort_flag;
+    const int row = warp * 32 + lane, n = n0 + row;
+    const float bias = warp < 4 && p.bias && n < p.N ? p.bias[n] : 0.0f;
+    auto write = [&](int m, float y) {
+        y += bias;
+        if (p.gelu) y = gelu(y);
+        const int64_t o = m * p.out_stride + n;
+        if (p.out_f32) static_cast<float*>(p.out)[o] = y;
+        else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+    };
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    tc_fence_after();
+    if (p.parts == 1) {
+        if (warp < 4 && sound) {
+#pragma unroll 1
+            for (int m0 = 0; m0 < p.M; m0 += 16) {
+                uint32_t y[16];
+                tmem_ld_x16_sync(lanes + m0, y);
+#pragma unroll
+                for (int m = 0; m < 16; ++m)
+                    if (m0 + m < p.M && n < p.N) write(m0 + m, __uint_as_float(y[m]));
+            }
+        }
+    } else {
+        // [part][row of a][row of b] of the CTA that adds up this row of a
+        const int shift = 31 - __clz(COLS / p.parts), share = 1 << shift;
+        cluster_sync_all();                                      // every ring is free
+        if (warp < 4 && sound) {
+            const uint32_t slot = s0 + static_cast<uint32_t>((part * share * ROWS + row) * 4);
+#pragma unroll 1
+            for (int m0 = 0; m0 < p.M; m0 += 16) {
+                uint32_t y[16];
+                tmem_ld_x16_sync(lanes + m0, y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int m = m0 + j;
+                    if (m < p.M)
+                        st_cluster(map_to_rank(slot + static_cast<uint32_t>((m & (share - 1)) * (ROWS * 4)), static_cast<uint32_t>(m >> shift)),
+                                   static_cast<int32_t>(y[j]));
+                }
+            }
+        }
+        cluster_sync_all();
+        if (warp < 4 && sound && n < p.N) {
+            const float* sums = reinterpret_cast<const float*>(smem) + row;
+            const int m0 = part * share, rows = min(share, p.M - m0);
+            for (int j = 0; j < rows; ++j) {
+                float y = sums[j * ROWS];
+                for (int from = 1; from < p.parts; ++from) y += sums[(from * share + j) * ROWS];
+                write(m0 + j, y);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <int COLS>
+cudaError_t launch(const Mx4Product& q, cudaStream_t s)
+{
+    RowsParams p{};
+    if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, COLS) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, ROWS) ||
+        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, 1))
+        return cudaErrorInvalidValue;
+    p.bias = q.bias;
+    p.out = q.out;
+    p.out_stride = q.out_stride;
+    p.err = q.err;
+    p.timeout_ns = q.timeout_ns;
+    p.drop = q.drop;
+    p.M = static_cast<int32_t>(q.M);
+    p.N = static_cast<int32_t>(q.N);
+    p.steps = (q.tiles + STEP_TILES - 1) / STEP_TILES;
+    p.out_f32 = q.out_f32;
+    p.gelu = q.gelu;
+    const int64_t clusters = (q.N + ROWS - 1) / ROWS;
+    // Parts of the depth for as many CTAs as the GPU holds (two an SM), of four steps at least: 3 rows at 5120 x 20480 take 25.0 us
+    // in one part and 13.1 in four, at 9216 x 1536 (six steps) 4.5 us in one and 5.3 in four.
+    p.parts = 1;
+    while (p.parts < kMaxParts && clusters * p.parts * 2 <= 304 && p.steps >= 8 * p.parts) p.parts *= 2;
+    constexpr int kBytes = static_cast<int>(Stage<COLS>::SMEM_BYTES);
+    static PerDevice once;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = once.run(dev, [] { return cudaFuncSetAttribute(rows_kernel<COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes); });
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2] = {chained_attribute(), {}};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * p.parts));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, rows_kernel<COLS>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s)
 {
-    const int warps = std::min(kMaxWarps, (p.tiles + kTogether - 1) / kTogether);
-    const unsigned grid = static_cast<unsigned>((p.N + kMx4Tile - 1) / kMx4Tile * 8);
-    auto kernel = p.M <= 8 ? rows_kernel<1> : p.M <= 16 ? rows_kernel<2> : rows_kernel<4>;
-    return launch_chained(kernel, grid, 32 * warps, 0, s, p);
+    return p.M <= 16 ? launch<16>(p, s) : p.M <= 32 ? launch<32>(p, s) : launch<64>(p, s);
 }
 
 }  // namespace sdv2

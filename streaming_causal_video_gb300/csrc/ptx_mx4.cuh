@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cstdint>
 
+#include "tmem_io.cuh"
+
 namespace sdv2 {
 
 // Instruction descriptor of kind::mxf4: A and B e2m1 (1, at bits 7 and 10), scales ue8m0 (bit 23), N/8 at bit 17, M/128 at bit
@@ -65,6 +67,38 @@ __device__ __forceinline__ void mx4_stage_pair_warp(uint32_t sums, uint64_t a, u
         : "memory");
 }
 
+// The same within one CTA, of 128 rows of a and few rows of b, whose scales are one row tile's as well (4 columns a tile).
+__device__ __forceinline__ void mx4_stage_warp(uint32_t sums, uint64_t a, uint64_t b, uint64_t as, uint64_t bs, uint32_t a_scales, uint32_t b_scales,
+                                               uint32_t i0, uint32_t i1, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        ".reg .b64 x, y;\n\t"
+        ".reg .b32 t, u;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %9, 0;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], %3;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%6], %4;\n\t"
+        "add.s32 t, %5, 4;\n\t"
+        "add.s64 x, %3, 32;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t], x;\n\t"
+        "add.s32 u, %6, 4;\n\t"
+        "add.s64 x, %4, 32;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [u], x;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %7, [%5], [%6], p;\n\t"
+        "add.s64 x, %1, 2;\n\t"
+        "add.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [%5], [%6], 1;\n\t"
+        "add.s64 x, %1, 4;\n\t"
+        "add.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %7, [t], [u], 1;\n\t"
+        "add.s64 x, %1, 6;\n\t"
+        "add.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [t], [u], 1;\n\t}" ::"r"(sums),
+        "l"(a), "l"(b), "l"(as), "l"(bs), "r"(a_scales), "r"(b_scales), "r"(i0), "r"(i1), "r"(accumulate)
+        : "memory");
+}
+
 // Bytes that a barrier of this CTA was told to expect and that no copy will bring.
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes)
 {
@@ -90,5 +124,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+
+// 16 or 32 columns of this thread's lane, and waits for them.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16_sync(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32_sync(taddr, r); }
 
 }  // namespace sdv2

@@ -110,10 +110,10 @@ class Product:
 
 
 FEW = [(1, 1, 1), (1, 128, 128), (2, 33, 129), (3, 9216, 1536), (4, 127, 31), (5, 257, 1050), (8, 1000, 2080), (1, 40, 20480),
-       (7, 300, 9000)]
-TILES = [(9, 1, 1), (16, 7, 32), (256, 256, 256), (128, 128, 128), (129, 255, 257), (100, 130, 1), (255, 257, 64), (257, 256, 127),
+       (7, 300, 9000), (9, 130, 640), (16, 257, 9000), (17, 1000, 1100), (31, 129, 256), (32, 513, 4096), (33, 640, 1280), (64, 300, 7001)]
+TILES = [(65, 1, 1), (70, 7, 32), (256, 256, 256), (128, 128, 128), (129, 255, 257), (100, 130, 1), (255, 257, 64), (257, 256, 127),
          (300, 500, 700), (1001, 777, 1050), (600, 300, 1280), (520, 1536, 1536)]
-DEEP = [(9, 300, 8200), (77, 1536, 8960), (512, 700, 4096), (300, 260, 20480), (256, 250, 7001)]
+DEEP = [(65, 300, 8200), (77, 1536, 8960), (512, 700, 4096), (300, 260, 20480), (256, 250, 7001)]
 
 
 @pytest.mark.parametrize("out_dtype", [FP, BF], ids=["f32", "bf16"])
