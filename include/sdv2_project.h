@@ -139,7 +139,7 @@ typedef struct {
     int64_t tokens;            /* in [1, 2^30]                                                  */
     int32_t dtype;             /* sdv2_dtype of q and k, in and out                             */
     int32_t axes;              /* in [1, 4]                                                     */
-    int32_t dims[4];           /* each even and >= 2, their sum <= head_dim                     */
+    int32_t dims[4];           /* each even and >= 0, their sum <= head_dim                     */
     int32_t halves;
     int32_t shared_positions;  /* 0: positions [batch][tokens][axes]; 1: [tokens][axes]         */
     double base;               /* in (1, 1e100]                                                 */

@@ -64,4 +64,4 @@ from ._project import (  # noqa: F401
     mx4_workspace_bytes,
     mx4_workspace_init,
 )
-from .layer import LayerCache, StreamSession  # noqa: F401
+from .layer import LayerCache, Mx4Matrix, StreamSession  # noqa: F401

@@ -48,7 +48,7 @@ class RopeStrides(ctypes.Structure):
 
 class AxesRopeConfig(_Config):
     """Mirror of sdv2_axes_rope_cfg.  make() takes dims and scale as sequences of one value per axis, and strides as
-    mappings of token_stride, head_stride and batch_stride."""
+    mappings of token_stride, head_stride and batch_stride.  To change strides later, assign a new RopeStrides."""
     _fields_ = [("batch", _i32), ("heads", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("tokens", _i64), ("dtype", _i32),
                 ("axes", _i32), ("dims", _i32 * 4), ("halves", _i32), ("shared_positions", _i32), ("base", _f64),
                 ("scale", _f64 * 4), ("q_in", RopeStrides), ("q_out", RopeStrides), ("k_in", RopeStrides), ("k_out", RopeStrides)]

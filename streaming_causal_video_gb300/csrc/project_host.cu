@@ -96,7 +96,7 @@ sdv2_status check_rope(const sdv2_axes_rope_cfg* c)
     if (c->axes < 1 || c->axes > 4) return refuse(SDV2_ERR_INVALID_ARG, "axes (%d) must be in [1, 4]", c->axes);
     int64_t sum = 0;
     for (int a = 0; a < c->axes; ++a) {
-        if (c->dims[a] < 2 || c->dims[a] % 2) return refuse(SDV2_ERR_INVALID_ARG, "dims[%d] (%d) must be even and >= 2", a, c->dims[a]);
+        if (c->dims[a] < 0 || c->dims[a] % 2) return refuse(SDV2_ERR_INVALID_ARG, "dims[%d] (%d) must be even and >= 0", a, c->dims[a]);
         if (!(std::fabs(c->scale[a]) <= 0x1p20)) return refuse(SDV2_ERR_INVALID_ARG, "scale[%d] must be a number of at most 2^20", a);
         sum += c->dims[a];
     }
@@ -153,6 +153,7 @@ int rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
     auto fits = [&](int half) { width = half % width == 0 ? width : half % 2 == 0 ? 2 : 1; };
     for (int a = 0; a < c->axes; ++a) {
         const int d = c->dims[a];
+        if (d == 0) continue;
         fits(d / 2);
         const double scale = c->scale[a] == 0.0 ? 1.0 : c->scale[a];
         const bool negative = (scale < 0) != backward;
@@ -169,7 +170,7 @@ int rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
         first += d;
     }
     const int rest = c->head_dim - first;
-    fits(rest / 2);
+    if (rest) fits(rest / 2);
     for (int j = 0; j < rest / 2; ++j) {
         RopePair& q = p->pair[n++];
         q = RopePair{};

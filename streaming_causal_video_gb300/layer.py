@@ -4,13 +4,17 @@ A StreamSession owns the workspace, one LayerCache (k, v, slot metadata) per DiT
 q_rot / out buffers; layer_step() issues sdv2_rope_append_kv then sdv2_chunk_attention for one
 layer of one denoise step.  Around it, norm_step() normalises a chunk's tokens (before the
 projections) and cross_step() attends to the layer's prompt states, which set_prompt() names and
-which stay for all chunks and steps until the prompt changes.  Nothing here computes: it allocates
-and calls the library.
+which stay for all chunks and steps until the prompt changes.  project_step() multiplies tokens by
+weights held in 4 bits (Mx4Matrix), and rope_step() turns queries and keys that do not go into the
+cache.  Nothing here computes: it allocates and calls the library.
 """
 import torch
 
 from . import _binding as sd
 from . import _block as block
+from . import _project as project
+
+_KINDS = {torch.bfloat16: block.BF16, torch.float32: block.F32}
 
 
 class LayerCache:
@@ -43,6 +47,57 @@ def _rows_of(t, name, groups, cols):
     return t, stride
 
 
+class Mx4Matrix:
+    """A matrix of microscaled 4-bit numbers: codes and scales as sdv2_mx4_quantize writes them.
+
+    A weight [N][K] is loaded once; activations [M][K] are loaded for every product.  For gradients a matrix can be loaded from its
+    transpose: with y = x w^T, dx is the product of dy [M][N] and w loaded as [K][N], dw that of dy and x loaded as [N][M] and [K][M].
+    """
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        cfg = project.Mx4Config.make(rows=rows, cols=cols)
+        if not project.mx4_codes_bytes(cfg):
+            raise ValueError("a matrix has at least one row and one column, not %d and %d" % (rows, cols))
+        self.rows, self.cols = rows, cols
+        self.codes = torch.empty(project.mx4_codes_bytes(cfg), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(project.mx4_scales_bytes(cfg), dtype=torch.uint8, device=device)
+        self.configs = {}              # of load and values, which follow from type, stride and direction
+
+    @classmethod
+    def of(cls, x, transposed=False, stream=None):
+        """A new matrix loaded from x [rows][cols], or from x [cols][rows]."""
+        if x.dim() != 2:
+            raise ValueError("x must have two dimensions, not %d" % x.dim())
+        rows, cols = reversed(x.shape) if transposed else x.shape
+        return cls(rows, cols, x.device).load(x, transposed, stream)
+
+    def _config(self, x, transposed):
+        shape = (self.cols, self.rows) if transposed else (self.rows, self.cols)
+        if x.dtype not in _KINDS or tuple(x.shape) != shape:
+            raise ValueError("expected bf16 or fp32 %s, got %s %s" % (shape, x.dtype, tuple(x.shape)))
+        if x.stride(1) != 1 and shape[1] > 1:
+            raise ValueError("rows must be dense, not %d elements apart" % x.stride(1))
+        stride = x.stride(0) if shape[0] > 1 else 0
+        if shape[0] > 1 and stride < shape[1]:
+            raise ValueError("rows of %d elements cannot lie %d apart" % (shape[1], stride))
+        key = (x.dtype, stride, transposed)
+        cfg = self.configs.get(key)
+        if cfg is None:
+            cfg = self.configs[key] = project.Mx4Config.make(rows=self.rows, cols=self.cols, x_dtype=_KINDS[x.dtype],
+                                                             transposed=int(transposed), x_row_stride=stride)
+        return cfg
+
+    def load(self, x, transposed=False, stream=None):
+        """Quantises x [rows][cols] (transposed: [cols][rows]), bf16 or fp32 with any stride between rows."""
+        project.mx4_quantize(self._config(x, transposed), x, self.codes, self.scales, stream)
+        return self
+
+    def values(self, out, stream=None):
+        """Writes the values that the matrix stands for into out [rows][cols], bf16 or fp32."""
+        project.mx4_dequantize(self._config(out, False), self.codes, self.scales, out, stream)
+        return out
+
+
 class StreamSession:
     def __init__(self, cfg: sd.StreamConfig, layers: int, start_frames, device="cuda", stream=None):
         self.cfg = cfg
@@ -56,6 +111,10 @@ class StreamSession:
         self.prompts = [None] * layers
         self.cross_ws = None
         self.norms = {}                # norm_step's configurations, which follow from shapes, types and strides
+        self.products = {}             # project_step's, and the 4-bit forms of its activations by their sizes
+        self.loaded = {}
+        self.product_ws = None
+        self.ropes = {}                # rope_step's
 
     def layer_step(self, layer: int, chunk_index, q, k, v, out=None, lse=None, stream=None):
         """Causal-RoPE + cache append, then chunk attention, for one layer.  q, k, v: [B][Nq][H][D]."""
@@ -106,8 +165,7 @@ class StreamSession:
         """Layer norm of a chunk's tokens x [B][Nq][C] (bf16 or fp32) into out [B][Nq][C].  weight, bias fp32: [C], the
         learned affine; or, modulated, [B*F][C], the scale and shift of every latent frame: xhat * (1 + weight) + bias.
         Those may be slices of one modulation tensor such as [B*F][6][C] (of the same one, as they share a stride)."""
-        kinds = {torch.bfloat16: block.BF16, torch.float32: block.F32}
-        if x.dtype not in kinds or out.dtype not in kinds:
+        if x.dtype not in _KINDS or out.dtype not in _KINDS:
             raise ValueError("x and out must be bf16 or fp32")
         if x.shape != out.shape or not x.is_contiguous() or not out.is_contiguous():
             raise ValueError("x and out must be contiguous and of one shape")
@@ -122,7 +180,82 @@ class StreamSession:
         cfg = self.norms.get(key)
         if cfg is None:
             cfg = self.norms[key] = block.NormConfig.make(
-                rows=rows, cols=C, x_dtype=kinds[x.dtype], y_dtype=kinds[out.dtype], weight_plus_one=int(modulated),
+                rows=rows, cols=C, x_dtype=_KINDS[x.dtype], y_dtype=_KINDS[out.dtype], weight_plus_one=int(modulated),
                 rows_per_group=self.cfg.hw if modulated else 0, group_stride=stride or bias_stride, eps=eps)
         block.layer_norm(cfg, x, out, weight=weight, bias=bias, stream=stream)
         return out
+
+    def quantize_step(self, x, stream=None):
+        """x [...][K] (bf16 or fp32, contiguous) in 4 bits, for several products of the same activations.  What it returns is the
+        session's and holds until its next activations of this size."""
+        if x.dim() < 1 or not x.is_contiguous() or not x.numel():
+            raise ValueError("x must be contiguous and hold at least one row")
+        rows, cols = x.numel() // x.shape[-1], x.shape[-1]
+        m = self.loaded.get((rows, cols))
+        if m is None:
+            m = self.loaded[rows, cols] = Mx4Matrix(rows, cols, self.ws.device)
+        return m.load(x.view(rows, cols), stream=stream)
+
+    def project_step(self, weight: Mx4Matrix, x, out, bias=None, activation=project.NO_ACTIVATION, stream=None):
+        """out [...][N] = act(x w^T + bias) for a weight [N][K] in 4 bits; x: [...][K], bf16 or fp32, or what quantize_step made of
+        it; out: contiguous, bf16 or fp32; bias: fp32 [N]; activation: NO_ACTIVATION or GELU."""
+        if out.dtype not in _KINDS or out.dim() < 1 or not out.is_contiguous():
+            raise ValueError("out must be contiguous bf16 or fp32")
+        a = x if isinstance(x, Mx4Matrix) else self.quantize_step(x, stream)
+        if a.cols != weight.cols:
+            raise ValueError("x has %d columns, the weight %d" % (a.cols, weight.cols))
+        if out.shape[-1] != weight.rows or out.numel() != a.rows * weight.rows:
+            raise ValueError("out is %s, not %d rows of %d" % (tuple(out.shape), a.rows, weight.rows))
+        if bias is not None and bias.numel() != weight.rows:
+            raise ValueError("bias has %d values, not %d" % (bias.numel(), weight.rows))
+        key = (a.rows, weight.rows, a.cols, out.dtype, activation)
+        cfg = self.products.get(key)
+        if cfg is None:
+            cfg = self.products[key] = project.Mx4ProductConfig.make(rows=a.rows, cols=weight.rows, depth=a.cols,
+                                                                     out_dtype=_KINDS[out.dtype], activation=activation)
+        if self.product_ws is None:            # one serves every product
+            ws = torch.empty(project.mx4_workspace_bytes(cfg), dtype=torch.uint8, device=self.ws.device)
+            project.mx4_workspace_init(cfg, ws, stream)
+            self.product_ws = ws
+        project.mx4_product(cfg, a.codes, a.scales, weight.codes, weight.scales, out.view(a.rows, weight.rows), self.product_ws, bias=bias,
+                            stream=stream)
+        return out
+
+    def chunk_positions(self, chunk_index):
+        """int32 [B][Nq][3]: time index, row and column of a chunk's tokens, the places that layer_step turns them by."""
+        c = self.cfg
+        n = torch.arange(c.nq)
+        grid = torch.stack([n // c.hw, n % c.hw // c.grid_w, n % c.grid_w], -1)
+        pos = grid.expand(c.batch, c.nq, 3).clone()
+        for b, (start, chunk) in enumerate(zip(self.start_frames, chunk_index)):
+            pos[b, :, 0] += start + c.chunk_frames * (chunk % c.refresh_chunks if c.refresh_chunks else chunk)
+        return pos.to(device=self.ws.device, dtype=torch.int32)
+
+    def rope_step(self, positions, q, q_out, k=None, k_out=None, stream=None):
+        """Turns q [B][N][H][D], and k, by their places on the session's three axes: positions int32 [B][N][3], or [N][3] for all of
+        the batch.  bf16 or fp32 views with any strides of whole 16 bytes; q_out may be q itself, k_out k."""
+        c = self.cfg
+        if q.dim() != 4 or q.dtype not in _KINDS or q.shape != q_out.shape or (k is not None and (k.dim() != 4 or k.shape != k_out.shape)):
+            raise ValueError("q, k and their results must be bf16 or fp32 [B][N][H][D], each of one shape with its result")
+        if k is not None and (k.shape[0], k.shape[1], k.shape[3]) != (q.shape[0], q.shape[1], q.shape[3]):
+            raise ValueError("k must have q's batch, tokens and head dim")
+        if q.shape[3] != c.head_dim:
+            raise ValueError("q has heads of %d dims, the session of %d" % (q.shape[3], c.head_dim))
+        if tuple(positions.shape) not in ((q.shape[0], q.shape[1], 3), (q.shape[1], 3)):
+            raise ValueError("positions must be [B][N][3] or [N][3], not %s" % (tuple(positions.shape),))
+        tensors = (q, q_out, k, k_out)
+        key = (q.shape, q.dtype, positions.dim(), *(None if t is None else (t.shape[2], t.stride()) for t in tensors))
+        cfg = self.ropes.get(key)
+        if cfg is None:
+            def strides(t):            # a dimension of size one has no stride to speak of
+                if t is None:
+                    return {}
+                of = lambda i: t.stride(i) if t.shape[i] > 1 else 0
+                return dict(token_stride=of(1), head_stride=of(2), batch_stride=of(0))
+            names = ("q_in", "q_out", "k_in", "k_out")
+            cfg = self.ropes[key] = project.AxesRopeConfig.make(
+                batch=q.shape[0], tokens=q.shape[1], heads=q.shape[2], kv_heads=0 if k is None else k.shape[2], head_dim=q.shape[3],
+                dims=(c.rope_t, c.rope_h, c.rope_w), base=c.rope_base, dtype=_KINDS[q.dtype], shared_positions=int(positions.dim() == 2),
+                **{n: strides(t) for n, t in zip(names, tensors)})
+        project.axes_rope(cfg, positions, q, q_out, k, k_out, stream)
+        return q_out
