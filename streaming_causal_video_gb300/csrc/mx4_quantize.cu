@@ -4,6 +4,8 @@
 // instructions.  A block of 256 threads takes 16 rows, 16 threads a row; a thread has 8 neighbouring columns of a tile of 128 and
 // two or four tiles, all of whose loads are under way together, at addresses that differ by constants.  The 16 rows are 4
 // neighbours and those 32, 64 and 96 behind them, whose scales lie together (64 bytes a tile).
+// Each lets the next launch set itself up at once, whose blocks then take the SMs that it leaves: quantisation and product of
+// 512 x 1536, depth 4096, take 13.8 us without and 13.1 with that, 3 x 9216, depth 1536, 7.1 and 6.5.
 // A row that is not whole vectors of 8 columns is read and written number by number, 16 neighbours at once, by way of shared
 // memory.
 #include <cuda_bf16.h>
@@ -53,6 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params
 {
     __shared__ __align__(16) float staged[VECTORS ? 1 : kRows * kMx4Tile];
     wait_for_launch_before();
+    launch_dependents();
     const Place<kUnroll> at(p, row_groups);
     const int lane = threadIdx.x & 15;
     const bool live = at.row < p.rows;
@@ -153,6 +156,7 @@ __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx
     __shared__ __align__(16) uint8_t codes[kTRows * kTPitch];
     __shared__ __align__(16) uint8_t scales[kTRows * 4];
     wait_for_launch_before();
+    launch_dependents();
     const int tile = static_cast<int>(blockIdx.x / row_blocks);
     const int64_t r0 = static_cast<int64_t>(blockIdx.x % row_blocks) * kTRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Mx4Params p,
 {
     __shared__ __align__(16) float staged[VECTORS ? 1 : kRows * kMx4Tile];
     wait_for_launch_before();
+    launch_dependents();
     const Place<kUnroll> at(p, row_groups);
     const int lane = threadIdx.x & 15;
     const bool live = at.row < p.rows;

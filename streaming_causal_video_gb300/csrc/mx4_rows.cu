@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     wait_for_launch_before();
+    launch_dependents();
 
     auto give_up = [&]() {
         *abort_flag = 1;
