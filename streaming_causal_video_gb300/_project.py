@@ -80,11 +80,14 @@ class AxesRopeConfig(_Config):
                 operand(self.kv_heads, self.k_out), places * max(self.axes, 0) * 4)
 
 
+_Tensor = torch.Tensor
+
+
 def _here(t):
     """The current device if t is a tensor on it, else a number that is no tensor's device."""
-    if t.__class__ is torch.Tensor and t.is_cuda:
+    if t.__class__ is _Tensor:
         d = t.get_device()
-        if d == _current_device():
+        if d >= 0 and d == _current_device():
             return d
     return -2
 
@@ -92,14 +95,14 @@ def _here(t):
 def _buffer(t, name, dtype, nbytes, device):
     """Pointer of a dense tensor of at least nbytes bytes.  What is as it should be is seen at once; anything else goes to
     the checks that say what is wrong with it (or find that nothing is)."""
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.nbytes >= nbytes and t.get_device() == device and t.is_contiguous():
+    if t.__class__ is _Tensor and t.dtype is dtype and t.get_device() == device and t.nbytes >= nbytes and t.is_contiguous():
         return t.data_ptr()
     return _Operands()(t, name, dtype, nbytes, True)
 
 
 def _view(t, name, kind, shape, strides, nbytes, device):
     """The same for a view of a configuration's shape and strides."""
-    if t.__class__ is torch.Tensor and t.dtype is kind and t.shape == shape and t.stride() == strides and t.get_device() == device:
+    if t.__class__ is _Tensor and t.dtype is kind and t.get_device() == device and t.shape == shape and t.stride() == strides:
         return t.data_ptr()
     return _Operands().view(t, name, kind, shape, strides, nbytes)
 

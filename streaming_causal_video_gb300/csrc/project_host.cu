@@ -1,6 +1,7 @@
 // Host side of the operators in sdv2_project.h: argument checks, derived sizes and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "host_checks.h"
 #include "project.h"
@@ -181,6 +182,37 @@ int rope_pairs(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
     return width;
 }
 
+// The same from the calling thread's last configuration, as most calls have the one of the call before: its pairs depend on
+// nothing else.
+int rope_table(const sdv2_axes_rope_cfg* c, bool backward, AxesRopeParams* p)
+{
+    struct Key {
+        double base, scale[4];
+        int32_t dims[4];
+        int32_t axes, head_dim, dtype, halves, backward, pad;
+    };
+    thread_local Key last{};
+    thread_local RopePair pairs[kRopePairs];
+    thread_local int width = 0;
+    Key key{};
+    key.base = c->base;
+    for (int a = 0; a < c->axes; ++a) key.scale[a] = c->scale[a], key.dims[a] = c->dims[a];
+    key.axes = c->axes;
+    key.head_dim = c->head_dim;
+    key.dtype = c->dtype;
+    key.halves = c->halves;
+    key.backward = backward;
+    const size_t bytes = static_cast<size_t>(c->head_dim / 2) * sizeof(RopePair);
+    if (width == 0 || std::memcmp(&key, &last, sizeof(key)) != 0) {
+        width = rope_pairs(c, backward, p);
+        std::memcpy(pairs, p->pair, bytes);
+        last = key;
+    } else {
+        std::memcpy(p->pair, pairs, bytes);
+    }
+    return width;
+}
+
 sdv2_status rope_call(const sdv2_axes_rope_cfg* c, const int32_t* positions, const void* q, void* q_new, const void* k,
                       void* k_new, bool backward, void* stream)
 {
@@ -209,7 +241,7 @@ sdv2_status rope_call(const sdv2_axes_rope_cfg* c, const int32_t* positions, con
     p.kv_heads = c->kv_heads;
     p.axes = c->axes;
     p.shared = c->shared_positions;
-    const int width = rope_pairs(c, backward, &p);
+    const int width = rope_table(c, backward, &p);
     const bool all = p.pair[c->head_dim / 2 - 1].axis >= 0;
     return launched(launch_axes_rope(p, !c->halves, width, all, c->dtype == SDV2_F32, c->head_dim, static_cast<cudaStream_t>(stream)),
                     "axes rope launch");
