@@ -1,7 +1,7 @@
 // Rotary positions of several axes, forward and backward (the rotation by the negative angle).
 //
 // Every element is read and written once, so that memory bounds this.  A thread owns the same pairs of dims in many heads of a
-// token: it finds their sines and cosines once and then only loads, turns and stores, six heads' loads under way together.  Pairs
+// token: it finds their sines and cosines once and then only loads, turns and stores, six or twelve heads' loads under way together.  Pairs
 // of neighbours lie in one vector of 16 bytes; pairs half a segment apart in two, as wide as every half segment is whole vectors of.
 // An angle in turns is position * scale * base^(-2j/d) / 2pi.  Its frequency is held as a 64-bit fraction of a turn (whole
 // turns of it change nothing), so that the 64-bit product with the position, which wraps around, is the fraction of a turn that
@@ -18,7 +18,9 @@ namespace sdv2 {
 namespace {
 
 constexpr int kThreads = 128;              // of a block, at most: whole rows of items
-constexpr int kBatch = 6;                  // heads whose loads are under way together
+// Heads whose loads are under way together.
+template <int BYTES>
+constexpr int kBatch = BYTES > 4 ? 6 : 12;
 
 __device__ __forceinline__ float2 cos_sin(uint64_t turn)
 {
@@ -76,7 +78,7 @@ __device__ __forceinline__ void narrow(Pack<__nv_bfloat16, N>& p, const float (&
 template <typename T, int N, bool ADJACENT, bool ALL>
 __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_constant__ AxesRopeParams p)
 {
-    constexpr int P = ADJACENT ? N / 2 : N, V = ADJACENT ? 1 : 2;
+    constexpr int P = ADJACENT ? N / 2 : N, V = ADJACENT ? 1 : 2, BATCH = kBatch<N * sizeof(T)>;
     const int place = threadIdx.x / p.items, item = threadIdx.x - place * p.items;
     const int together = blockDim.x / p.items;               // tokens of a block
     const bool second = blockIdx.y >= p.q_parts;
@@ -95,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
     T* const out0 = static_cast<T*>(t.out) + blockIdx.z * t.os.batch_stride + h0 * t.os.head_stride + u0;
     const int32_t* const pos0 = p.positions + (p.shared ? 0 : blockIdx.z * p.tokens * p.axes);
     wait_for_launch_before();
+    launch_dependents();                                     // 4680 x 12 heads 13.4 us without and 11.9 with this, one token 2.4 and 1.7
     for (int64_t n = static_cast<int64_t>(blockIdx.x) * together + place; n < p.tokens; n += static_cast<int64_t>(gridDim.x) * together) {
         int32_t pos[P];
 #pragma unroll
@@ -102,10 +105,10 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
         float2 cs[P];
         const T* in = in0 + n * t.is.token_stride;
         T* out = out0 + n * t.os.token_stride;
-        for (int h = 0; h < heads; h += kBatch) {
-            Pack<T, N> x[kBatch][V];
+        for (int h = 0; h < heads; h += BATCH) {
+            Pack<T, N> x[BATCH][V];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
+            for (int b = 0; b < BATCH; ++b) {
                 const T* from = in + min(b, heads - 1 - h) * t.is.head_stride;
                 x[b][0] = *reinterpret_cast<const Pack<T, N>*>(from);
                 if constexpr (!ADJACENT) x[b][1] = *reinterpret_cast<const Pack<T, N>*>(from + (v0 - u0));
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
                 for (int i = 0; i < P; ++i) cs[i] = cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos[i])) * turn[i]);
             }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
+            for (int b = 0; b < BATCH; ++b) {
                 if (h + b >= heads) break;
                 float y[V][N];
 #pragma unroll
@@ -136,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
                     *reinterpret_cast<Pack<T, N>*>(to + (i ? v0 - u0 : 0)) = w;
                 }
             }
-            in += kBatch * t.is.head_stride;
-            out += kBatch * t.os.head_stride;
+            in += BATCH * t.is.head_stride;
+            out += BATCH * t.os.head_stride;
         }
     }
 }
@@ -145,14 +148,15 @@ __global__ void __launch_bounds__(kThreads) axes_rope_kernel(const __grid_consta
 template <typename T, int N, bool ADJACENT>
 cudaError_t launch(AxesRopeParams& p, bool all, int head_dim, cudaStream_t s)
 {
+    constexpr int BATCH = kBatch<N * sizeof(T)>;
     p.items = head_dim / (ADJACENT ? N : 2 * N);
     const int together = std::max(1, kThreads / p.items);
     const int64_t places = (p.tokens + together - 1) / together;
     // Heads of a thread: all of a tensor's, unless that leaves SMs without work; a part of them costs its sines and cosines again.
     constexpr int64_t kFull = 152 * 12;
     const int heads = std::max(p.heads, p.kv_heads), tensors = p.kv_heads ? 2 : 1;
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((heads + kBatch - 1) / kBatch, kFull / std::max<int64_t>(1, places * p.batch * tensors)));
-    p.per = static_cast<int>((heads + parts - 1) / parts + kBatch - 1) / kBatch * kBatch;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((heads + BATCH - 1) / BATCH, kFull / std::max<int64_t>(1, places * p.batch * tensors)));
+    p.per = static_cast<int>((heads + parts - 1) / parts + BATCH - 1) / BATCH * BATCH;
     p.q_parts = (p.heads + p.per - 1) / p.per;
     const int all_parts = p.q_parts + (p.kv_heads + p.per - 1) / p.per;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(places, INT32_MAX)), static_cast<unsigned>(all_parts), static_cast<unsigned>(p.batch));
