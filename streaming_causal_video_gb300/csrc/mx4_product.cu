@@ -50,7 +50,8 @@ struct Tile {
     static constexpr uint32_t STAGE_PITCH = (STAGE_BYTES + 1023) / 1024 * 1024;
     static constexpr uint32_t OUT_BYTES = 32 * 64;                     // a warp's staging of its rows
     static constexpr uint32_t OUT_OFF = STAGES * STAGE_PITCH;
-    static constexpr uint32_t BAR_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
+    static constexpr uint32_t BIAS_OFF = OUT_OFF + EPI_WARPS * OUT_BYTES;
+    static constexpr uint32_t BAR_OFF = BIAS_OFF + EPI_WARPS * 64 * 4;
     static constexpr uint32_t SMEM_BYTES = BAR_OFF + 256 + 1024;
     // Tensor memory: the sums of two tiles, and behind them the scales of a and of b of a step.  Two tiles of 256 columns do
     // not fit beside the scales: the second begins with the first's last 32.  The epilogue takes the shared columns of a tile
@@ -160,29 +161,37 @@ struct Epilogue {
     static constexpr int PIECE = F32 ? 16 : 32;
     const ProductParams& p;
     uint8_t* stage;                            // 2 KB, swizzled as TMA takes 64-byte rows
+    float* bias;                               // of 64 columns
 
-    __device__ __forceinline__ Epilogue(const ProductParams& p_, uint8_t* stage_) : p(p_), stage(stage_) {}
+    __device__ __forceinline__ Epilogue(const ProductParams& p_, uint8_t* stage_, uint8_t* bias_)
+        : p(p_), stage(stage_), bias(reinterpret_cast<float*>(bias_))
+    {
+    }
 
-    // Columns n to n + PIECE of rows row0 to row0 + 32, of which there is one at least.
-    __device__ __forceinline__ void write(const uint32_t (&y)[PIECE], int row0, int n)
+    // Brings the bias of columns n to n + 64, while their sums are still being formed.
+    __device__ __forceinline__ void begin(int n)
+    {
+        if (!p.bias) return;
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        bias[lane] = n + lane < p.N ? p.bias[n + lane] : 0.0f;
+        bias[32 + lane] = n + 32 + lane < p.N ? p.bias[n + 32 + lane] : 0.0f;
+        __syncwarp();
+    }
+
+    // Columns n to n + PIECE of rows row0 to row0 + 32, of which there is one at least; column n is the c-th from begin's.
+    __device__ __forceinline__ void write(const uint32_t (&y)[PIECE], int row0, int n, int c)
     {
         const int lane = threadIdx.x & 31;
         uint64_t v[PIECE / 2];
 #pragma unroll
         for (int j = 0; j < PIECE / 2; ++j) v[j] = f32x2_pack(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
         if (p.bias) {
-            if (n + PIECE <= p.N) {                              // the same addresses in all lanes
-                const ulonglong2* b = reinterpret_cast<const ulonglong2*>(p.bias + n);
 #pragma unroll
-                for (int j = 0; j < PIECE / 4; ++j) {
-                    const ulonglong2 b4 = b[j];
-                    v[2 * j] = fadd2(v[2 * j], b4.x);
-                    v[2 * j + 1] = fadd2(v[2 * j + 1], b4.y);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < PIECE / 2; ++j)
-                    v[j] = fadd2(v[j], f32x2_pack(n + 2 * j < p.N ? p.bias[n + 2 * j] : 0.0f, n + 2 * j + 1 < p.N ? p.bias[n + 2 * j + 1] : 0.0f));
+            for (int j = 0; j < PIECE / 4; ++j) {
+                const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bias + c + 4 * j);
+                v[2 * j] = fadd2(v[2 * j], b4.x);
+                v[2 * j + 1] = fadd2(v[2 * j + 1], b4.y);
             }
         }
         if (p.gelu) {
@@ -212,9 +221,10 @@ struct Epilogue {
         }
     }
 
+    // The staged bytes have been read.  (The stores themselves end before the kernel does.)
     __device__ __forceinline__ void finish()
     {
-        if ((threadIdx.x & 31) == 0) tma_store_wait();
+        if ((threadIdx.x & 31) == 0) tma_store_wait_read();
         __syncwarp();
     }
 };
@@ -364,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         // Four warps per quarter, 64 columns each; of 192 columns another one has none in each tile.
         const int group = (warp - 2) >> 2, quarter = warp & 3;
         constexpr int PIECE = Epilogue<F32>::PIECE, PIECES = 64 / PIECE;
-        Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES);
+        Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES, smem + T::BIAS_OFF + (warp - 2) * 256);
         const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), leader), shared_leader = map_to_rank(bar(B_SHARED), leader);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int li = 0;
@@ -373,6 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             const int place = T::SHARES ? group : (group + li) & 3;
             const int row0 = t.m0 + rank * CM + quarter * 32, n0 = t.n0 + place * 64;
             const bool mine = (T::SHARES || place < 3) && row0 < p.M && n0 < p.N;
+            if (!SPLIT && mine) out.begin(n0);
             const bool ok = mbar_wait_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 tmem_ld_cols(trow + c, y);
                 if (shared && (i + 1) * PIECE == 32) arrive(shared_leader);
                 if (i == PIECES - 1) arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
-                out.write(y, row0, n0 + c);
+                out.write(y, row0, n0 + c, c);
             }
         }
         if constexpr (!SPLIT) out.finish();
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         cluster_sync_all();
         if (warp >= 2 && sound) {
             constexpr int PIECE = Epilogue<F32>::PIECE;
-            Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES);
+            Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES, smem + T::BIAS_OFF + (warp - 2) * 256);
             const Unit t(p, pair, TN);
             const int row0 = t.m0 + rank * CM + quarter * 32;
             for (int c = group * PIECE; c < width; c += 4 * PIECE) {
@@ -459,7 +470,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                         y[j + 3] = __float_as_uint(__uint_as_float(y[j + 3]) + __uint_as_float(v.w));
                     }
                 }
-                out.write(y, row0, n);
+                out.begin(n);
+                out.write(y, row0, n, 0);
             }
             out.finish();
         }

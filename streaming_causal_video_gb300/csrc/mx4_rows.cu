@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
     wait_for_launch_before();
     launch_dependents();
 
+    const int row = warp * 32 + lane, n = n0 + row;              // of b, of warps 0-3
+    const float bias = warp < 4 && p.bias && n < p.N ? p.bias[n] : 0.0f;
     auto give_up = [&]() {
         *abort_flag = 1;
         atomicOr(p.err, kErrTimeout);
@@ -159,8 +161,6 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
     }
     __syncthreads();
     const bool sound = !*abort_flag;
-    const int row = warp * 32 + lane, n = n0 + row;
-    const float bias = warp < 4 && p.bias && n < p.N ? p.bias[n] : 0.0f;
     auto write = [&](int m, float y) {
         y += bias;
         if (p.gelu) y = gelu(y);
