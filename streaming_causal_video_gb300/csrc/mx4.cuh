@@ -14,6 +14,14 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return d;
 }
 
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float max_size(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The scale's byte of a block whose largest magnitude has the bits `amax` (as fp32): the least e with
 // amax <= 7 * 2^e, plus 127.  With amax = 1.m * 2^(E - 127) that is E - 2, and one more where 1.m > 1.75, which a carry out
 // of the mantissa gives; infinities and NaN (whose bits compare above all others) give 255.

@@ -4,8 +4,9 @@
 // instructions.  A block of 256 threads takes 16 rows, 16 threads a row; a thread has 8 neighbouring columns of a tile of 128 and
 // two or four tiles, all of whose loads are under way together, at addresses that differ by constants.  The 16 rows are 4
 // neighbours and those 32, 64 and 96 behind them, whose scales lie together (64 bytes a tile).
-// Each lets the next launch set itself up at once, whose blocks then take the SMs that it leaves: quantisation and product of
-// 512 x 1536, depth 4096, take 13.8 us without and 13.1 with that, 3 x 9216, depth 1536, 7.1 and 6.5.
+// Quantisation of rows lets the next launch set itself up at once, whose blocks then take the SMs that it leaves: quantisation and
+// product of 512 x 1536, depth 4096, take 13.8 us without and 13.1 with that, 3 x 9216, depth 1536, 7.1 and 6.5.  (The others are
+// slower with it: a transpose of 4680 x 1536 behind another one 5.1 and 6.3.)
 // A row that is not whole vectors of 8 columns is read and written number by number, 16 neighbours at once, by way of shared
 // memory.
 #include <cuda_bf16.h>
@@ -48,8 +49,6 @@ __device__ __forceinline__ float bf16_at(const void* x, int64_t i)
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x)[i]) << 16);
 }
 
-__device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 template <bool F32, bool VECTORS, int kUnroll>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params p, unsigned row_groups)
 {
@@ -62,7 +61,6 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params
     const int64_t c0 = static_cast<int64_t>(at.tile) * kMx4Tile;
     const int64_t first = live ? at.row * p.stride + c0 : 0;
     float x[kUnroll][8];
-    uint32_t top[kUnroll];
     if constexpr (VECTORS) {
         uint4 raw[kUnroll][F32 ? 2 : 1];
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.x) + first * (F32 ? 4 : 2)) + lane * (F32 ? 2 : 1);
@@ -79,22 +77,15 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params
             if constexpr (F32) {
                 const uint4 w = raw[i][1];
                 const uint32_t all[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
-                top[i] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[i][j] = __uint_as_float(all[j]);
-                    top[i] = max(top[i], all[j] & 0x7FFFFFFFu);
-                }
+                for (int j = 0; j < 8; ++j) x[i][j] = __uint_as_float(all[j]);
             } else {
                 const uint32_t all[4] = {v.x, v.y, v.z, v.w};
-                uint32_t two = 0;                        // the largest of the even and of the odd ones
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     x[i][2 * j] = __uint_as_float(all[j] << 16);
                     x[i][2 * j + 1] = __uint_as_float(all[j] & 0xFFFF0000u);
-                    two = __vmaxu2(two, all[j] & 0x7FFF7FFFu);
                 }
-                top[i] = max(two << 16, two & 0xFFFF0000u);
             }
         }
     } else {
@@ -114,19 +105,22 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Mx4Params
 #pragma unroll
             for (int j = 0; j < 8; ++j) mine[j * 16 + lane] = raw[i][j];
             __syncwarp();
-            top[i] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[i][j] = mine[lane * 8 + j];
-                top[i] = max(top[i], size_bits(x[i][j]));
-            }
+            for (int j = 0; j < 8; ++j) x[i][j] = mine[lane * 8 + j];
         }
     }
     uint8_t* codes = p.codes + at.codes(p) + lane * 4;
     uint8_t* scales = p.scales + at.scales(p);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        uint32_t t = top[i];                             // four threads hold a block of 32
+        uint32_t t;                                      // four threads hold a block of 32
+        if constexpr (F32) {                             // (4680 x 5120 16.9 us; with max_size 18.1)
+            t = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(x[i][j]) & 0x7FFFFFFFu);
+        } else {
+            t = __float_as_uint(max_size(max_size(x[i][0], x[i][1], x[i][2]), max_size(x[i][3], x[i][4], x[i][5]), max_size(x[i][6], x[i][7], 0.0f)));
+        }
         t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
         t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
         const uint32_t byte = mx4_scale_byte(t);
@@ -156,7 +150,6 @@ __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx
     __shared__ __align__(16) uint8_t codes[kTRows * kTPitch];
     __shared__ __align__(16) uint8_t scales[kTRows * 4];
     wait_for_launch_before();
-    launch_dependents();
     const int tile = static_cast<int>(blockIdx.x / row_blocks);
     const int64_t r0 = static_cast<int64_t>(blockIdx.x % row_blocks) * kTRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,14 +191,16 @@ __global__ void __launch_bounds__(kTThreads) quantize_transposed_kernel(const Mx
     uint32_t top[2] = {};
     if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            top[0] = max(top[0], x[0][i] & 0x7FFFFFFFu);
-            top[1] = max(top[1], x[1][i] & 0x7FFFFFFFu);
+        for (int h = 0; h < 2; ++h) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) t = max_size(t, __uint_as_float(x[F32 ? h : 0][i]), __uint_as_float(x[F32 ? h : 0][i + 1]));
+            top[h] = __float_as_uint(t);
         }
     } else {
         uint32_t two = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) two = __vmaxu2(two, x[0][i] & 0x7FFF7FFFu);
+        for (int i = 0; i < 32; i += 2) two = __vimax3_u16x2(two, x[0][i] & 0x7FFF7FFFu, x[0][i + 1] & 0x7FFF7FFFu);
         top[0] = two << 16, top[1] = two & 0xFFFF0000u;
     }
 #pragma unroll
@@ -246,7 +241,6 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Mx4Params p,
 {
     __shared__ __align__(16) float staged[VECTORS ? 1 : kRows * kMx4Tile];
     wait_for_launch_before();
-    launch_dependents();
     const Place<kUnroll> at(p, row_groups);
     const int lane = threadIdx.x & 15;
     const bool live = at.row < p.rows;
