@@ -10,8 +10,9 @@
  *   sdv2_cross_attention       the chunk's queries attend to each stream's prompt states.
  * sdv2_layer_norm_backward and sdv2_cross_attention_backward give the gradients of these two, so
  * that what the prompt passes through (adapters, prompt states, norms) can be trained.  The library
- * has no gradient of the chunk attention, of RoPE or of the projections: a loss that has to pass
- * through those needs the caller's own.
+ * has no gradient of the chunk attention, of the append's RoPE or of the fused projection: a loss
+ * that has to pass through those needs the caller's own.  (sdv2_project.h has products in 4 bits and
+ * a rotation, both with gradients.)
  *
  * The conventions of sdv2.h hold: the caller owns all device memory, work is enqueued on the
  * caller's stream, arguments are checked on the host before anything is launched, host arrays are

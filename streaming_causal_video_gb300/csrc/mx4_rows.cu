@@ -4,7 +4,7 @@
 // a launch.  The operands change places: 128 rows of b are the rows of a tcgen05 MMA (kind::mxf4, M = 128), and the rows of a its
 // 16, 32 or 64 columns, so that an MMA takes a fraction of the time that its rows of b take to come.  (Decoding b on the CUDA cores
 // for mma.sync was bound by that: 3 rows at 5120 x 20480 took 30 us.)  A CTA has four stages of 256 columns, 16 KB of b each, and two
-// CTAs fit an SM.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
+// CTAs fit an SM: 3 rows at 5120 x 20480 take 12.6 us (4.4 TB/s), at 9216 x 1536 4.6.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
 // shared memory, and each adds up, in the order of the parts, and writes its share of the rows of a.
 //   warps 0-3: epilogue, thread = row of b: its sums lie in its lane of tensor memory, and a warp's stores of a row of out are
 //   neighbours; warp 4: TMA producer; warp 5: scale copies and MMAs.

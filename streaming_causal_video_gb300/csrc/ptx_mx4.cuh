@@ -1,5 +1,5 @@
-// Inline-PTX spellings for products of microscaled 4-bit matrices by CTA pairs.  Each function is one instruction, issued by
-// an elected lane of a converged warp where its name says so.
+// Inline-PTX spellings for products of microscaled 4-bit matrices by CTA pairs.  Each function is one instruction
+// or one ring stage's block of them, issued by an elected lane of a converged warp where its name says so.
 #pragma once
 #include <cuda.h>
 #include <cstdint>
@@ -25,8 +25,7 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
 
 // One ring stage, 256 columns, issued by one elected lane: the scales of both scale tiles of a and of the two by two of b go from each
 // CTA's shared memory to its own tensor memory (a: 4 columns a tile; b: 8), and four MMAs over the pair add 64 columns each to
-// the sums.  One block of instructions, because what bounds these products is how fast a single thread issues them: with an
-// election, a predicate and descriptors computed for each, a stage took 540 cycles, whatever its MMAs were.
+// the sums.  One block of instructions with one election, as a single thread issues them all.
 //   a, b: descriptors of the codes, a row's 64 columns 32 bytes apart; as, bs: of the scales, tiles 512 bytes apart, b's second
 //   row tile 1024; i0, i1: instruction descriptors for the first and the second half of a scale tile
 __device__ __forceinline__ void mx4_stage_pair_warp(uint32_t sums, uint64_t a, uint64_t b, uint64_t as, uint64_t bs, uint32_t a_scales,

@@ -14,7 +14,8 @@ import torch
 
 from . import _binding as sd
 from . import _block as block
-from .layer import StreamSession
+from . import _project as project
+from .layer import Mx4Matrix, StreamSession
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
@@ -41,7 +42,7 @@ def main():
     ap.add_argument("--peak-gbs", type=float, default=0.0, help="HBM peak (GB/s); default: MEASURED_PEAKS.json or 6800")
     ap.add_argument("--layers", type=int, default=8, help="distinct layer caches cycled (more than L2 in total)")
     ap.add_argument("--only", default="", help="comma-separated subset of: append, attention, rerotate, sink, "
-                    "qkv, cublas, unfused, qkv14b, cross, norm, motion, noise, copies (default: all)")
+                    "qkv, cublas, unfused, qkv14b, cross, norm, mx4, rope, motion, noise, copies (default: all)")
     args = ap.parse_args()
     only = {x.strip() for x in args.only.split(",") if x.strip()}
 
@@ -243,6 +244,35 @@ def main():
                    ms=_time(lambda i: block.layer_norm_backward(cfg_n, y, x[i % n], mean, rstd, dx, wsn, weight=par[0],
                                                              dweight=par[2], dbias=par[3], stream=stream), 60, stream))
             del x
+        # a feed-forward pair of four times the width in 4 bits, and the rotation of q and k outside the cache
+        if want("mx4"):
+            for rows, cols, depth, act in ((ww.nq, 4 * C, C, project.GELU), (ww.nq, C, 4 * C, project.NO_ACTIVATION),
+                                           (ww.chunk_frames, 6 * C, C, project.NO_ACTIVATION)):
+                sets = [(Mx4Matrix(rows, depth, dev), Mx4Matrix(cols, depth, dev), bf(rows, depth), bf(rows, cols)) for _ in range(n)]
+                for a, b, x, _ in sets:
+                    a.load(x, stream=stream)
+                    b.load(bf(cols, depth), stream=stream)
+                cfg_p = project.Mx4ProductConfig.make(rows=rows, cols=cols, depth=depth, activation=act)
+                ws = torch.zeros(project.mx4_workspace_bytes(cfg_p), dtype=torch.uint8, device=dev)
+
+                def multiply(i):
+                    a, b, _, y = sets[i % n]
+                    project.mx4_product(cfg_p, a.codes, a.scales, b.codes, b.scales, y, ws, stream=stream)
+                what = ww.name + " (%d x %d, depth %d%s)" % (rows, cols, depth, ", GELU" if act else "")
+                report("sdv2_mx4_product", what, flops_per_call=2.0 * rows * cols * depth, ms=_time(multiply, 60, stream))
+                report("sdv2_mx4_quantize", ww.name + " (%d x %d bf16)" % (rows, depth), bytes_per_call=rows * depth * (2 + 17 / 32),
+                       ms=_time(lambda i: sets[i % n][0].load(sets[i % n][2], stream=stream), 60, stream))
+                sd.check_device_error(ws, stream)
+                del sets
+        if want("rope"):
+            cfg_r2 = project.AxesRopeConfig.make(batch=1, tokens=ww.nq, heads=ww.heads, kv_heads=ww.heads, head_dim=128,
+                                                 dims=(ww.rope_t, ww.rope_h, ww.rope_w), shared_positions=1)
+            grid = torch.arange(ww.nq, device=dev)
+            pos = torch.stack([grid // ww.hw, grid % ww.hw // ww.grid_w, grid % ww.grid_w], -1).int().contiguous()
+            sets = [[bf(1, ww.nq, ww.heads, 128) for _ in range(4)] for _ in range(n)]
+            report("sdv2_axes_rope", ww.name + " (q and k)", bytes_per_call=4 * ww.nq * C * 2,
+                   ms=_time(lambda i: project.axes_rope(cfg_r2, pos, *sets[i % n], stream=stream), 60, stream))
+            del sets
         torch.cuda.empty_cache()
 
     if not (want("motion") or want("noise")):
