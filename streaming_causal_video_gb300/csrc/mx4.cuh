@@ -84,8 +84,8 @@ __device__ __forceinline__ uint64_t gelu2(uint64_t y)
     y = f32x2_pack(a, b);
     const uint64_t z = mul2(y, ffma2(mul2(y, y), f32x2_pack(k * 0.044715f, k * 0.044715f), f32x2_pack(k, k)));
     f32x2_unpack(z, a, b);
-    a = 1.0f + ex2_approx(a);
-    b = 1.0f + ex2_approx(b);
+    a = fmaxf(1.0f + ex2_approx(a), 1.0f);           // (1 for NaN, which then reaches its own result only)
+    b = fmaxf(1.0f + ex2_approx(b), 1.0f);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
     return mul2(y, mul2(f32x2_pack(r, r), f32x2_pack(b, a)));

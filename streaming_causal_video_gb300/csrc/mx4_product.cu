@@ -13,7 +13,7 @@
 // What bounds a deep product is filling the ring: 35 KB a stage and CTA at the 64 bytes a clock that an SM takes in are 560 cycles,
 // the MMAs of a stage 512, and a stage takes 600.  4680 x 5120 of depth 20480 takes 131 us (7.5 PFLOP/s, 127.5 at four times the
 // rate that bf16 products reach), of depth 5120 40 us.  Shallow ones have the start and the end of tiles as well: 4680 x 6144 of
-// depth 1536 takes 22.0 us to bf16, 23.4 with GELU and 27.8 to fp32; 4680 x 1536 of depth 1536 9.7.
+// depth 1536 takes 22.0 us to bf16, 23.9 with GELU and 27.8 to fp32; 4680 x 1536 of depth 1536 9.7.
 // Where tiles are fewer than pairs, the depth is cut into two or four parts, one for each pair of a larger cluster.  Their sums are
 // exchanged through shared memory when the ring is free, and each pair adds up and writes its share of the columns, in the order of
 // the parts, so that results do not depend on which part ends first.

@@ -259,6 +259,25 @@ def test_a_scale_of_nan_reaches_its_row_and_its_column_only(size):
     within(torch.where(nan, ref.float(), p.out), ref, tol, "out")
 
 
+@pytest.mark.parametrize("size", SHAPES, ids=str)
+def test_a_nan_leaves_its_neighbours_with_an_activation(size):
+    """The activation takes columns two at a time."""
+    for dtype in (FP, BF):
+        p = Product(*size, dtype, gelu=True, seed=7)
+        nan = torch.zeros((p.M, p.N), dtype=torch.bool, device="cuda")
+        for n, value in ((1, math.nan), (p.N // 2, math.nan), (p.N // 2 + 3, math.inf), (p.N - 1, -math.inf)):
+            p.bias[n] = value
+            nan[:, n] = math.isnan(value)
+        p.run()
+        sd.check_device_error(p.ws)
+        assert torch.equal(p.out.isnan(), nan)
+        assert bool((p.out[:, p.N // 2 + 3] == math.inf).all())
+        ref, tol = product_reference(p.a, p.b, torch.where(p.bias.isfinite(), p.bias, torch.zeros_like(p.bias)), True, dtype)
+        sound = p.bias.isfinite()
+        within(p.out[:, sound], ref[:, sound], tol[:, sound], "out")
+        assert bool((p.out[:, p.N - 1].abs() <= 2.0 ** -40).all())
+
+
 def test_extreme_scales():
     """Scales of 2^-127 and 2^126 that cancel: no intermediate leaves the range of 32 bits, in few rows and in tiles."""
     K = 256
