@@ -6,7 +6,8 @@ layer of one denoise step.  Around it, norm_step() normalises a chunk's tokens (
 projections) and cross_step() attends to the layer's prompt states, which set_prompt() names and
 which stay for all chunks and steps until the prompt changes.  project_step() multiplies tokens by
 weights held in 4 bits (Mx4Matrix), and rope_step() turns queries and keys that do not go into the
-cache.  Nothing here computes: it allocates and calls the library.
+cache.  Nothing here computes: it allocates and calls the library.  Steps of one session share its
+buffers and error word: steps, or graphs of them, that run at the same time need sessions of their own.
 """
 import torch
 
@@ -63,9 +64,18 @@ class Mx4Matrix:
         self.scales = torch.empty(project.mx4_scales_bytes(cfg), dtype=torch.uint8, device=device)
         self.configs = {}              # of load and values, which follow from type, stride and direction
 
+    def _first(self, rows):
+        """A matrix of that many rows at the start of this one's memory."""
+        m = object.__new__(Mx4Matrix)
+        cfg = project.Mx4Config.make(rows=rows, cols=self.cols)
+        m.rows, m.cols, m.configs = rows, self.cols, {}
+        m.codes, m.scales = self.codes[:project.mx4_codes_bytes(cfg)], self.scales[:project.mx4_scales_bytes(cfg)]
+        return m
+
     @classmethod
     def of(cls, x, transposed=False, stream=None):
-        """A new matrix loaded from x [rows][cols], or from x [cols][rows]."""
+        """A new matrix loaded from x [rows][cols], or from x [cols][rows].  Its memory is the current stream's, which another
+        `stream` has to follow."""
         if x.dim() != 2:
             raise ValueError("x must have two dimensions, not %d" % x.dim())
         rows, cols = reversed(x.shape) if transposed else x.shape
@@ -111,9 +121,9 @@ class StreamSession:
         self.prompts = [None] * layers
         self.cross_ws = None
         self.norms = {}                # norm_step's configurations, which follow from shapes, types and strides
-        self.products = {}             # project_step's, and the 4-bit forms of its activations by their sizes
-        self.loaded = {}
-        self.product_ws = None
+        self.products = {}             # project_step's
+        self.loaded = {}               # the 4-bit forms of its activations by their sizes, and the memory that those share
+        self.scratch = {}
         self.ropes = {}                # rope_step's
 
     def layer_step(self, layer: int, chunk_index, q, k, v, out=None, lse=None, stream=None):
@@ -187,13 +197,18 @@ class StreamSession:
 
     def quantize_step(self, x, stream=None):
         """x [...][K] (bf16 or fp32, contiguous) in 4 bits, for several products of the same activations.  What it returns is the
-        session's and holds until its next activations of this size."""
+        session's and holds until its next activations of K columns."""
         if x.dim() < 1 or not x.is_contiguous() or not x.numel():
             raise ValueError("x must be contiguous and hold at least one row")
         rows, cols = x.numel() // x.shape[-1], x.shape[-1]
         m = self.loaded.get((rows, cols))
         if m is None:
-            m = self.loaded[rows, cols] = Mx4Matrix(rows, cols, self.ws.device)
+            # Memory for 128 * 2^n rows, so that any number of lengths takes at most four times what the longest does.  It is kept as
+            # long as the session, as graphs may hold it.
+            room = max(128, 1 << (rows - 1).bit_length())
+            if (room, cols) not in self.scratch:
+                self.scratch[room, cols] = Mx4Matrix(room, cols, self.ws.device)
+            m = self.loaded[rows, cols] = self.scratch[room, cols]._first(rows)
         return m.load(x.view(rows, cols), stream=stream)
 
     def project_step(self, weight: Mx4Matrix, x, out, bias=None, activation=project.NO_ACTIVATION, stream=None):
@@ -213,28 +228,31 @@ class StreamSession:
         if cfg is None:
             cfg = self.products[key] = project.Mx4ProductConfig.make(rows=a.rows, cols=weight.rows, depth=a.cols,
                                                                      out_dtype=_KINDS[out.dtype], activation=activation)
-        if self.product_ws is None:            # one serves every product
-            ws = torch.empty(project.mx4_workspace_bytes(cfg), dtype=torch.uint8, device=self.ws.device)
-            project.mx4_workspace_init(cfg, ws, stream)
-            self.product_ws = ws
-        project.mx4_product(cfg, a.codes, a.scales, weight.codes, weight.scales, out.view(a.rows, weight.rows), self.product_ws, bias=bias,
+        # (a product needs the error word alone, which is where the session's workspace has it)
+        project.mx4_product(cfg, a.codes, a.scales, weight.codes, weight.scales, out.view(a.rows, weight.rows), self.ws, bias=bias,
                             stream=stream)
         return out
 
     def chunk_positions(self, chunk_index):
         """int32 [B][Nq][3]: time index, row and column of a chunk's tokens, the places that layer_step turns them by."""
         c = self.cfg
+        if len(chunk_index) != c.batch:
+            raise ValueError("%d chunk indexes for %d streams" % (len(chunk_index), c.batch))
         n = torch.arange(c.nq)
         grid = torch.stack([n // c.hw, n % c.hw // c.grid_w, n % c.grid_w], -1)
         pos = grid.expand(c.batch, c.nq, 3).clone()
         for b, (start, chunk) in enumerate(zip(self.start_frames, chunk_index)):
             pos[b, :, 0] += start + c.chunk_frames * (chunk % c.refresh_chunks if c.refresh_chunks else chunk)
+        if int(pos.max()) >= 1 << 31:
+            raise ValueError("time index %d is past 32 bits" % int(pos.max()))
         return pos.to(device=self.ws.device, dtype=torch.int32)
 
     def rope_step(self, positions, q, q_out, k=None, k_out=None, stream=None):
         """Turns q [B][N][H][D], and k, by their places on the session's three axes: positions int32 [B][N][3], or [N][3] for all of
         the batch.  bf16 or fp32 views with any strides of whole 16 bytes; q_out may be q itself, k_out k."""
         c = self.cfg
+        if (k is None) != (k_out is None):
+            raise ValueError("k and k_out go together")
         if q.dim() != 4 or q.dtype not in _KINDS or q.shape != q_out.shape or (k is not None and (k.dim() != 4 or k.shape != k_out.shape)):
             raise ValueError("q, k and their results must be bf16 or fp32 [B][N][H][D], each of one shape with its result")
         if k is not None and (k.shape[0], k.shape[1], k.shape[3]) != (q.shape[0], q.shape[1], q.shape[3]):

@@ -684,6 +684,39 @@ def test_a_layer_as_a_session_runs_it():
     few = torch.empty(B, C, device="cuda")
     sess.project_step(held["q"], x[:, 0].contiguous(), few)
     within(few, *product_reference(plain(x[:, 0]), plain(weights["q"]), None, False, FP), "one token of each stream")
-    sd.check_device_error(sess.product_ws)
+    sd.check_device_error(sess.ws)
     with pytest.raises(ValueError, match="columns"):
         sess.project_step(held["down"], y, down)
+
+
+def test_a_session_reports_its_products_and_captures_its_first_ones():
+    cfg = sd.StreamConfig.make(batch=1, heads=2, head_dim=128, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=6, grid_w=8,
+                               chunk_frames=2, sink_frames=2, window_frames=4, refresh_chunks=0, qkv_token_stride=0)
+    sess = sd.StreamSession(cfg, 1, [0], "cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w = sd.Mx4Matrix.of(torch.randn(200, 520, generator=g, device="cuda"))
+    x = [torch.randn(rows, 520, generator=g, device="cuda") for rows in (96, 100, 3)]
+    y = [torch.zeros(len(t), 200, device="cuda") for t in x]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for a, b in zip(x, y):
+            sess.project_step(w, a, b)
+    sd.check_device_error(sess.ws)                             # nothing has run
+    want = [sess.project_step(w, a, torch.empty_like(b)) for a, b in zip(x, y)]
+    for t in y:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(y, want))
+    try:
+        sd.set_wait_timeout_ns(20_000_000)
+        sd.debug_drop_kv_tile(1)
+        sess.project_step(w, x[0], y[0])
+        with pytest.raises(sd.SDV2Error):
+            sd.check_device_error(sess.ws)
+    finally:
+        sd.debug_drop_kv_tile(-1)
+        sd.set_wait_timeout_ns(2_000_000_000)
+    assert torch.equal(sess.project_step(w, x[0], y[0]), want[0])
+    sd.check_device_error(sess.ws)

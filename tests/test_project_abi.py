@@ -239,7 +239,7 @@ def session(**over):
                                  chunk_frames=2, sink_frames=1, window_frames=3, refresh_chunks=5, qkv_token_stride=0)
     s.ws = torch.zeros(1, dtype=torch.uint8)
     s.start_frames = [7]
-    s.products, s.loaded, s.ropes, s.product_ws = {}, {}, {}, None
+    s.products, s.loaded, s.scratch, s.ropes = {}, {}, {}, {}
     return s
 
 
@@ -277,6 +277,23 @@ def test_session_and_matrix_refuse_what_does_not_fit():
     q = torch.zeros(1, 12, 2, 128)
     pos = torch.zeros(1, 12, 3, dtype=torch.int32)
     for args in ((pos, q, torch.zeros(1, 12, 2, 64)), (pos, q[..., :64], q[..., :64]), (pos[:, :5], q, q), (pos, q, q, q[:, :5], q[:, :5]),
-                 (pos, q.half(), q.half()), (pos, q, q, q, q[:, :, :1])):
+                 (pos, q.half(), q.half()), (pos, q, q, q, q[:, :, :1]), (pos, q, q, q), (pos, q, q, None, q)):
         with pytest.raises(ValueError):
             s.rope_step(*args)
+    for chunks in ([1, 2], []):
+        with pytest.raises(ValueError, match="chunk indexes"):
+            s.chunk_positions(chunks)
+    s.cfg.refresh_chunks = 0
+    with pytest.raises(ValueError, match="past 32 bits"):
+        s.chunk_positions([1 << 30])
+
+
+def test_activations_of_many_lengths_share_memory():
+    s = session()
+    s.ws = torch.zeros(1, dtype=torch.uint8)
+    for rows in range(1, 700):
+        with pytest.raises(ValueError):                        # there is no GPU to load it on
+            s.quantize_step(torch.zeros(rows, 40))
+        m, whole = s.loaded[rows, 40], sd.Mx4Matrix(rows, 40, "cpu")
+        assert (m.rows, m.cols, m.codes.numel(), m.scales.numel()) == (rows, 40, whole.codes.numel(), whole.scales.numel())
+    assert sorted(s.scratch) == [(n, 40) for n in (128, 256, 512, 1024)]
