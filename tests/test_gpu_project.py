@@ -77,6 +77,32 @@ def test_quantize_and_values(rows, cols, pad, dtype, transposed):
         assert out_pad == 0 or bool(base[:, cols:].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(2500, 1800, 0), (2500, 1800, 8), (2500, 1793, 0), (2500, 1793, 1), (2600, 1922, 0), (2600, 1921, 3),
+                                           (1300, 1150, 0), (1300, 1151, 0), (2500, 1152, 0), (9800, 2, 0), (9800, 1, 0), (9800, 1, 2)])
+def test_rows_enough_for_several_tiles_of_a_thread(rows, cols, pad, dtype):
+    """Rows that begin on even and odd places, whole and cut tiles at the end of a thread's, and results between guard bytes."""
+    g = cpu_gen(rows + cols)
+    x = special(torch.randn(rows, cols, generator=g) * torch.exp(4 * torch.randn(rows, 1, generator=g)), g).to(dtype)
+    view, _ = strided(x, pad)
+    cfg = sd.Mx4Config.make(rows=rows, cols=cols, x_dtype=KIND[dtype], x_row_stride=cols + pad)
+    codes, scales = buffers(cfg)
+    sd.mx4_quantize(cfg, view, codes, scales)
+    code, byte, bad = quantized(x)
+    want_codes, want_scales = packed(code, byte, rows, cols)
+    assert torch.equal(scales.cpu(), want_scales.flatten())
+    sound = torch.nn.functional.pad(~bad.repeat_interleave(32, 1), (0, -bad.shape[1] % 4 * 32), value=True)[:, 0::2]
+    assert torch.equal(codes.cpu().view(rows, -1)[sound], want_codes[sound])
+    ref = values(code, byte)
+    ref[bad.repeat_interleave(32, 1)[:, :cols]] = math.nan
+    ref[ref.abs() >= 2.0 ** 128] *= math.inf
+    base = torch.full((16 + rows * (cols + pad) + 16,), 77.0, dtype=dtype, device="cuda")
+    inner = base[16:-16].view(rows, cols + pad)
+    sd.mx4_dequantize(cfg, codes, scales, inner[:, :cols])
+    assert torch.equal(inner[:, :cols].cpu().double().nan_to_num(nan=12345.0), ref.nan_to_num(nan=12345.0))
+    assert bool((base[:16] == 77).all()) and bool((base[-16:] == 77).all()) and bool((inner[:, cols:] == 77).all())
+
+
 # ---- products ---------------------------------------------------------------------------------------
 
 class Product:
