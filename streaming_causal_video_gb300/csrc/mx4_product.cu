@@ -1,8 +1,8 @@
 // Products of microscaled 4-bit matrices on the tensor cores: out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]).
 //
 // Clusters of two CTAs on the two SMs of a TPC share each MMA (tcgen05.mma.cta_group::2.kind::mxf4, M = 256, N = 256, 64
-// columns a step): a pair tile is 256 rows of a by 256 rows of b; each CTA holds 128 rows of either and gets the sums of its
-// 128 rows of a in its own tensor memory.  A ring stage is 256 columns: 128 bytes of codes of a row, so that the tiles in
+// columns a step): a pair tile is 256 rows of a by 256 (or 192 or 128) rows of b; each CTA holds half of the rows of either and gets
+// the sums of its 128 rows of a in its own tensor memory.  A ring stage is 256 columns: 128 bytes of codes of a row, so that the tiles in
 // shared memory, their swizzle and their descriptors are those of 64 bf16 columns; with the scales 35 KB a CTA.  The scales lie
 // in global memory as the tensor memory takes them and go there by tcgen05.cp, in front of the MMAs that use them: those of a
 // CTA's own 128 rows of a, and those of all 256 rows of b, which both CTAs read.
@@ -10,10 +10,10 @@
 //   the leader arms for both); warp 1: in the leader, scale copies and MMAs, whose commits arrive on the barriers of both CTAs;
 //   warps 2-17: epilogue, four per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 64
 //   bytes of a row at a time go through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
-// What bounds a deep product is filling the ring: 35 KB a stage and CTA at the 64 bytes a clock that an SM takes in are 560 cycles,
-// the MMAs of a stage 512, and a stage takes 600.  4680 x 5120 of depth 20480 takes 131 us (7.5 PFLOP/s, 127.5 at four times the
-// rate that bf16 products reach), of depth 5120 40 us.  Shallow ones have the start and the end of tiles as well: 4680 x 6144 of
-// depth 1536 takes 22.0 us to bf16, 23.9 with GELU and 27.8 to fp32; 4680 x 1536 of depth 1536 9.7.
+// What bounds a deep product is shared memory: the MMAs of a stage of 256 x 256 take 262 ns (512 cycles) and read 32 KB of each CTA's
+// meanwhile, while copies write 35 KB; together they take 288.  4680 x 5120 of depth 20480 takes 127 us (7.7 PFLOP/s; 127.5 at four
+// times the rate that bf16 products reach), of depth 5120 39 us.  Shallow ones have the start and the end of tiles as well: 4680 x
+// 6144 of depth 1536 takes 21.3 us to bf16, 23.4 with GELU and 27.1 to fp32; 4680 x 1536 of depth 1536 8.6.
 // Where tiles are fewer than pairs, the depth is cut into two or four parts, one for each pair of a larger cluster.  Their sums are
 // exchanged through shared memory when the ring is free, and each pair adds up and writes its share of the columns, in the order of
 // the parts, so that results do not depend on which part ends first.
@@ -45,7 +45,7 @@ constexpr int THREADS = 32 * (2 + EPI_WARPS);
 template <int TN>
 struct Tile {
     static constexpr int CN = TN / 2;                                  // rows of b in each CTA
-    static constexpr int STAGES = TN == 256 ? 5 : 6;
+    static constexpr int STAGES = TN == 256 ? 5 : TN == 192 ? 6 : 7;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 2, B_SHARED = 2 * STAGES + 4,
                          B_DONE = 2 * STAGES + 5, NBARS = 2 * STAGES + 6;
     static constexpr uint32_t A_BYTES = CM * 128, B_BYTES = CN * 128;
@@ -62,9 +62,11 @@ struct Tile {
     // first, and the next tile begins when they are free, about 1300 cycles behind the last one's end; tiles of 192 columns
     // follow at once.
     static constexpr bool SHARES = TN == 256;
+    // Columns that a warp of the epilogue takes: of 192 columns, one of the four groups has none in each tile, by turns.
+    static constexpr int GROUP_COLS = TN == 128 ? 32 : 64;
     static constexpr uint32_t COL_SECOND = SHARES ? TN - 32 : TN;
     static constexpr uint32_t COL_AS = COL_SECOND + TN, COL_BS = COL_AS + 4 * STEP_TILES;
-    static_assert(TN == 256 || TN == 192, "rows of b from a multiple of 64 on, in two scale tiles");
+    static_assert(TN == 256 || TN == 192 || TN == 128, "rows of b from a multiple of 64 on, in two scale tiles");
     static_assert(COL_AS + 12 * STEP_TILES <= 512, "tensor memory");
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && OUT_OFF % 1024 == 0, "128-byte swizzle");
     static_assert(NBARS * 8 + 16 <= 256 && SMEM_BYTES <= 232448, "shared memory");
@@ -300,30 +302,33 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     };
     int issued = 0;              // the producer's steps
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t full_leader = map_to_rank(bar(B_FULL), leader);
-            bool ok = true;
-            for (Unit t(p, pair, TN); ok && t.u < units; t.next(p, pairs, TN)) {
-                const int m0 = t.m0 + rank * CM, n0 = t.n0 + rank * T::CN;
-                for (int k = t.first; k < t.last; ++k) {
-                    const int st = issued % STAGES;
-                    if (!mbar_wait_bounded(bar(B_EMPTY + st), (static_cast<uint32_t>(issued / STAGES) & 1u) ^ 1u, tmo, abort_flag)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = s0 + st * T::STAGE_PITCH, fb = full_leader + 8u * static_cast<uint32_t>(st);
-                    if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2 * STAGE_BYTES);
-                    ++issued;
-                    if (k == p.drop) continue;
-                    tma_load_3d_pair(sa, &p.a, fb, k * 128, m0, 0);
-                    tma_load_3d_pair(sa + A_BYTES, &p.b, fb, k * 128, n0, 0);
-                    tma_load_3d_pair(sa + A_BYTES + B_BYTES, &p.as, fb, 0, k * STEP_TILES, m0 / 128);
-                    tma_load_3d_pair(sa + A_BYTES + B_BYTES + AS_BYTES, &p.bs, fb, 0, k * STEP_TILES, t.n0 / 128);
+        const uint32_t full_leader = map_to_rank(bar(B_FULL), leader);
+        int st = 0;                                                  // the ring's stage and its phase
+        uint32_t phase = 1;
+        bool ok = true;
+        for (Unit t(p, pair, TN); ok && t.u < units; t.next(p, pairs, TN)) {
+            const int m0 = t.m0 + rank * CM, n0 = t.n0 + rank * T::CN;
+            for (int k = t.first; k < t.last; ++k) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_EMPTY + st), phase, tmo, abort_flag))) {
+                    if (lane == 0) give_up();
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = s0 + st * T::STAGE_PITCH;
+                if (k != p.drop)
+                    mx4_load_pair_warp(rank == 0, bar(B_FULL + st), 2 * STAGE_BYTES, full_leader + 8u * static_cast<uint32_t>(st), &p.a, &p.b, &p.as, &p.bs,
+                                       sa, sa + A_BYTES, sa + A_BYTES + B_BYTES, sa + A_BYTES + B_BYTES + AS_BYTES, k * 128, m0, n0, k * STEP_TILES,
+                                       m0 / 128, t.n0 / 128);
+                else if (rank == 0 && lane == 0)
+                    mbar_arrive_expect_tx(bar(B_FULL + st), 2 * STAGE_BYTES);
+                ++issued;
+                if (++st == STAGES) {
+                    st = 0;
+                    phase ^= 1u;
                 }
             }
-            if (rank == 1) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_steps)), leader), issued);
         }
+        if (rank == 1 && lane == 0) st_cluster(map_to_rank(smem_u32(const_cast<int*>(peer_steps)), leader), issued);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -375,18 +380,18 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         }
         __syncwarp();
     } else {
-        // Four warps per quarter, 64 columns each; of 192 columns another one has none in each tile.
+        // Four warps per quarter.
         const int group = (warp - 2) >> 2, quarter = warp & 3;
-        constexpr int PIECE = Epilogue<F32>::PIECE, PIECES = 64 / PIECE;
+        constexpr int PIECE = Epilogue<F32>::PIECE, GROUP = T::GROUP_COLS, PIECES = GROUP / PIECE;
         Epilogue<F32> out(p, smem + T::OUT_OFF + (warp - 2) * T::OUT_BYTES, smem + T::BIAS_OFF + (warp - 2) * 256);
         const uint32_t empty_leader = map_to_rank(bar(B_ACC_EMPTY), leader), shared_leader = map_to_rank(bar(B_SHARED), leader);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int li = 0;
         for (Unit t(p, pair, TN); t.u < units; t.next(p, pairs, TN), ++li) {
             const int buf = li & 1;
-            const int place = T::SHARES ? group : (group + li) & 3;
-            const int row0 = t.m0 + rank * CM + quarter * 32, n0 = t.n0 + place * 64;
-            const bool mine = (T::SHARES || place < 3) && row0 < p.M && n0 < p.N;
+            const int place = TN == 192 ? (group + li) & 3 : group;
+            const int row0 = t.m0 + rank * CM + quarter * 32, n0 = t.n0 + place * GROUP;
+            const bool mine = (TN != 192 || place < 3) && row0 < p.M && n0 < p.N;
             if (!SPLIT && mine) out.begin(n0);
             const bool ok = mbar_wait_bounded(bar(B_ACC_FULL + buf), static_cast<uint32_t>(li >> 1) & 1u, tmo, abort_flag) && !*abort_flag;
             if (!__all_sync(0xffffffffu, ok)) {
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                 arrive(empty_leader + 8u * static_cast<uint32_t>(buf));
                 continue;
             }
-            const uint32_t trow = lanes + (buf ? T::COL_SECOND : 0u) + static_cast<uint32_t>(place * 64);
+            const uint32_t trow = lanes + (buf ? T::COL_SECOND : 0u) + static_cast<uint32_t>(place * GROUP);
             const int flip = T::SHARES && buf == 0 ? PIECES - 1 : 0;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
@@ -436,15 +441,16 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         const bool sound = !*abort_flag;
         if (warp >= 2 && sound) {
             const Unit t(p, pair, TN);
-            const int owner = group * 64 / width;
-            if (owner != own && t.m0 + rank * CM + quarter * 32 < p.M && t.n0 + group * 64 < p.N) {
+            constexpr int GROUP = TN / 4;
+            const int owner = group * GROUP / width;
+            if (owner != own && t.m0 + rank * CM + quarter * 32 < p.M && t.n0 + group * GROUP < p.N) {
                 // [part][four columns][row][column]: a warp stores 512 bytes together
                 const uint32_t to = map_to_rank(s0, static_cast<uint32_t>(2 * owner + rank)) +
-                                    static_cast<uint32_t>((own < owner ? own : own - 1) * width + group * 64 % width) * (CM * 4) + my_row;
+                                    static_cast<uint32_t>((own < owner ? own : own - 1) * width + group * GROUP % width) * (CM * 4) + my_row;
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
+                for (int c = 0; c < GROUP; c += 32) {
                     uint32_t y[32];
-                    tmem_ld_x32_sync(lanes + group * 64 + c, y);
+                    tmem_ld_x32_sync(lanes + group * GROUP + c, y);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) st_cluster_v4(to + static_cast<uint32_t>(c + j) * (CM * 4), y[j], y[j + 1], y[j + 2], y[j + 3]);
                 }
@@ -578,10 +584,12 @@ struct Plan {
 };
 
 // Rows of b in a tile, and parts of the depth, by an estimate of the time in nanoseconds: what a step and a tile were measured to
-// take with every pair at work.  Tiles of 192 rows read more for the same work (4680 x 5120, depth 20480: 132.6 us with 256 rows,
-// 171.4 with 192), but their tiles follow one another closer and fill the pairs evenly at other sizes (4680 x 1536, depth 1536: 10.8
-// and 10.0 us).  Where tiles of 256 rows are few, two or four pairs may share the depth of each (the GPU holds 36 clusters of four CTAs
-// and 15 of eight at once), if that saves more than the exchange of their sums from SM to SM costs.
+// take.  Tiles of fewer rows read more for the same work, but have less to wait for and fill the pairs evenly at other sizes; us with
+// 256, 192 and 128 rows: 4680 x 5120 of depth 5120 39.1, 42.1 and 52.5, 4680 x 1536 of depth 1536 9.1, 8.5 and 9.6, 1536 x 1536 of depth
+// 4680 11.6, 10.3 and 9.7.  Where even tiles of 128 rows are few, two or four pairs may share the depth of each (the GPU holds 36
+// clusters of four CTAs and 15 of eight at once), if that saves more than the exchange of their sums from SM to SM, at 25 bytes a
+// nanosecond, and what comes with it cost: 512 x 512 of depth 8192 10.9 us in one part, 10.1 in two and 9.8 in four, 512 x 1536 of
+// depth 4096 7.7 in one and 9.1 in two.
 Plan plan_of(int64_t M, int64_t N, int tiles)
 {
     const int64_t mtiles = (M + TM - 1) / TM;
@@ -594,15 +602,18 @@ Plan plan_of(int64_t M, int64_t N, int tiles)
             best = {tn, splits};
         }
     };
-    for (int tn : {256, 192}) {
-        const int64_t units = mtiles * ((N + tn - 1) / tn);
-        const int64_t waves = (units + kPairs - 1) / kPairs;
-        offer(tn, 1, static_cast<double>(waves) * (tn == 256 ? 315.0 * steps + 1090 : 291.0 * steps + 650));
+    constexpr struct {
+        int tn;
+        double step, tile;
+    } kinds[] = {{256, 290, 1380}, {192, 225, 1000}, {128, 214, 750}};
+    for (const auto& kind : kinds) {
+        const int64_t units = mtiles * ((N + kind.tn - 1) / kind.tn);
+        offer(kind.tn, 1, static_cast<double>((units + kPairs - 1) / kPairs) * (kind.step * steps + kind.tile));
     }
-    const int64_t units = mtiles * ((N + 255) / 256);
-    const double exchange = static_cast<double>(std::min<int64_t>(M, CM) * 256 * 4) / 25;     // of all sums, at 25 bytes a nanosecond
-    if (units <= 36 && steps >= 2) offer(256, 2, 315.0 * ((steps + 1) / 2) + 1090 + 700 + exchange / 2);
-    if (units <= 15 && steps >= 4) offer(256, 4, 315.0 * ((steps + 3) / 4) + 1090 + 700 + exchange * 3 / 4);
+    const int64_t units = mtiles * ((N + 127) / 128);
+    const double exchange = static_cast<double>(std::min<int64_t>(M, CM) * 128 * 4) / 25;     // of all sums
+    if (units <= 36 && steps >= 2) offer(128, 2, 214.0 * ((steps + 1) / 2) + 750 + 1500 + exchange / 2);
+    if (units <= 15 && steps >= 4) offer(128, 4, 214.0 * ((steps + 3) / 4) + 750 + 2200 + exchange * 3 / 4);
     return best;
 }
 
@@ -634,7 +645,8 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     // (a store's last 16 bytes of a row are written whole)
     if ((pitch | q.N * size) % 16 != 0 || pitch > (int64_t(1) << 39) / q.M) p.direct = q.out;
     else if (!out_map(&p.out, q.out, q.out_f32, q.M, q.N, q.out_stride)) return cudaErrorInvalidValue;
-    if (p.splits > 1) return q.out_f32 ? launch<256, true, true>(p, s) : launch<256, false, true>(p, s);
+    if (p.splits > 1) return q.out_f32 ? launch<128, true, true>(p, s) : launch<128, false, true>(p, s);
+    if (plan.tn == 128) return q.out_f32 ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
     if (plan.tn == 256) return q.out_f32 ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
     return q.out_f32 ? launch<192, true, false>(p, s) : launch<192, false, false>(p, s);
 }

@@ -4,7 +4,7 @@
 // a launch.  The operands change places: 128 rows of b are the rows of a tcgen05 MMA (kind::mxf4, M = 128), and the rows of a its
 // 16, 32 or 64 columns, so that an MMA takes a fraction of the time that its rows of b take to come.  (Decoding b on the CUDA cores
 // for mma.sync was bound by that: 3 rows at 5120 x 20480 took 30 us.)  A CTA has four stages of 256 columns, 16 KB of b each, and two
-// CTAs fit an SM: 3 rows at 5120 x 20480 take 12.6 us (4.4 TB/s), at 9216 x 1536 4.6.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
+// CTAs fit an SM: 3 rows at 5120 x 20480 take 12.4 us (4.5 TB/s), at 9216 x 1536 4.3.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
 // shared memory, and each adds up, in the order of the parts, and writes its share of the rows of a.
 //   warps 0-3: epilogue, thread = row of b: its sums lie in its lane of tensor memory, and a warp's stores of a row of out are
 //   neighbours; warp 4: TMA producer; warp 5: scale copies and MMAs.
@@ -105,22 +105,26 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
         atomicOr(p.err, kErrTimeout);
     };
     if (warp == 4) {
-        if (lane == 0) {
-            int issued = 0;
-            for (; issued < steps; ++issued) {
-                const int st = issued % STAGES, k = first + issued;
-                if (!mbar_wait_bounded(bar(B_EMPTY + st), (static_cast<uint32_t>(issued / STAGES) & 1u) ^ 1u, tmo, abort_flag)) {
-                    give_up();
-                    break;
-                }
-                const uint32_t sb = s0 + st * S::BYTES, full = bar(B_FULL + st);
-                mbar_arrive_expect_tx(full, S::BYTES);
-                if (k == p.drop) continue;
-                tma_load_3d(sb, &p.b, full, k * 128, n0, 0);
-                tma_load_3d(sb + B_BYTES, &p.a, full, k * 128, 0, 0);
-                tma_load_3d(sb + B_BYTES + S::A_BYTES, &p.bs, full, 0, k * STEP_TILES, n0 / 128);
-                tma_load_3d(sb + B_BYTES + S::A_BYTES + SCALE_BYTES, &p.as, full, 0, k * STEP_TILES, 0);
+        int issued = 0, st = 0;                                  // steps; the ring's stage and its phase
+        uint32_t phase = 1;
+        for (; issued < steps; ++issued) {
+            const int k = first + issued;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(B_EMPTY + st), phase, tmo, abort_flag))) {
+                if (lane == 0) give_up();
+                break;
             }
+            const uint32_t sb = s0 + st * S::BYTES;
+            if (k != p.drop)
+                mx4_load_warp(bar(B_FULL + st), S::BYTES, &p.b, &p.a, &p.bs, &p.as, sb, sb + B_BYTES, sb + B_BYTES + S::A_BYTES,
+                              sb + B_BYTES + S::A_BYTES + SCALE_BYTES, k * 128, n0, 0, k * STEP_TILES, n0 / 128, 0);
+            else if (lane == 0)
+                mbar_arrive_expect_tx(bar(B_FULL + st), S::BYTES);
+            if (++st == STAGES) {
+                st = 0;
+                phase ^= 1u;
+            }
+        }
+        if (lane == 0) {
             // the last copies land before their memory is used again or left
             volatile int no_abort = 0;
             for (int g = max(0, issued - STAGES); g < issued; ++g)
@@ -161,12 +165,28 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
     }
     __syncthreads();
     const bool sound = !*abort_flag;
-    auto write = [&](int m, float y) {
-        y += bias;
-        if (p.gelu) y = gelu(y);
-        const int64_t o = m * p.out_stride + n;
-        if (p.out_f32) static_cast<float*>(p.out)[o] = y;
-        else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+    // `count` rows of out from m on, of which y has room for all
+    auto write = [&](int m, int count, auto& y) {
+        constexpr int ROOM = sizeof(y) / sizeof(float);
+#pragma unroll
+        for (int j = 0; j < ROOM; ++j) y[j] += bias;
+        if (p.gelu) {
+#pragma unroll
+            for (int j = 0; j < ROOM; ++j) y[j] = gelu(y[j]);
+        }
+        if (n >= p.N) return;
+        const int64_t at = m * p.out_stride + n;
+        if (p.out_f32) {
+            float* const o = static_cast<float*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < ROOM; ++j)
+                if (j < count) o[j * p.out_stride] = y[j];
+        } else {
+            __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < ROOM; ++j)
+                if (j < count) o[j * p.out_stride] = __float2bfloat16_rn(y[j]);
+        }
     };
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     tc_fence_after();
@@ -174,11 +194,12 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
         if (warp < 4 && sound) {
 #pragma unroll 1
             for (int m0 = 0; m0 < p.M; m0 += 16) {
-                uint32_t y[16];
-                tmem_ld_x16_sync(lanes + m0, y);
+                uint32_t sums[16];
+                tmem_ld_x16_sync(lanes + m0, sums);
+                float y[16];
 #pragma unroll
-                for (int m = 0; m < 16; ++m)
-                    if (m0 + m < p.M && n < p.N) write(m0 + m, __uint_as_float(y[m]));
+                for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(sums[j]);
+                write(m0, p.M - m0, y);
             }
         }
     } else {
@@ -201,13 +222,23 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
             }
         }
         cluster_sync_all();
-        if (warp < 4 && sound && n < p.N) {
-            const float* sums = reinterpret_cast<const float*>(smem) + row;
+        if (warp < 4 && sound) {
             const int m0 = part * share, rows = min(share, p.M - m0);
-            for (int j = 0; j < rows; ++j) {
-                float y = sums[j * ROWS];
-                for (int from = 1; from < p.parts; ++from) y += sums[(from * share + j) * ROWS];
-                write(m0 + j, y);
+            constexpr int TOGETHER = 4;
+#pragma unroll 1
+            for (int j0 = 0; j0 < rows; j0 += TOGETHER) {
+                const float* sums = reinterpret_cast<const float*>(smem) + j0 * ROWS + row;
+                const int count = min(rows - j0, TOGETHER);
+                float y[TOGETHER];
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) y[j] = j < count ? sums[j * ROWS] : 0.0f;
+                for (int from = 1; from < p.parts; ++from) {
+                    sums += share * ROWS;
+#pragma unroll
+                    for (int j = 0; j < TOGETHER; ++j)
+                        if (j < count) y[j] += sums[j * ROWS];
+                }
+                write(m0 + j0, count, y);
             }
         }
     }

@@ -43,8 +43,8 @@ struct Mx4Product {
     int64_t drop;                          // fault injection: 256-column step whose copies are left out, or -1
 };
 
-// Rows of a that go to launch_mx4_rows: 64 rows at 1536 x 8960 take 8.0 us there and 77 rows 10.9 in tiles, at 5120 x 20480 17.5 and
-// 21.9 (128 rows); where b is wide and shallow the two meet (64 rows at 9216 x 1536 7.3, 128 rows in tiles 6.9).
+// Rows of a that go to launch_mx4_rows, us there and in tiles: 64 rows at 1536 x 8960 6.9 and 9.6, at 5120 x 20480 15.1 and 21.7, at
+// 5120 x 5120 8.6 and 8.7, at 9216 x 1536 5.9 and 6.7, at 1536 x 1536 4.3 and 4.6; fewer rows are further apart.
 constexpr int kMx4FewRows = 64;
 
 // Few rows of a.

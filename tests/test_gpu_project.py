@@ -144,7 +144,8 @@ FEW = [(1, 1, 1), (1, 128, 128), (2, 33, 129), (3, 9216, 1536), (4, 127, 31), (5
        (7, 300, 9000), (9, 130, 640), (16, 257, 9000), (17, 1000, 1100), (31, 129, 256), (32, 513, 4096), (33, 640, 1280), (64, 300, 7001)]
 TILES = [(65, 1, 1), (70, 7, 32), (256, 256, 256), (128, 128, 128), (129, 255, 257), (100, 130, 1), (255, 257, 64), (257, 256, 127),
          (300, 500, 700), (1001, 777, 1050), (600, 300, 1280), (520, 1536, 1536)]
-DEEP = [(65, 300, 8200), (77, 1536, 8960), (512, 700, 4096), (300, 260, 20480), (256, 250, 7001)]
+DEEP = [(65, 300, 8200), (77, 1536, 8960), (512, 700, 4096), (300, 260, 20480), (256, 250, 7001),
+        (700, 650, 8300)]
 
 
 @pytest.mark.parametrize("out_dtype", [FP, BF], ids=["f32", "bf16"])
@@ -163,6 +164,26 @@ def test_products(size, out_dtype):
         p = Product(*size, out_dtype, bias, gelu, pad, seed=sum(size))
         p.run()
         p.check()
+
+
+@pytest.mark.parametrize("out_dtype", [FP, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(4100, 1600, 600), (4500, 1530, 1300), (4100, 1600, 2900), (4100, 1603, 2900), (9000, 2100, 2100), (260, 40000, 520)],
+                         ids=str)
+def test_products_of_several_tiles_of_a_pair(size, out_dtype):
+    """Tiles of 128, 192 and 256 rows one after the other, whose operands the library quantises."""
+    M, N, K = size
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, b = (torch.randn(n, K, generator=g, device="cuda") for n in (M, N))
+    a4, b4 = sd.Mx4Matrix.of(a), sd.Mx4Matrix.of(b)
+    a, b = a4.values(a).double(), b4.values(b).double()
+    bias = torch.randn(N, generator=g, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for gelu in (False, True):
+        cfg = sd.Mx4ProductConfig.make(rows=M, cols=N, depth=K, out_dtype=KIND[out_dtype], activation=sd.GELU if gelu else sd.NO_ACTIVATION)
+        out = torch.full((M, N), math.nan, dtype=out_dtype, device="cuda")
+        sd.mx4_product(cfg, a4.codes, a4.scales, b4.codes, b4.scales, out, ws, bias=bias)
+        sd.check_device_error(ws)
+        within(out, *product_reference(a, b, bias, gelu, out_dtype), "out")
 
 
 # ---- rotary positions ---------------------------------------------------------------------------------
@@ -242,8 +263,10 @@ def test_rotary_positions_and_their_gradient(case, dtype):
 
 # ---- products: exact sums, NaN, places, graphs, errors ---------------------------------------------
 
-SHAPES = [(3, 200, 2048), (40, 130, 2048), (70, 300, 2048), (90, 260, 9000), (300, 260, 1300), (600, 700, 2048)]
-# few rows in one part and in several, tiles of 192 and of 256 rows, and clusters that share the depth
+SHAPES = [(3, 200, 2048), (40, 130, 2048), (70, 300, 2048), (90, 260, 9000), (300, 260, 1300), (600, 700, 2048), (300, 1030, 8200),
+          (1560, 1530, 700), (2040, 2050, 300), (4100, 1600, 300)]
+# few rows in one part and in several; tiles of 128 rows, their depth shared by four pairs and by two; tiles of 192 and of 256 rows,
+# and several tiles of a pair
 
 
 @pytest.mark.parametrize("size", SHAPES, ids=str)
@@ -390,7 +413,8 @@ def test_rows_from_a_multiple_of_128_are_a_matrix_of_their_own():
     within(out, ref, tol, "part")
 
 
-@pytest.mark.parametrize("size,step", [((3, 200, 2048), 3), ((16, 300, 9000), 30), ((70, 300, 2048), 0), ((90, 260, 9000), 20), ((600, 700, 2048), 7)],
+@pytest.mark.parametrize("size,step", [((3, 200, 2048), 3), ((16, 300, 9000), 30), ((70, 300, 2048), 0), ((90, 260, 9000), 20), ((600, 700, 2048), 7),
+                                       ((300, 1030, 8200), 12), ((1560, 1530, 700), 1), ((2040, 2050, 300), 0), ((4100, 1600, 300), 1)],
                          ids=str)
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(size, step):
     p = Product(*size, BF, seed=4)
