@@ -49,7 +49,8 @@ struct Tile {
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_ACC_FULL = 2 * STAGES, B_ACC_EMPTY = 2 * STAGES + 2, B_SHARED = 2 * STAGES + 4,
                          B_DONE = 2 * STAGES + 5, NBARS = 2 * STAGES + 6;
     static constexpr uint32_t A_BYTES = CM * 128, B_BYTES = CN * 128;
-    static constexpr uint32_t AS_BYTES = STEP_TILES * 512, BS_BYTES = 2 * STEP_TILES * 512;
+    static constexpr int B_ROW_TILES = TN == 128 ? 1 : 2;              // scale tiles that these lie in
+    static constexpr uint32_t AS_BYTES = STEP_TILES * 512, BS_BYTES = B_ROW_TILES * STEP_TILES * 512;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
     static constexpr uint32_t STAGE_PITCH = (STAGE_BYTES + 1023) / 1024 * 1024;
     static constexpr uint32_t OUT_BYTES = 32 * 64;                     // a warp's staging of its rows
@@ -66,7 +67,7 @@ struct Tile {
     static constexpr int GROUP_COLS = TN == 128 ? 32 : 64;
     static constexpr uint32_t COL_SECOND = SHARES ? TN - 32 : TN;
     static constexpr uint32_t COL_AS = COL_SECOND + TN, COL_BS = COL_AS + 4 * STEP_TILES;
-    static_assert(TN == 256 || TN == 192 || TN == 128, "rows of b from a multiple of 64 on, in two scale tiles");
+    static_assert(TN == 256 || TN == 192 || TN == 128, "rows of b from a multiple of 64 on, in two scale tiles, or a scale tile's");
     static_assert(COL_AS + 12 * STEP_TILES <= 512, "tensor memory");
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && OUT_OFF % 1024 == 0, "128-byte swizzle");
     static_assert(NBARS * 8 + 16 <= 256 && SMEM_BYTES <= 232448, "shared memory");
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     __syncthreads();
     cluster_sync_all();          // both CTAs' barriers are initialised before either signals the other's
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;                                     // of all 512 columns the first (what the allocation returns)
     wait_for_launch_before();
     launch_dependents();
 
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
                         break;
                     }
                     tc_fence_after();
-                    mx4_stage_pair_warp(acc, dA + at, dB + at, dAS + at, dBS + at, tmem + COL_AS, tmem + COL_BS, b_scales, idesc_mx4(TM, TN, 0),
+                    mx4_stage_pair_warp<T::B_ROW_TILES>(acc, dA + at, dB + at, dAS + at, dBS + at, tmem + COL_AS, tmem + COL_BS, b_scales, idesc_mx4(TM, TN, 0),
                                         idesc_mx4(TM, TN, 1), k > t.first ? 1u : 0u);
                     mma_commit_pair_warp(bar(B_EMPTY + st), both);
                     at += T::STAGE_PITCH >> 4;
@@ -605,15 +606,15 @@ Plan plan_of(int64_t M, int64_t N, int tiles)
     constexpr struct {
         int tn;
         double step, tile;
-    } kinds[] = {{256, 290, 1380}, {192, 225, 1000}, {128, 214, 750}};
+    } kinds[] = {{256, 290, 1380}, {192, 225, 1000}, {128, 200, 750}};
     for (const auto& kind : kinds) {
         const int64_t units = mtiles * ((N + kind.tn - 1) / kind.tn);
         offer(kind.tn, 1, static_cast<double>((units + kPairs - 1) / kPairs) * (kind.step * steps + kind.tile));
     }
     const int64_t units = mtiles * ((N + 127) / 128);
     const double exchange = static_cast<double>(std::min<int64_t>(M, CM) * 128 * 4) / 25;     // of all sums
-    if (units <= 36 && steps >= 2) offer(128, 2, 214.0 * ((steps + 1) / 2) + 750 + 1500 + exchange / 2);
-    if (units <= 15 && steps >= 4) offer(128, 4, 214.0 * ((steps + 3) / 4) + 750 + 2200 + exchange * 3 / 4);
+    if (units <= 36 && steps >= 2) offer(128, 2, 200.0 * ((steps + 1) / 2) + 750 + 1500 + exchange / 2);
+    if (units <= 15 && steps >= 4) offer(128, 4, 200.0 * ((steps + 3) / 4) + 750 + 2200 + exchange * 3 / 4);
     return best;
 }
 
@@ -639,7 +640,7 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     p.inner = p.m_fastest ? mtiles : ntiles;
     p.units = mtiles * ntiles * p.splits;
     if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, CM) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) ||
-        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, 2))
+        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, plan.tn == 128 ? 1 : 2))
         return cudaErrorInvalidValue;
     const int64_t size = q.out_f32 ? 4 : 2, pitch = q.out_stride * size;
     // (a store's last 16 bytes of a row are written whole)

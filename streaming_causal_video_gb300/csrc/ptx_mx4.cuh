@@ -26,7 +26,7 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr)
 // A ring stage's copies: codes of a and b (columns `k` of rows `ra`, `rb`) and their scales (from scale tile `t` of row tiles `sa`,
 // `sb`) to `to` and the places behind it, counted on the barrier `full` of the pair's leader, which arms its own barrier `mine`
 // for `bytes` before.  One block of instructions with one election, as what bounds small tiles is how fast a thread issues them:
-// with the four copies issued by a thread on its own, a stage takes 290 ns whatever its size, with this 214 at 128 rows of b.
+// with the four copies issued by a thread on its own, a stage takes 290 ns whatever its size, with this 200 at 128 rows of b.
 __device__ __forceinline__ void mx4_load_pair_warp(bool leads, uint32_t mine, uint32_t bytes, uint32_t full, const CUtensorMap* a, const CUtensorMap* b,
                                                    const CUtensorMap* as, const CUtensorMap* bs, uint32_t to_a, uint32_t to_b, uint32_t to_as,
                                                    uint32_t to_bs, int k, int ra, int rb, int t, int sa, int sb)
@@ -64,47 +64,78 @@ __device__ __forceinline__ void mx4_load_warp(uint32_t full, uint32_t bytes, con
         : "memory");
 }
 
-// One ring stage, 256 columns, issued by one elected lane: the scales of both scale tiles of a and of the two by two of b go from each
+// One ring stage, 256 columns, issued by one elected lane: the scales of both scale tiles of a and of b's one or two row tiles go from each
 // CTA's shared memory to its own tensor memory (a: 4 columns a tile; b: 8), and four MMAs over the pair add 64 columns each to
 // the sums.  One block of instructions with one election, as a single thread issues them all.
 //   a, b: descriptors of the codes, a row's 64 columns 32 bytes apart; as, bs: of the scales, tiles 512 bytes apart, b's second
 //   row tile 1024; i0, i1: instruction descriptors for the first and the second half of a scale tile
+template <int ROW_TILES>
 __device__ __forceinline__ void mx4_stage_pair_warp(uint32_t sums, uint64_t a, uint64_t b, uint64_t as, uint64_t bs, uint32_t a_scales,
                                                     uint32_t b_scales, uint32_t b_first, uint32_t i0, uint32_t i1, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        ".reg .b64 x, y;\n\t"
-        ".reg .b32 t, u;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %10, 0;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %3;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %4;\n\t"
-        "add.s32 t, %6, 4;\n\t"
-        "add.s64 x, %4, 64;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
-        "add.s32 t, %5, 4;\n\t"
-        "add.s64 x, %3, 32;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
-        "add.s32 u, %6, 8;\n\t"
-        "add.s64 x, %4, 32;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
-        "add.s32 u, %6, 12;\n\t"
-        "add.s64 x, %4, 96;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %8, [%5], [%7], p;\n\t"
-        "add.s64 x, %1, 2;\n\t"
-        "add.s64 y, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [%5], [%7], 1;\n\t"
-        "add.s64 x, %1, 4;\n\t"
-        "add.s64 y, %2, 4;\n\t"
-        "add.s32 u, %7, 8;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [t], [u], 1;\n\t"
-        "add.s64 x, %1, 6;\n\t"
-        "add.s64 y, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [t], [u], 1;\n\t}" ::"r"(sums),
-        "l"(a), "l"(b), "l"(as), "l"(bs), "r"(a_scales), "r"(b_scales), "r"(b_first), "r"(i0), "r"(i1), "r"(accumulate)
-        : "memory");
+    if constexpr (ROW_TILES == 2) {
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t"
+            ".reg .b64 x, y;\n\t"
+            ".reg .b32 t, u;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %10, 0;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %3;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %4;\n\t"
+            "add.s32 t, %6, 4;\n\t"
+            "add.s64 x, %4, 64;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+            "add.s32 t, %5, 4;\n\t"
+            "add.s64 x, %3, 32;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+            "add.s32 u, %6, 8;\n\t"
+            "add.s64 x, %4, 32;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
+            "add.s32 u, %6, 12;\n\t"
+            "add.s64 x, %4, 96;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %8, [%5], [%7], p;\n\t"
+            "add.s64 x, %1, 2;\n\t"
+            "add.s64 y, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [%5], [%7], 1;\n\t"
+            "add.s64 x, %1, 4;\n\t"
+            "add.s64 y, %2, 4;\n\t"
+            "add.s32 u, %7, 8;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [t], [u], 1;\n\t"
+            "add.s64 x, %1, 6;\n\t"
+            "add.s64 y, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [t], [u], 1;\n\t}" ::"r"(sums),
+            "l"(a), "l"(b), "l"(as), "l"(bs), "r"(a_scales), "r"(b_scales), "r"(b_first), "r"(i0), "r"(i1), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t"
+            ".reg .b64 x, y;\n\t"
+            ".reg .b32 t, u;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %10, 0;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %3;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %4;\n\t"
+            "add.s32 t, %5, 4;\n\t"
+            "add.s64 x, %3, 32;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+            "add.s32 u, %6, 8;\n\t"
+            "add.s64 x, %4, 32;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], x;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %8, [%5], [%7], p;\n\t"
+            "add.s64 x, %1, 2;\n\t"
+            "add.s64 y, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [%5], [%7], 1;\n\t"
+            "add.s64 x, %1, 4;\n\t"
+            "add.s64 y, %2, 4;\n\t"
+            "add.s32 u, %7, 8;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %8, [t], [u], 1;\n\t"
+            "add.s64 x, %1, 6;\n\t"
+            "add.s64 y, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %9, [t], [u], 1;\n\t}" ::"r"(sums),
+            "l"(a), "l"(b), "l"(as), "l"(bs), "r"(a_scales), "r"(b_scales), "r"(b_first), "r"(i0), "r"(i1), "r"(accumulate)
+            : "memory");
+    }
 }
 
 // The same within one CTA, of 128 rows of a and few rows of b, whose scales are one row tile's as well (4 columns a tile).
