@@ -4,7 +4,9 @@ import ctypes
 import torch
 
 from . import _binding as _b
-from ._block import _FP, _TYPE, _U8, _Config, _current_device, _Operands, _stream
+from ._block import _FP, _TYPE, _U8, _Config, _current_device, _Operands, _raw_stream, _stream
+
+_I32 = torch.int32
 
 NO_ACTIVATION, GELU = 0, 1     # sdv2_activation
 
@@ -64,7 +66,7 @@ class AxesRopeConfig(_Config):
         return super().make(axes=len(dims), dims=(_i32 * 4)(*dims), scale=(_f64 * 4)(*scale), base=base, **kw)
 
     def _derive(self):
-        """Type; shape, strides and bytes of q in, q out, k in and k out; bytes of the positions."""
+        """Type; shape, strides and bytes of q in, q out, k in and k out; bytes of the positions; whether there is a k."""
         kind, size = _TYPE.get(self.dtype, (None, 4))
 
         def operand(heads, s):
@@ -77,34 +79,11 @@ class AxesRopeConfig(_Config):
             return (self.batch, self.tokens, heads, self.head_dim), (batch, tok, hd, 1), span
         places = max(self.tokens, 0) * (1 if self.shared_positions else max(self.batch, 0))
         return (kind, operand(self.heads, self.q_in), operand(self.heads, self.q_out), operand(self.kv_heads, self.k_in),
-                operand(self.kv_heads, self.k_out), places * max(self.axes, 0) * 4)
+                operand(self.kv_heads, self.k_out), places * max(self.axes, 0) * 4, self.kv_heads != 0)
 
 
-_Tensor = torch.Tensor
-
-
-def _here(t):
-    """The current device if t is a tensor on it, else a number that is no tensor's device."""
-    if t.__class__ is _Tensor:
-        d = t.get_device()
-        if d >= 0 and d == _current_device():
-            return d
-    return -2
-
-
-def _buffer(t, name, dtype, nbytes, device):
-    """Pointer of a dense tensor of at least nbytes bytes.  What is as it should be is seen at once; anything else goes to
-    the checks that say what is wrong with it (or find that nothing is)."""
-    if t.__class__ is _Tensor and t.dtype is dtype and t.get_device() == device and t.nbytes >= nbytes and t.is_contiguous():
-        return t.data_ptr()
-    return _Operands()(t, name, dtype, nbytes, True)
-
-
-def _view(t, name, kind, shape, strides, nbytes, device):
-    """The same for a view of a configuration's shape and strides."""
-    if t.__class__ is _Tensor and t.dtype is kind and t.get_device() == device and t.shape == shape and t.stride() == strides:
-        return t.data_ptr()
-    return _Operands().view(t, name, kind, shape, strides, nbytes)
+def _stream_on(device, stream):
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 _LIB = None
@@ -148,23 +127,38 @@ def mx4_workspace_init(cfg, ws, stream=None):
               "sdv2_mx4_workspace_init")
 
 
+# The calls below see at once, operand by operand, that all is as it should be, as most of a small call's time on the host goes
+# there.  Anything else goes to the checks of _Operands, which say what is wrong or find that nothing is.
+
+def _matrix(plan, x, name, codes, scales, stream):
+    """Pointers of x or y, codes and scales, and the stream."""
+    nc, ns, (kind, shape, strides, nbytes) = plan
+    try:
+        dev = x.get_device()
+        if (dev >= 0 and dev == _current_device() and x.dtype is kind and x.shape == shape and x.stride() == strides
+                and codes.dtype is _U8 and codes.get_device() == dev and codes.nbytes >= nc and codes.is_contiguous()
+                and scales.dtype is _U8 and scales.get_device() == dev and scales.nbytes >= ns and scales.is_contiguous()):
+            return x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream_on(dev, stream)
+    except AttributeError:             # a pointer in a tensor's place
+        pass
+    op = _Operands()
+    return (op.view(x, name, kind, shape, strides, nbytes), op(codes, "codes", _U8, nc, True), op(scales, "scales", _U8, ns, True),
+            _stream(stream))
+
+
 def mx4_quantize(cfg, x, codes, scales, stream=None):
     """x: [rows][cols] (transposed: [cols][rows]) of cfg.x_dtype; codes, scales: uint8, of mx4_codes_bytes(cfg) and
     mx4_scales_bytes(cfg) bytes."""
-    dev = _here(x)
-    nc, ns, plan = cfg.derived()
-    status = _lib().sdv2_mx4_quantize(cfg, _view(x, "x", *plan, dev), _buffer(codes, "codes", _U8, nc, dev),
-                                      _buffer(scales, "scales", _U8, ns, dev), _stream(stream))
+    px, pc, ps, st = _matrix(cfg.derived(), x, "x", codes, scales, stream)
+    status = _lib().sdv2_mx4_quantize(cfg, px, pc, ps, st)
     if status:
         _b._check(status, "sdv2_mx4_quantize")
 
 
 def mx4_dequantize(cfg, codes, scales, y, stream=None):
     """y: [rows][cols] of cfg.x_dtype, the values that codes and scales stand for."""
-    dev = _here(y)
-    nc, ns, plan = cfg.derived()
-    status = _lib().sdv2_mx4_dequantize(cfg, _buffer(codes, "codes", _U8, nc, dev), _buffer(scales, "scales", _U8, ns, dev),
-                                        _view(y, "y", *plan, dev), _stream(stream))
+    py, pc, ps, st = _matrix(cfg.derived(), y, "y", codes, scales, stream)
+    status = _lib().sdv2_mx4_dequantize(cfg, pc, ps, py, st)
     if status:
         _b._check(status, "sdv2_mx4_dequantize")
 
@@ -172,39 +166,66 @@ def mx4_dequantize(cfg, codes, scales, y, stream=None):
 def mx4_product(cfg, a_codes, a_scales, b_codes, b_scales, out, ws, bias=None, stream=None):
     """out [rows][cols] = act(a b^T + bias) of matrices that mx4_quantize wrote: a of `rows` and b of `cols` rows, both of
     `depth` columns; bias: fp32 [cols]; ws: mx4_workspace_bytes(cfg) bytes."""
-    dev = _here(out)
-    ac, asc, bc, bsc, nb, nw, plan = cfg.derived()
-    status = _lib().sdv2_mx4_product(cfg, _buffer(a_codes, "a_codes", _U8, ac, dev), _buffer(a_scales, "a_scales", _U8, asc, dev),
-                                     _buffer(b_codes, "b_codes", _U8, bc, dev), _buffer(b_scales, "b_scales", _U8, bsc, dev),
-                                     None if bias is None else _buffer(bias, "bias", _FP, nb, dev), _view(out, "out", *plan, dev),
-                                     _buffer(ws, "ws", _U8, nw, dev), _stream(stream))
+    nac, nas, nbc, nbs, nb, nw, (kind, shape, strides, nbytes) = cfg.derived()
+    args = None
+    try:
+        dev = out.get_device()
+        if (dev >= 0 and dev == _current_device() and out.dtype is kind and out.shape == shape and out.stride() == strides
+                and a_codes.dtype is _U8 and a_codes.get_device() == dev and a_codes.nbytes >= nac and a_codes.is_contiguous()
+                and a_scales.dtype is _U8 and a_scales.get_device() == dev and a_scales.nbytes >= nas and a_scales.is_contiguous()
+                and b_codes.dtype is _U8 and b_codes.get_device() == dev and b_codes.nbytes >= nbc and b_codes.is_contiguous()
+                and b_scales.dtype is _U8 and b_scales.get_device() == dev and b_scales.nbytes >= nbs and b_scales.is_contiguous()
+                and ws.dtype is _U8 and ws.get_device() == dev and ws.nbytes >= nw and ws.is_contiguous()
+                and (bias is None or bias.dtype is _FP and bias.get_device() == dev and bias.nbytes >= nb and bias.is_contiguous())):
+            args = (a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+                    None if bias is None else bias.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream_on(dev, stream))
+    except AttributeError:
+        pass
+    if args is None:
+        op = _Operands()
+        args = (op(a_codes, "a_codes", _U8, nac, True), op(a_scales, "a_scales", _U8, nas, True), op(b_codes, "b_codes", _U8, nbc, True),
+                op(b_scales, "b_scales", _U8, nbs, True), op(bias, "bias", _FP, nb, True),
+                op.view(out, "out", kind, shape, strides, nbytes), op(ws, "ws", _U8, nw, True), _stream(stream))
+    status = _lib().sdv2_mx4_product(cfg, *args)
     if status:
         _b._check(status, "sdv2_mx4_product")
 
 
-def _turn(cfg, positions, q, q_new, k, k_new, backward, stream):
-    dev = _here(q)
-    kind, q_in, q_out, k_in, k_out, np = cfg.derived()
-    if backward:
-        q_in, q_out, k_in, k_out = q_out, q_in, k_out, k_in
-        names, call = ("dq_out", "dq", "dk_out", "dk"), _lib().sdv2_axes_rope_backward
-    else:
-        names, call = ("q", "q_out", "k", "k_out"), _lib().sdv2_axes_rope
-    pk = pk_new = None
-    if cfg.kv_heads:
-        pk, pk_new = _view(k, names[2], kind, *k_in, dev), _view(k_new, names[3], kind, *k_out, dev)
-    status = call(cfg, _buffer(positions, "positions", torch.int32, np, dev), _view(q, names[0], kind, *q_in, dev),
-                  _view(q_new, names[1], kind, *q_out, dev), pk, pk_new, _stream(stream))
-    if status:
-        _b._check(status, "sdv2_axes_rope_backward" if backward else "sdv2_axes_rope")
+_FORWARD, _BACKWARD = ("q", "q_out", "k", "k_out"), ("dq_out", "dq", "dk_out", "dk")
+
+
+def _turn(plan, names, positions, q, q_new, k, k_new, stream):
+    """Pointers of the positions, of q and its result and of k and its result (None without a k), and the stream."""
+    kind, (qs, qt, qn), (rs, rt, rn), (ks, kt, kn), (ls, lt, ln), np, with_k = plan
+    try:
+        dev = q.get_device()
+        if (dev >= 0 and dev == _current_device() and positions.dtype is _I32 and positions.get_device() == dev and positions.nbytes >= np
+                and positions.is_contiguous() and q.dtype is kind and q.shape == qs and q.stride() == qt
+                and q_new.dtype is kind and q_new.get_device() == dev and q_new.shape == rs and q_new.stride() == rt
+                and (not with_k or k.dtype is kind and k.get_device() == dev and k.shape == ks and k.stride() == kt
+                     and k_new.dtype is kind and k_new.get_device() == dev and k_new.shape == ls and k_new.stride() == lt)):
+            return (positions.data_ptr(), q.data_ptr(), q_new.data_ptr(), k.data_ptr() if with_k else None,
+                    k_new.data_ptr() if with_k else None, _stream_on(dev, stream))
+    except AttributeError:
+        pass
+    op = _Operands()
+    return (op(positions, "positions", _I32, np, True), op.view(q, names[0], kind, qs, qt, qn), op.view(q_new, names[1], kind, rs, rt, rn),
+            op.view(k, names[2], kind, ks, kt, kn) if with_k else None, op.view(k_new, names[3], kind, ls, lt, ln) if with_k else None,
+            _stream(stream))
 
 
 def axes_rope(cfg, positions, q, q_out, k=None, k_out=None, stream=None):
     """q, q_out: [batch][tokens][heads][head_dim], k, k_out: [batch][tokens][kv_heads][head_dim] with cfg's strides;
     positions: int32 [batch][tokens][axes], or [tokens][axes] shared by the batch."""
-    _turn(cfg, positions, q, q_out, k, k_out, False, stream)
+    status = _lib().sdv2_axes_rope(cfg, *_turn(cfg.derived(), _FORWARD, positions, q, q_out, k, k_out, stream))
+    if status:
+        _b._check(status, "sdv2_axes_rope")
 
 
 def axes_rope_backward(cfg, positions, dq_out, dq, dk_out=None, dk=None, stream=None):
     """Gradients dq (cfg.q_in's strides) and dk (cfg.k_in's) from those of axes_rope's results."""
-    _turn(cfg, positions, dq_out, dq, dk_out, dk, True, stream)
+    kind, q_in, q_out, k_in, k_out, nbytes, with_k = cfg.derived()
+    status = _lib().sdv2_axes_rope_backward(cfg, *_turn((kind, q_out, q_in, k_out, k_in, nbytes, with_k), _BACKWARD, positions, dq_out, dq,
+                                                        dk_out, dk, stream))
+    if status:
+        _b._check(status, "sdv2_axes_rope_backward")
