@@ -400,6 +400,19 @@ def test_calls_write_only_their_outputs(size):
         assert not ws.any()
 
 
+@pytest.mark.parametrize("size", [(20, 300), (300, 520), (700, 8300)], ids=str)
+def test_a_matrix_with_itself(size):
+    """Both operands may be the same matrix."""
+    M, K = size
+    a = sd.Mx4Matrix.of(torch.randn(M, K, generator=cpu_gen(M)).cuda())
+    v = a.values(torch.empty(M, K, device="cuda")).double()
+    cfg = sd.Mx4ProductConfig.make(rows=M, cols=M, depth=K, out_dtype=sd.F32)
+    ws, out = torch.zeros(256, dtype=torch.uint8, device="cuda"), torch.empty(M, M, device="cuda")
+    sd.mx4_product(cfg, a.codes, a.scales, a.codes, a.scales, out, ws)
+    sd.check_device_error(ws)
+    within(out, *product_reference(v, v, None, False, FP), "out")
+
+
 def test_rows_from_a_multiple_of_128_are_a_matrix_of_their_own():
     """One projection's part of a packed weight, and the tokens of one stream of a batch."""
     K, N, first, count = 300, 700, 256, 333
@@ -657,6 +670,19 @@ def test_gradient_of_the_rotation_against_differences():
         # each of the three rotations is off by at most 2^-21 + 2^-23 of both dims of a pair
         slack = 3 * 2.0 ** -20 * float((x.abs() + bump.abs()).double().sum(-1).mul(dy.abs().double().sum(-1)).sum())
         assert abs(step - got) <= slack
+
+
+@pytest.mark.parametrize("B,H,Hk", [(65535, 1, 1), (1, 65535, 65535), (1, 65535, 0)])
+def test_rotation_of_the_most_streams_and_heads(B, H, Hk):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k = (torch.randn(B, 1, n, 8, generator=g, device="cuda").bfloat16() for n in (H, max(Hk, 1)))
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (B, 1, 1), generator=g, device="cuda", dtype=torch.int64).int()
+    cfg = sd.AxesRopeConfig.make(batch=B, tokens=1, heads=H, kv_heads=Hk, head_dim=8, dims=(6,))
+    new = [torch.full_like(t, math.nan) for t in (q, k)]
+    sd.axes_rope(cfg, pos, q, new[0], k, new[1])
+    for x, y in list(zip((q, k), new))[:2 if Hk else 1]:
+        within(y, *rope_reference(x, pos, (6,), 10000.0, (), False), "rotated")
+    assert Hk or bool(new[1].isnan().all())
 
 
 def test_rotation_beyond_2_to_the_31_elements():
