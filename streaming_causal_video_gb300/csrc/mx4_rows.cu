@@ -4,8 +4,9 @@
 // a launch.  The operands change places: 128 rows of b are the rows of a tcgen05 MMA (kind::mxf4, M = 128), and the rows of a its
 // 16, 32 or 64 columns, so that an MMA takes a fraction of the time that its rows of b take to come.  (Decoding b on the CUDA cores
 // for mma.sync was bound by that: 3 rows at 5120 x 20480 took 30 us.)  A CTA has four stages of 256 columns, 16 KB of b each, and two
-// CTAs fit an SM: 3 rows at 5120 x 20480 take 12.4 us (4.5 TB/s), at 9216 x 1536 4.3.  Where rows of b are few, up to eight CTAs of a cluster share the depth; their sums change hands through
-// shared memory, and each adds up, in the order of the parts, and writes its share of the rows of a.
+// CTAs fit an SM: 3 rows at 5120 x 20480 take 12.3 us (4.5 TB/s), at 9216 x 1536 4.3.  Where rows of b are few, up to eight CTAs of a
+// cluster share the depth; their sums change hands through shared memory, and each adds up, in the order of the parts, and writes
+// its share of the rows of a.
 //   warps 0-3: epilogue, thread = row of b: its sums lie in its lane of tensor memory, and a warp's stores of a row of out are
 //   neighbours; warp 4: TMA producer; warp 5: scale copies and MMAs.
 #include <cuda_bf16.h>
@@ -269,10 +270,11 @@ cudaError_t launch(const Mx4Product& q, cudaStream_t s)
     p.out_f32 = q.out_f32;
     p.gelu = q.gelu;
     const int64_t clusters = (q.N + ROWS - 1) / ROWS;
-    // Parts of the depth for as many CTAs as the GPU holds (two an SM), of four steps at least: 3 rows at 5120 x 20480 take 25.0 us
-    // in one part and 13.1 in four, at 9216 x 1536 (six steps) 4.5 us in one and 5.3 in four.
+    // Parts of the depth for as many CTAs as the GPU holds (two an SM), of two steps at least, where that saves more steps than the
+    // exchange costs: 3 rows at 5120 x 20480 take 23.4 us in one part and 12.3 in four, at 512 x 4096 (16 steps) 4.2 in one, 3.9 in
+    // two, 3.4 in four and 3.2 in eight, at 1536 x 1536 (six) 2.9 in one and 3.3 in two.
     p.parts = 1;
-    while (p.parts < kMaxParts && clusters * p.parts * 2 <= 304 && p.steps >= 8 * p.parts) p.parts *= 2;
+    while (p.parts < kMaxParts && clusters * p.parts * 2 <= 304 && p.steps >= std::max(12, 4 * p.parts)) p.parts *= 2;
     constexpr int kBytes = static_cast<int>(Stage<COLS>::SMEM_BYTES);
     static PerDevice once;
     int dev = 0;
