@@ -9,10 +9,12 @@
 //   warp 0: TMA producer (both CTAs load into their own shared memory and count the bytes on the leader's stage barrier, which
 //   the leader arms for both); warp 1: in the leader, scale copies and MMAs, whose commits arrive on the barriers of both CTAs;
 //   warps 2-17: epilogue, four per quarter of the tensor memory's lanes, thread = row of a, while the next tile's MMAs run; 64
-//   bytes of a row at a time go through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not whole 16 bytes.
-// What bounds a deep product is shared memory: the MMAs of a stage of 256 x 256 take 262 ns (512 cycles) and read 32 KB of each CTA's
-// meanwhile, while copies write 35 KB; together they take 288.  4680 x 5120 of depth 20480 takes 127 us (7.7 PFLOP/s; 127.5 at four
-// times the rate that bf16 products reach), of depth 5120 39 us.  Shallow ones have the start and the end of tiles as well: 4680 x
+//   bytes of a row at a time go through swizzled shared memory to a TMA store, or to coalesced stores where rows of out are not
+//   whole 16 bytes.
+// What bounds a deep product is the ring: a stage's memory comes round again after 1.4 us, its MMAs and the way of its next copies, so
+// that five stages of 256 x 256 give one in 288 ns (four 340, six 280), where the MMAs take 262 (512 cycles) and shared memory, which
+// they read while copies write it, little less.  4680 x 5120 of depth 20480 takes 127 us (7.7 PFLOP/s; 127.5 at four times the rate
+// that bf16 products reach), of depth 5120 39 us.  Shallow ones have the start and the end of tiles as well: 4680 x
 // 6144 of depth 1536 takes 21.3 us to bf16, 23.4 with GELU and 27.1 to fp32; 4680 x 1536 of depth 1536 8.6.
 // Where tiles are fewer than pairs, the depth is cut into two or four parts, one for each pair of a larger cluster.  Their sums are
 // exchanged through shared memory when the ring is free, and each pair adds up and writes its share of the columns, in the order of
