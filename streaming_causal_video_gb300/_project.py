@@ -163,11 +163,9 @@ def mx4_dequantize(cfg, codes, scales, y, stream=None):
         _b._check(status, "sdv2_mx4_dequantize")
 
 
-def mx4_product(cfg, a_codes, a_scales, b_codes, b_scales, out, ws, bias=None, stream=None):
-    """out [rows][cols] = act(a b^T + bias) of matrices that mx4_quantize wrote: a of `rows` and b of `cols` rows, both of
-    `depth` columns; bias: fp32 [cols]; ws: mx4_workspace_bytes(cfg) bytes."""
-    nac, nas, nbc, nbs, nb, nw, (kind, shape, strides, nbytes) = cfg.derived()
-    args = None
+def _product(plan, a_codes, a_scales, b_codes, b_scales, out, ws, bias, stream):
+    """Pointers of a product's operands, its result and its workspace, and the stream."""
+    nac, nas, nbc, nbs, nb, nw, (kind, shape, strides, nbytes) = plan
     try:
         dev = out.get_device()
         if (dev >= 0 and dev == _current_device() and out.dtype is kind and out.shape == shape and out.stride() == strides
@@ -177,16 +175,27 @@ def mx4_product(cfg, a_codes, a_scales, b_codes, b_scales, out, ws, bias=None, s
                 and b_scales.dtype is _U8 and b_scales.get_device() == dev and b_scales.nbytes >= nbs and b_scales.is_contiguous()
                 and ws.dtype is _U8 and ws.get_device() == dev and ws.nbytes >= nw and ws.is_contiguous()
                 and (bias is None or bias.dtype is _FP and bias.get_device() == dev and bias.nbytes >= nb and bias.is_contiguous())):
-            args = (a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
+            return (a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
                     None if bias is None else bias.data_ptr(), out.data_ptr(), ws.data_ptr(), _stream_on(dev, stream))
     except AttributeError:
         pass
-    if args is None:
-        op = _Operands()
-        args = (op(a_codes, "a_codes", _U8, nac, True), op(a_scales, "a_scales", _U8, nas, True), op(b_codes, "b_codes", _U8, nbc, True),
-                op(b_scales, "b_scales", _U8, nbs, True), op(bias, "bias", _FP, nb, True),
-                op.view(out, "out", kind, shape, strides, nbytes), op(ws, "ws", _U8, nw, True), _stream(stream))
-    status = _lib().sdv2_mx4_product(cfg, *args)
+    op = _Operands()
+    return (op(a_codes, "a_codes", _U8, nac, True), op(a_scales, "a_scales", _U8, nas, True), op(b_codes, "b_codes", _U8, nbc, True),
+            op(b_scales, "b_scales", _U8, nbs, True), op(bias, "bias", _FP, nb, True),
+            op.view(out, "out", kind, shape, strides, nbytes), op(ws, "ws", _U8, nw, True), _stream(stream))
+
+
+def mx4_product(cfg, a_codes, a_scales, b_codes, b_scales, out, ws, bias=None, stream=None):
+    """out [rows][cols] = act(a b^T + bias) of matrices that mx4_quantize wrote: a of `rows` and b of `cols` rows, both of
+    `depth` columns; bias: fp32 [cols]; ws: mx4_workspace_bytes(cfg) bytes."""
+    status = _lib().sdv2_mx4_product(cfg, *_product(cfg.derived(), a_codes, a_scales, b_codes, b_scales, out, ws, bias, stream))
+    if status:
+        _b._check(status, "sdv2_mx4_product")
+
+
+def _multiply(cfg, operands):
+    """The product of operands that _product has seen, between which and this the caller may have quantised a."""
+    status = _lib().sdv2_mx4_product(cfg, *operands)
     if status:
         _b._check(status, "sdv2_mx4_product")
 

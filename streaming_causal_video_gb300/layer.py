@@ -198,27 +198,34 @@ class StreamSession:
     def quantize_step(self, x, stream=None):
         """x [...][K] (bf16 or fp32, contiguous) in 4 bits, for several products of the same activations.  What it returns is the
         session's and holds until its next activations of K columns."""
+        return self._activations(x).load(x.view(-1, x.shape[-1]), stream=stream)
+
+    def _activations(self, x):
+        """The session's matrix for activations of x's size, whatever it holds."""
         if x.dim() < 1 or not x.is_contiguous() or not x.numel():
             raise ValueError("x must be contiguous and hold at least one row")
         rows, cols = x.numel() // x.shape[-1], x.shape[-1]
         m = self.loaded.get((rows, cols))
         if m is None:
-            # Memory for 128 * 2^n rows, so that any number of lengths takes at most four times what the longest does.  It is kept as
-            # long as the session, as graphs may hold it.
+            # Memory for 128 * 2^n rows, so that any number of lengths takes at most four times what the longest does, or 128 rows
+            # where that is shorter.  It is kept as long as the session, as graphs may hold it.
             room = max(128, 1 << (rows - 1).bit_length())
             if (room, cols) not in self.scratch:
                 self.scratch[room, cols] = Mx4Matrix(room, cols, self.ws.device)
             m = self.loaded[rows, cols] = self.scratch[room, cols]._first(rows)
-        return m.load(x.view(rows, cols), stream=stream)
+        return m
 
     def project_step(self, weight: Mx4Matrix, x, out, bias=None, activation=project.NO_ACTIVATION, stream=None):
         """out [...][N] = act(x w^T + bias) for a weight [N][K] in 4 bits; x: [...][K], bf16 or fp32, or what quantize_step made of
-        it; out: contiguous, bf16 or fp32; bias: fp32 [N]; activation: NO_ACTIVATION or GELU."""
+        it; out: contiguous, bf16 or fp32; bias: fp32 [N]; activation: NO_ACTIVATION or GELU.  A call that is refused has quantised
+        nothing, so that what quantize_step returned before still holds."""
         if out.dtype not in _KINDS or out.dim() < 1 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 or fp32")
-        a = x if isinstance(x, Mx4Matrix) else self.quantize_step(x, stream)
-        if a.cols != weight.cols:
-            raise ValueError("x has %d columns, the weight %d" % (a.cols, weight.cols))
+        loaded = isinstance(x, Mx4Matrix)
+        cols = x.cols if loaded else x.shape[-1] if x.dim() else 0
+        if cols != weight.cols:
+            raise ValueError("x has %d columns, the weight %d" % (cols, weight.cols))
+        a = x if loaded else self._activations(x)
         if out.shape[-1] != weight.rows or out.numel() != a.rows * weight.rows:
             raise ValueError("out is %s, not %d rows of %d" % (tuple(out.shape), a.rows, weight.rows))
         if bias is not None and bias.numel() != weight.rows:
@@ -226,11 +233,18 @@ class StreamSession:
         key = (a.rows, weight.rows, a.cols, out.dtype, activation)
         cfg = self.products.get(key)
         if cfg is None:
+            if activation not in (project.NO_ACTIVATION, project.GELU):
+                raise ValueError("activation must be NO_ACTIVATION or GELU, not %r" % (activation,))
             cfg = self.products[key] = project.Mx4ProductConfig.make(rows=a.rows, cols=weight.rows, depth=a.cols,
                                                                      out_dtype=_KINDS[out.dtype], activation=activation)
         # (a product needs the error word alone, which is where the session's workspace has it)
-        project.mx4_product(cfg, a.codes, a.scales, weight.codes, weight.scales, out.view(a.rows, weight.rows), self.ws, bias=bias,
-                            stream=stream)
+        operands = project._product(cfg.derived(), a.codes, a.scales, weight.codes, weight.scales, out.view(a.rows, weight.rows), self.ws,
+                                    bias, stream)
+        if not loaded:
+            if (operands[2] | operands[3] | (operands[4] or 0) | operands[5]) & 15:
+                raise ValueError("the weight, bias and out must begin on 16 bytes")
+            a.load(x.view(a.rows, cols), stream=stream)
+        project._multiply(cfg, operands)
         return out
 
     def chunk_positions(self, chunk_index):

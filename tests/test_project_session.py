@@ -1,0 +1,70 @@
+"""CPU tests of what a session does around its 4-bit products and rotations: what it checks before it computes.  Nothing is
+computed here: there is no GPU."""
+import pytest
+import torch
+
+import streaming_causal_video_gb300 as sd
+from streaming_causal_video_gb300 import _project
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build_library()
+
+
+def session(**over):
+    """A session's shape without its buffers."""
+    s = object.__new__(sd.StreamSession)
+    d = dict(batch=1, heads=2, head_dim=128, rope_t=44, rope_h=42, rope_w=42, rope_base=1e4, grid_h=2, grid_w=3, chunk_frames=2,
+             sink_frames=1, window_frames=3, refresh_chunks=5, qkv_token_stride=0)
+    d.update(over)
+    s.cfg = sd.StreamConfig.make(**d)
+    s.ws = torch.zeros(256, dtype=torch.uint8)
+    s.start_frames = [7] * s.cfg.batch
+    s.products, s.loaded, s.scratch, s.ropes = {}, {}, {}, {}
+    s.prompts, s.cross_ws = [None], None
+    return s
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    """Records quantisations and products instead of calling the library, behind the binding's checks of the bias."""
+    done = []
+
+    def operands(plan, a_codes, a_scales, b_codes, b_scales, out, ws, bias, stream):
+        if bias is not None and (bias.dtype is not torch.float32 or not bias.is_contiguous()):
+            raise ValueError("bias")
+        return (a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), None if bias is None else bias.data_ptr(),
+                out.data_ptr(), ws.data_ptr(), 0)
+    monkeypatch.setattr(sd.Mx4Matrix, "load", lambda self, x, transposed=False, stream=None: done.append(("load", self.codes.data_ptr())) or self)
+    monkeypatch.setattr(_project, "_product", operands, raising=False)
+    monkeypatch.setattr(_project, "_multiply", lambda cfg, args: done.append(("multiply", args[0])), raising=False)
+    return done
+
+
+def test_a_refused_product_has_quantised_nothing(steps):
+    """What quantize_step returned is the session's memory for all activations of its columns: a call that ends in an error may not
+    have overwritten it."""
+    s = session()
+    w = sd.Mx4Matrix(24, 40, "cpu")
+    kept = s.quantize_step(torch.zeros(5, 40))
+    assert steps == [("load", kept.codes.data_ptr())]
+    del steps[:]
+    x, out = torch.zeros(6, 40), torch.zeros(6, 24)
+    odd = torch.zeros(6 * 24 + 1)[1:].view(6, 24)
+    long = torch.zeros(25)
+    for args, kw in (((w, torch.zeros(6, 41), out), {}), ((w, torch.tensor(1.0), out), {}), ((w, x, torch.zeros(6, 25)), {}),
+                     ((w, x, torch.zeros(5, 24)), {}), ((w, x, torch.zeros(24, 6).t()), {}), ((w, x, out.half()), {}), ((w, x, odd), {}),
+                     ((w, x, out), dict(bias=torch.zeros(25))), ((w, x, out), dict(bias=torch.zeros(24, dtype=torch.bfloat16))),
+                     ((w, x, out), dict(bias=torch.zeros(24, 2)[:, 0])), ((w, x, out), dict(bias=long[1:])),
+                     ((w, x, out), dict(activation=2)), ((w, x, out), dict(activation=-1)), ((w, torch.zeros(40, 6).t(), out), {})):
+        with pytest.raises(ValueError):
+            s.project_step(*args, **kw)
+        assert not steps, (args[1].shape, kw)
+    assert all(cols == 40 for _, cols in s.scratch)
+    assert s.project_step(w, x, out, bias=torch.zeros(24), activation=sd.GELU) is out
+    assert [name for name, _ in steps] == ["load", "multiply"] and steps[0][1] == steps[1][1]
+    del steps[:]
+    s.project_step(w, kept, out[:5])
+    assert steps == [("multiply", kept.codes.data_ptr())]
