@@ -9,6 +9,8 @@ weights held in 4 bits (Mx4Matrix), and rope_step() turns queries and keys that 
 cache.  Nothing here computes: it allocates and calls the library.  Steps of one session share its
 buffers and error word: steps, or graphs of them, that run at the same time need sessions of their own.
 """
+import contextlib
+
 import torch
 
 from . import _binding as sd
@@ -18,6 +20,17 @@ from . import _project as project
 _KINDS = {torch.bfloat16: block.BF16, torch.float32: block.F32}
 
 
+def _memory_of(stream, device):
+    """A context in which new memory is that of `stream`, where it is first written.  The allocator hands out what the current
+    stream has freed at once, in the order of that stream alone: on another one such memory may still be in use."""
+    device = torch.device(device)
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    handle = sd._stream(stream)
+    # 0 and 1 are the names of the legacy default stream
+    return torch.cuda.stream(torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device))
+
+
 class LayerCache:
     """One layer's KV cache: k and v [B][H][(F_s+W)*HW][D] bf16, meta [B][F_s+W][2] int64."""
 
@@ -25,9 +38,10 @@ class LayerCache:
         B, H, D = cfg.batch, cfg.heads, cfg.head_dim
         rows = cfg.slots * cfg.hw
         assert sd.cache_bytes(cfg) == B * H * rows * D * 2
-        self.k = torch.empty((B, H, rows, D), dtype=torch.bfloat16, device=device)
-        self.v = torch.empty((B, H, rows, D), dtype=torch.bfloat16, device=device)
-        self.meta = torch.empty((B, cfg.slots, 2), dtype=torch.int64, device=device)
+        with _memory_of(stream, device):
+            self.k = torch.empty((B, H, rows, D), dtype=torch.bfloat16, device=device)
+            self.v = torch.empty((B, H, rows, D), dtype=torch.bfloat16, device=device)
+            self.meta = torch.empty((B, cfg.slots, 2), dtype=torch.int64, device=device)
         sd.cache_reset(cfg, self.k, self.v, self.meta, stream)
 
 
@@ -113,11 +127,12 @@ class StreamSession:
         self.cfg = cfg
         self.start_frames = [int(s) for s in start_frames]
         B, H, D, nq = cfg.batch, cfg.heads, cfg.head_dim, cfg.nq
-        self.ws = torch.zeros(sd.workspace_bytes(cfg), dtype=torch.uint8, device=device)
+        with _memory_of(stream, device):
+            self.ws = torch.zeros(sd.workspace_bytes(cfg), dtype=torch.uint8, device=device)
+            self.q_rot = torch.empty((B, H, nq, D), dtype=torch.bfloat16, device=device)
+            self.out = torch.empty((B, nq, H, D), dtype=torch.bfloat16, device=device)
         sd.workspace_init(cfg, self.ws, stream)
         self.layers = [LayerCache(cfg, device, stream) for _ in range(layers)]
-        self.q_rot = torch.empty((B, H, nq, D), dtype=torch.bfloat16, device=device)
-        self.out = torch.empty((B, nq, H, D), dtype=torch.bfloat16, device=device)
         self.prompts = [None] * layers
         self.cross_ws = None
         self.norms = {}                # norm_step's configurations, which follow from shapes, types and strides
@@ -157,7 +172,8 @@ class StreamSession:
         lens = [nk] * B if lens is None else [int(n) for n in lens]
         need = block.cross_workspace_bytes(cross)
         if self.cross_ws is None or not need:          # init names what is wrong with a configuration without a size
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.ws.device)
+            with _memory_of(stream, self.ws.device):
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.ws.device)
             block.cross_workspace_init(cross, ws, stream)
             self.cross_ws = ws
         self.prompts[layer] = (cross, k, v, lens)
@@ -198,10 +214,10 @@ class StreamSession:
     def quantize_step(self, x, stream=None):
         """x [...][K] (bf16 or fp32, contiguous) in 4 bits, for several products of the same activations.  What it returns is the
         session's and holds until its next activations of K columns."""
-        return self._activations(x).load(x.view(-1, x.shape[-1]), stream=stream)
+        return self._activations(x, stream).load(x.view(-1, x.shape[-1]), stream=stream)
 
-    def _activations(self, x):
-        """The session's matrix for activations of x's size, whatever it holds."""
+    def _activations(self, x, stream):
+        """The session's matrix for activations of x's size, whatever it holds.  Its memory is that of the stream of its first use."""
         if x.dim() < 1 or not x.is_contiguous() or not x.numel():
             raise ValueError("x must be contiguous and hold at least one row")
         rows, cols = x.numel() // x.shape[-1], x.shape[-1]
@@ -211,7 +227,8 @@ class StreamSession:
             # where that is shorter.  It is kept as long as the session, as graphs may hold it.
             room = max(128, 1 << (rows - 1).bit_length())
             if (room, cols) not in self.scratch:
-                self.scratch[room, cols] = Mx4Matrix(room, cols, self.ws.device)
+                with _memory_of(stream, self.ws.device):
+                    self.scratch[room, cols] = Mx4Matrix(room, cols, self.ws.device)
             m = self.loaded[rows, cols] = self.scratch[room, cols]._first(rows)
         return m
 
@@ -225,7 +242,7 @@ class StreamSession:
         cols = x.cols if loaded else x.shape[-1] if x.dim() else 0
         if cols != weight.cols:
             raise ValueError("x has %d columns, the weight %d" % (cols, weight.cols))
-        a = x if loaded else self._activations(x)
+        a = x if loaded else self._activations(x, stream)
         if out.shape[-1] != weight.rows or out.numel() != a.rows * weight.rows:
             raise ValueError("out is %s, not %d rows of %d" % (tuple(out.shape), a.rows, weight.rows))
         if bias is not None and bias.numel() != weight.rows:

@@ -1,10 +1,12 @@
 """CPU tests of what a session does around its 4-bit products and rotations: what it checks before it computes.  Nothing is
 computed here: there is no GPU."""
+import contextlib
+
 import pytest
 import torch
 
 import streaming_causal_video_gb300 as sd
-from streaming_causal_video_gb300 import _project
+from streaming_causal_video_gb300 import _binding, _block, _project, layer
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -68,3 +70,45 @@ def test_a_refused_product_has_quantised_nothing(steps):
     del steps[:]
     s.project_step(w, kept, out[:5])
     assert steps == [("multiply", kept.codes.data_ptr())]
+
+
+def test_memory_that_a_session_makes_is_that_of_the_stream_it_is_first_written_on(steps, monkeypatch):
+    """Memory of another stream may be what that stream's kernels still use: the allocator orders its reuse on one stream only."""
+    inside, made = [None], []
+
+    @contextlib.contextmanager
+    def memory_of(stream, device):
+        inside[0] = stream
+        yield
+        inside[0] = None
+
+    def recorded(make):
+        def wrapped(*a, **k):
+            made.append(inside[0])
+            return make(*a, **k)
+        return wrapped
+    monkeypatch.setattr(layer, "_memory_of", memory_of, raising=False)
+    for call in ("workspace_init", "cache_reset"):
+        monkeypatch.setattr(_binding, call, lambda *a: None)
+    monkeypatch.setattr(_block, "cross_workspace_init", lambda *a: None)
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
+    x, w, out, kv = torch.ones(200, 40), sd.Mx4Matrix(24, 40, "cpu"), torch.ones(200, 24), torch.ones(1, 9, 2, 128)
+
+    def made_by(f, *a, **k):
+        del made[:]
+        f(*a, **k)
+        return set(made), len(made)
+    s = session()
+    assert made_by(s.quantize_step, x, stream=11) == ({11}, 2)
+    assert made_by(s.quantize_step, x[:150], stream=12) == (set(), 0)
+    assert made_by(s.project_step, w, x[:100], out[:100], stream=13) == ({13}, 2)
+    assert made_by(s.set_prompt, 0, kv, kv, stream=14) == ({14}, 1)
+    assert made_by(sd.StreamSession, s.cfg, 2, [0], "cpu", 15) == ({15}, 9)
+    assert made_by(sd.StreamSession, s.cfg, 1, [0], "cpu") == ({None}, 6)
+
+
+def test_memory_of_no_stream_and_of_no_gpu():
+    for stream, device in ((None, "cuda"), (None, "cuda:1"), (7, "cpu"), (None, torch.device("cpu"))):
+        with layer._memory_of(stream, device):
+            pass
