@@ -44,8 +44,13 @@ class Mx4ProductConfig(_Config):
 
 
 class RopeStrides(ctypes.Structure):
-    """Mirror of sdv2_rope_strides."""
+    """Mirror of sdv2_rope_strides.  Those in a configuration change as a whole, so that what is derived from them does as well."""
     _fields_ = [("token_stride", _i64), ("head_stride", _i64), ("batch_stride", _i64)]
+
+    def __setattr__(self, name, value):
+        if self._b_base_ is not None:
+            raise AttributeError("assign a new RopeStrides to the configuration")
+        super().__setattr__(name, value)
 
 
 class AxesRopeConfig(_Config):

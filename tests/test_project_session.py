@@ -1,5 +1,5 @@
-"""CPU tests of what a session does around its 4-bit products and rotations: what it checks before it computes.  Nothing is
-computed here: there is no GPU."""
+"""CPU tests of what the session and the binding do around 4-bit products and rotations: what they check before anything is
+computed, and where a session's memory comes from.  Nothing is computed here: there is no GPU."""
 import contextlib
 
 import pytest
@@ -112,3 +112,21 @@ def test_memory_of_no_stream_and_of_no_gpu():
     for stream, device in ((None, "cuda"), (None, "cuda:1"), (7, "cpu"), (None, torch.device("cpu"))):
         with layer._memory_of(stream, device):
             pass
+
+
+def test_strides_of_a_rotation_change_as_a_whole():
+    """What the binding checks tensors by is derived from them: a stride that changed behind its back would let a tensor pass that
+    the call runs beyond."""
+    cfg = sd.AxesRopeConfig.make(batch=2, tokens=5, heads=4, head_dim=128, dims=(64, 64))
+    assert cfg.derived()[1][1] == (5 * 512, 512, 128, 1)
+    for name in ("q_in", "q_out", "k_in", "k_out"):
+        for field in ("token_stride", "head_stride", "batch_stride"):
+            with pytest.raises(AttributeError, match="assign a new RopeStrides"):
+                setattr(getattr(cfg, name), field, 4096)
+    assert cfg.q_in.token_stride == 0
+    alone = sd.RopeStrides(token_stride=1024)
+    alone.head_stride = 256
+    cfg.q_in = alone
+    assert (cfg.q_in.token_stride, cfg.q_in.head_stride) == (1024, 256) and cfg.derived()[1][1] == (5 * 1024, 1024, 256, 1)
+    alone.token_stride = 8192                              # the configuration holds a copy
+    assert cfg.q_in.token_stride == 1024
