@@ -129,7 +129,9 @@ typedef struct {
  * by the angle scale[a] * position[a] * base^(-2j/d):
  *   (u, v) -> (u cos - v sin, u sin + v cos).
  * halves = 0: pair j is dims (2j, 2j+1) of its segment; halves = 1: dims (j, j + d/2).
- * Strides are multiples of 8 elements (the token and the head stride at least head_dim) and at most 2^38.
+ * Strides are multiples of 8 elements (the token and the head stride at least head_dim) and at most 2^38.  Rows of a result
+ * (q_out and k_out; of the gradients q_in and k_in) lie apart: ordered by size, each stride of an axis longer than one passes over
+ * all that those before it reach.  Rows that are only read may share memory.
  */
 typedef struct {
     int32_t batch;             /* in [1, 65535]                                                 */

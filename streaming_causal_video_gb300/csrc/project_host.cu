@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "host_checks.h"
 #include "project.h"
@@ -82,6 +83,21 @@ sdv2_status rope_strides(const char* name, const sdv2_axes_rope_cfg* c, int head
                       "(%lld) at least 8, all multiples of 8", name, (long long)s->token_stride, (long long)s->head_stride,
                       (long long)s->batch_stride);
     return SDV2_OK;
+}
+
+// Whether the rows of a result lie apart: from the smallest stride of an axis longer than one on, each passes over all that those
+// before it reach.
+bool rows_apart(const sdv2_axes_rope_cfg* c, int heads, const sdv2_rope_strides& s)
+{
+    std::pair<int64_t, int64_t> axis[3] = {{s.head_stride, heads}, {s.token_stride, c->tokens}, {s.batch_stride, c->batch}};
+    std::sort(axis, axis + 3);
+    __int128 reach = c->head_dim;
+    for (const auto& [stride, n] : axis) {
+        if (n == 1) continue;
+        if (stride < reach) return false;
+        reach += static_cast<__int128>(n - 1) * stride;
+    }
+    return true;
 }
 
 sdv2_status check_rope(const sdv2_axes_rope_cfg* c)
@@ -226,6 +242,9 @@ sdv2_status rope_call(const sdv2_axes_rope_cfg* c, const int32_t* positions, con
         if ((s = rope_strides(t ? "k_in" : "q_in", c, heads, *ends[t][0], &in)) != SDV2_OK) return s;
         if ((s = rope_strides(t ? "k_out" : "q_out", c, heads, *ends[t][1], &out)) != SDV2_OK) return s;
         p.t[t] = {t ? k : q, t ? k_new : q_new, backward ? out : in, backward ? in : out};
+        if (!rows_apart(c, heads, p.t[t].os))
+            return refuse(SDV2_ERR_INVALID_ARG, "rows of %c_%s overlap: a stride must pass over all that the smaller ones reach", t ? 'k' : 'q',
+                          backward ? "in" : "out");
         if (!given(p.t[t].in) || !given(p.t[t].out))
             return refuse(SDV2_ERR_INVALID_ARG, "device pointers must be non-null and 16-byte aligned");
         if (p.t[t].in == p.t[t].out && (in.token_stride != out.token_stride || in.head_stride != out.head_stride ||
