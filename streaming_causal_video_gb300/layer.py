@@ -269,6 +269,8 @@ class StreamSession:
         c = self.cfg
         if len(chunk_index) != c.batch:
             raise ValueError("%d chunk indexes for %d streams" % (len(chunk_index), c.batch))
+        if min(chunk_index) < 0:
+            raise ValueError("chunk indexes must be >= 0, not %s" % (list(chunk_index),))
         n = torch.arange(c.nq)
         grid = torch.stack([n // c.hw, n % c.hw // c.grid_w, n % c.grid_w], -1)
         pos = grid.expand(c.batch, c.nq, 3).clone()

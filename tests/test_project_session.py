@@ -130,3 +130,13 @@ def test_strides_of_a_rotation_change_as_a_whole():
     assert (cfg.q_in.token_stride, cfg.q_in.head_stride) == (1024, 256) and cfg.derived()[1][1] == (5 * 1024, 1024, 256, 1)
     alone.token_stride = 8192                              # the configuration holds a copy
     assert cfg.q_in.token_stride == 1024
+
+
+@pytest.mark.parametrize("refresh", [0, 5])
+def test_there_are_no_places_before_the_first_chunk(refresh):
+    """layer_step refuses such a chunk; with a refresh every 5 chunks, chunk -1 would look like chunk 4."""
+    s = session(batch=2, refresh_chunks=refresh)
+    for chunks in ([0, -1], [-5, 0], (-1, -1)):
+        with pytest.raises(ValueError, match="must be >= 0"):
+            s.chunk_positions(chunks)
+    assert s.chunk_positions((0, 3))[1, 0].tolist() == [13, 0, 0]
