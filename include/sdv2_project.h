@@ -113,6 +113,15 @@ sdv2_status sdv2_mx4_product(const sdv2_mx4_product_cfg* cfg, const void* a_code
                              const void* b_codes, const void* b_scales, const float* bias, void* out, void* ws,
                              void* stream);
 
+/*
+ * How sdv2_mx4_product runs a configuration on a GB300, for tests and measurements; host only.
+ *   plan[0]: 16, 32 or 64 where the rows of a, at most that many, are the columns of the MMAs; otherwise
+ *            128, 192 or 256, the rows of b in a tile of 256 rows of a;
+ *   plan[1]: the parts that the depth of each tile is cut in;
+ *   plan[2]: the most tiles that a pair of SMs takes one after another (1 for the few rows).
+ */
+sdv2_status sdv2_debug_mx4_plan(const sdv2_mx4_product_cfg* cfg, int32_t* plan);
+
 /* ---- rotary positions of several axes ------------------------------------------------------- */
 
 /* Element (b, n, h, d) lies batch_stride*b + token_stride*n + head_stride*h + d elements after a tensor's pointer.  0

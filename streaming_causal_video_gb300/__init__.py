@@ -56,6 +56,7 @@ from ._project import (  # noqa: F401
     RopeStrides,
     axes_rope,
     axes_rope_backward,
+    debug_mx4_plan,
     mx4_codes_bytes,
     mx4_dequantize,
     mx4_product,

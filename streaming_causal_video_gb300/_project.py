@@ -12,8 +12,8 @@ NO_ACTIVATION, GELU = 0, 1     # sdv2_activation
 
 # Every symbol that include/sdv2_project.h declares.
 PROJECT_EXPORTS = ["sdv2_mx4_codes_bytes", "sdv2_mx4_scales_bytes", "sdv2_mx4_quantize", "sdv2_mx4_dequantize",
-                   "sdv2_mx4_workspace_bytes", "sdv2_mx4_workspace_init", "sdv2_mx4_product", "sdv2_axes_rope",
-                   "sdv2_axes_rope_backward"]
+                   "sdv2_mx4_workspace_bytes", "sdv2_mx4_workspace_init", "sdv2_mx4_product", "sdv2_debug_mx4_plan",
+                   "sdv2_axes_rope", "sdv2_axes_rope_backward"]
 
 _i32, _i64, _f64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
 
@@ -106,6 +106,7 @@ def _lib():
                  "sdv2_mx4_workspace_bytes": (ctypes.c_size_t, [prodp]),
                  "sdv2_mx4_workspace_init": (ctypes.c_int, [prodp, _vp, _vp]),
                  "sdv2_mx4_product": (ctypes.c_int, [prodp] + [_vp] * 8),
+                 "sdv2_debug_mx4_plan": (ctypes.c_int, [prodp, ctypes.POINTER(_i32)]),
                  "sdv2_axes_rope": (ctypes.c_int, [ropep] + [_vp] * 6),
                  "sdv2_axes_rope_backward": (ctypes.c_int, [ropep] + [_vp] * 6)}
         for name, (res, args) in types.items():
@@ -125,6 +126,13 @@ def mx4_scales_bytes(cfg: Mx4Config) -> int:
 
 def mx4_workspace_bytes(cfg: Mx4ProductConfig) -> int:
     return _lib().sdv2_mx4_workspace_bytes(ctypes.byref(cfg))
+
+
+def debug_mx4_plan(cfg: Mx4ProductConfig):
+    """(width, parts, rounds): how mx4_product runs a configuration, as sdv2_debug_mx4_plan tells; host only."""
+    plan = (_i32 * 3)()
+    _b._check(_lib().sdv2_debug_mx4_plan(cfg, plan), "sdv2_debug_mx4_plan")
+    return tuple(plan)
 
 
 def mx4_workspace_init(cfg, ws, stream=None):

@@ -580,12 +580,6 @@ bool mx4_scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int til
     return encode_tensor_map_of(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, map, base, 3, dims, strides, box);
 }
 
-namespace {
-
-struct Plan {
-    int tn, splits;
-};
-
 // Rows of b in a tile, and parts of the depth, by an estimate of the time in nanoseconds: what a step and a tile were measured to
 // take.  Tiles of fewer rows read more for the same work, but have less to wait for and fill the pairs evenly at other sizes; us with
 // 256, 192 and 128 rows: 4680 x 5120 of depth 5120 39.1, 42.1 and 52.5, 4680 x 1536 of depth 1536 9.1, 8.5 and 9.6, 1536 x 1536 of depth
@@ -593,16 +587,16 @@ struct Plan {
 // clusters of four CTAs and 15 of eight at once), if that saves more than the exchange of their sums from SM to SM, at 25 bytes a
 // nanosecond, and what comes with it cost: 512 x 512 of depth 8192 10.9 us in one part, 10.1 in two and 9.8 in four, 512 x 1536 of
 // depth 4096 7.7 in one and 9.1 in two.
-Plan plan_of(int64_t M, int64_t N, int tiles)
+Mx4Plan mx4_product_plan(int64_t M, int64_t N, int tiles)
 {
     const int64_t mtiles = (M + TM - 1) / TM;
     const int steps = (tiles + STEP_TILES - 1) / STEP_TILES;
-    Plan best{256, 1};
+    Mx4Plan best{256, 1, 1};
     double least = 0;
-    auto offer = [&](int tn, int splits, double time) {
+    auto offer = [&](int tn, int parts, int64_t rounds, double time) {
         if (least == 0 || time < least) {
             least = time;
-            best = {tn, splits};
+            best = {tn, parts, static_cast<int>(rounds)};
         }
     };
     constexpr struct {
@@ -610,27 +604,25 @@ Plan plan_of(int64_t M, int64_t N, int tiles)
         double step, tile;
     } kinds[] = {{256, 290, 1380}, {192, 225, 1000}, {128, 200, 750}};
     for (const auto& kind : kinds) {
-        const int64_t units = mtiles * ((N + kind.tn - 1) / kind.tn);
-        offer(kind.tn, 1, static_cast<double>((units + kPairs - 1) / kPairs) * (kind.step * steps + kind.tile));
+        const int64_t rounds = (mtiles * ((N + kind.tn - 1) / kind.tn) + kPairs - 1) / kPairs;
+        offer(kind.tn, 1, rounds, static_cast<double>(rounds) * (kind.step * steps + kind.tile));
     }
     const int64_t units = mtiles * ((N + 127) / 128);
     const double exchange = static_cast<double>(std::min<int64_t>(M, CM) * 128 * 4) / 25;     // of all sums
-    if (units <= 36 && steps >= 2) offer(128, 2, 200.0 * ((steps + 1) / 2) + 750 + 1500 + exchange / 2);
-    if (units <= 15 && steps >= 4) offer(128, 4, 200.0 * ((steps + 3) / 4) + 750 + 2200 + exchange * 3 / 4);
+    if (units <= 36 && steps >= 2) offer(128, 2, 1, 200.0 * ((steps + 1) / 2) + 750 + 1500 + exchange / 2);
+    if (units <= 15 && steps >= 4) offer(128, 4, 1, 200.0 * ((steps + 3) / 4) + 750 + 2200 + exchange * 3 / 4);
     return best;
 }
-
-}  // namespace
 
 cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
 {
     ProductParams p{};
     p.M = static_cast<int32_t>(q.M);
     p.N = static_cast<int32_t>(q.N);
-    const Plan plan = plan_of(q.M, q.N, q.tiles);
-    const int32_t mtiles = static_cast<int32_t>((q.M + TM - 1) / TM), ntiles = static_cast<int32_t>((q.N + plan.tn - 1) / plan.tn);
+    const Mx4Plan plan = mx4_product_plan(q.M, q.N, q.tiles);
+    const int32_t mtiles = static_cast<int32_t>((q.M + TM - 1) / TM), ntiles = static_cast<int32_t>((q.N + plan.width - 1) / plan.width);
     p.steps = (q.tiles + STEP_TILES - 1) / STEP_TILES;
-    p.splits = plan.splits;
+    p.splits = plan.parts;
     p.bias = q.bias;
     p.gelu = q.gelu;
     p.err = q.err;
@@ -641,16 +633,16 @@ cudaError_t launch_mx4_product(const Mx4Product& q, cudaStream_t s)
     p.m_fastest = q.N > q.M;
     p.inner = p.m_fastest ? mtiles : ntiles;
     p.units = mtiles * ntiles * p.splits;
-    if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, CM) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, plan.tn / 2) ||
-        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, plan.tn == 128 ? 1 : 2))
+    if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, CM) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, plan.width / 2) ||
+        !mx4_scales_map(&p.as, q.as, q.M, q.tiles, STEP_TILES, 1) || !mx4_scales_map(&p.bs, q.bs, q.N, q.tiles, STEP_TILES, plan.width == 128 ? 1 : 2))
         return cudaErrorInvalidValue;
     const int64_t size = q.out_f32 ? 4 : 2, pitch = q.out_stride * size;
     // (a store's last 16 bytes of a row are written whole)
     if ((pitch | q.N * size) % 16 != 0 || pitch > (int64_t(1) << 39) / q.M) p.direct = q.out;
     else if (!out_map(&p.out, q.out, q.out_f32, q.M, q.N, q.out_stride)) return cudaErrorInvalidValue;
     if (p.splits > 1) return q.out_f32 ? launch<128, true, true>(p, s) : launch<128, false, true>(p, s);
-    if (plan.tn == 128) return q.out_f32 ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
-    if (plan.tn == 256) return q.out_f32 ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
+    if (plan.width == 128) return q.out_f32 ? launch<128, true, false>(p, s) : launch<128, false, false>(p, s);
+    if (plan.width == 256) return q.out_f32 ? launch<256, true, false>(p, s) : launch<256, false, false>(p, s);
     return q.out_f32 ? launch<192, true, false>(p, s) : launch<192, false, false>(p, s);
 }
 

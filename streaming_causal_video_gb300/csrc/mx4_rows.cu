@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, 1) rows_kernel(const __grid_constant_
 }
 
 template <int COLS>
-cudaError_t launch(const Mx4Product& q, cudaStream_t s)
+cudaError_t launch(const Mx4Product& q, int parts, cudaStream_t s)
 {
     RowsParams p{};
     if (!mx4_codes_map(&p.a, q.a, q.M, q.tiles, COLS) || !mx4_codes_map(&p.b, q.b, q.N, q.tiles, ROWS) ||
@@ -270,11 +270,7 @@ cudaError_t launch(const Mx4Product& q, cudaStream_t s)
     p.out_f32 = q.out_f32;
     p.gelu = q.gelu;
     const int64_t clusters = (q.N + ROWS - 1) / ROWS;
-    // Parts of the depth for as many CTAs as the GPU holds (two an SM), of two steps at least, where that saves more steps than the
-    // exchange costs: 3 rows at 5120 x 20480 take 23.4 us in one part and 12.3 in four, at 512 x 4096 (16 steps) 4.2 in one, 3.9 in
-    // two, 3.4 in four and 3.2 in eight, at 1536 x 1536 (six) 2.9 in one and 3.3 in two.
-    p.parts = 1;
-    while (p.parts < kMaxParts && clusters * p.parts * 2 <= 304 && p.steps >= std::max(12, 4 * p.parts)) p.parts *= 2;
+    p.parts = parts;
     constexpr int kBytes = static_cast<int>(Stage<COLS>::SMEM_BYTES);
     static PerDevice once;
     int dev = 0;
@@ -297,9 +293,22 @@ cudaError_t launch(const Mx4Product& q, cudaStream_t s)
 
 }  // namespace
 
+// Parts of the depth for as many CTAs as the GPU holds (two an SM), of two steps at least, where that saves more steps than the
+// exchange costs: 3 rows at 5120 x 20480 take 23.4 us in one part and 12.3 in four, at 512 x 4096 (16 steps) 4.2 in one, 3.9 in
+// two, 3.4 in four and 3.2 in eight, at 1536 x 1536 (six) 2.9 in one and 3.3 in two.
+Mx4Plan mx4_rows_plan(int64_t M, int64_t N, int tiles)
+{
+    const int64_t clusters = (N + ROWS - 1) / ROWS;
+    const int steps = (tiles + STEP_TILES - 1) / STEP_TILES;
+    int parts = 1;
+    while (parts < kMaxParts && clusters * parts * 2 <= 304 && steps >= std::max(12, 4 * parts)) parts *= 2;
+    return {M <= 16 ? 16 : M <= 32 ? 32 : 64, parts, 1};
+}
+
 cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s)
 {
-    return p.M <= 16 ? launch<16>(p, s) : p.M <= 32 ? launch<32>(p, s) : launch<64>(p, s);
+    const Mx4Plan plan = mx4_rows_plan(p.M, p.N, p.tiles);
+    return plan.width == 16 ? launch<16>(p, plan.parts, s) : plan.width == 32 ? launch<32>(p, plan.parts, s) : launch<64>(p, plan.parts, s);
 }
 
 }  // namespace sdv2

@@ -47,6 +47,15 @@ struct Mx4Product {
 // 5120 x 5120 8.6 and 8.7, at 9216 x 1536 5.9 and 6.7, at 1536 x 1536 4.3 and 4.6; fewer rows are further apart.
 constexpr int kMx4FewRows = 64;
 
+// How a product runs: rows of b in a tile (of few rows: columns of an MMA, as many rows of a at most), parts of the depth, and the
+// most tiles of a pair of SMs.
+struct Mx4Plan {
+    int width, parts, rounds;
+};
+
+Mx4Plan mx4_rows_plan(int64_t M, int64_t N, int tiles);
+Mx4Plan mx4_product_plan(int64_t M, int64_t N, int tiles);
+
 // Few rows of a.
 cudaError_t launch_mx4_rows(const Mx4Product& p, cudaStream_t s);
 

@@ -355,6 +355,20 @@ sdv2_status sdv2_mx4_product(const sdv2_mx4_product_cfg* c, const void* a_codes,
     return launched(p.M <= kMx4FewRows ? launch_mx4_rows(p, st) : launch_mx4_product(p, st), "4-bit product launch");
 }
 
+sdv2_status sdv2_debug_mx4_plan(const sdv2_mx4_product_cfg* c, int32_t* plan)
+{
+    const sdv2_status s = check_product(c);
+    if (s != SDV2_OK) return s;
+    if (!plan) return refuse(SDV2_ERR_INVALID_ARG, "plan is NULL");
+    const int tiles = tiles_of(c->depth);
+    const Mx4Plan p = c->rows <= kMx4FewRows ? mx4_rows_plan(c->rows, c->cols, tiles) : mx4_product_plan(c->rows, c->cols, tiles);
+    plan[0] = p.width;
+    plan[1] = p.parts;
+    plan[2] = p.rounds;
+    set_last_error("");
+    return SDV2_OK;
+}
+
 sdv2_status sdv2_axes_rope(const sdv2_axes_rope_cfg* c, const int32_t* positions, const void* q, void* q_out, const void* k,
                            void* k_out, void* stream)
 {
