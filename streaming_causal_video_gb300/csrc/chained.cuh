@@ -5,8 +5,8 @@
 // memory that the call's own launches write); calls in a row measured, unchained and
 // chained, in a stream: cross attention 480p 23.4 and 21.3 us, 720p 60.1 and 57.6, layer norm of 4680 x 5120 35.1 and
 // 32.4.  A launch that lets the next one start before its own blocks are done (launch_dependents) is faster inside the
-// backward passes, where a comment says so, and no faster or slower elsewhere (cross attention of the ragged batch:
-// 42.8 us without, 46.0 with).
+// backward passes, in 4-bit quantisation of rows, in the 4-bit products and in the rotations, where comments say so, and no
+// faster or slower elsewhere (cross attention of the ragged batch: 42.8 us without, 46.0 with).
 #pragma once
 
 #include <cuda_runtime.h>

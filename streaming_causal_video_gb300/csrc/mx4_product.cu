@@ -13,8 +13,8 @@
 //   whole 16 bytes.
 // What bounds a deep product is the ring: a stage's memory comes round again after 1.4 us, its MMAs and the way of its next copies, so
 // that five stages of 256 x 256 give one in 288 ns (four 340, six 280), where the MMAs take 262 (512 cycles) and shared memory, which
-// they read while copies write it, little less.  4680 x 5120 of depth 20480 takes 127 us (7.7 PFLOP/s; 127.5 at four times the rate
-// that bf16 products reach), of depth 5120 39 us.  Shallow ones have the start and the end of tiles as well: 4680 x
+// they read while copies write it, little less.  4680 x 5120 of depth 20480 takes 127 us in bursts of 5 ms at 2070 MHz (7.7 PFLOP/s; the
+// MMAs alone 105) and 142 back to back, where the power limit holds the SMs at 1620 to 1680 MHz; of depth 5120 39 us.  Shallow ones have the start and the end of tiles as well: 4680 x
 // 6144 of depth 1536 takes 21.3 us to bf16, 23.4 with GELU and 27.1 to fp32; 4680 x 1536 of depth 1536 8.6.
 // Where tiles are fewer than pairs, the depth is cut into two or four parts, one for each pair of a larger cluster.  Their sums are
 // exchanged through shared memory when the ring is free, and each pair adds up and writes its share of the columns, in the order of
@@ -585,8 +585,8 @@ bool mx4_scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int til
 // 256, 192 and 128 rows: 4680 x 5120 of depth 5120 39.1, 42.1 and 52.5, 4680 x 1536 of depth 1536 9.1, 8.5 and 9.6, 1536 x 1536 of depth
 // 4680 11.6, 10.3 and 9.7.  Where even tiles of 128 rows are few, two or four pairs may share the depth of each (the GPU holds 36
 // clusters of four CTAs and 15 of eight at once), if that saves more than the exchange of their sums from SM to SM, at 25 bytes a
-// nanosecond, and what comes with it cost: 512 x 512 of depth 8192 10.9 us in one part, 10.1 in two and 9.8 in four, 512 x 1536 of
-// depth 4096 7.7 in one and 9.1 in two.
+// nanosecond, and what comes with it cost; us in one part, two and four: 512 x 512 of depth 8192 10.6, 9.6 and 9.0, of depth 4096 6.9, 7.5
+// and 7.7; 512 x 1536 of depth 12288 14.1 and 12.0, of depth 4096 7.5 and 8.6; 1000 x 1000 of depth 8192 11.0 and 10.7.
 Mx4Plan mx4_product_plan(int64_t M, int64_t N, int tiles)
 {
     const int64_t mtiles = (M + TM - 1) / TM;

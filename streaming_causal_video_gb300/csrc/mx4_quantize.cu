@@ -9,6 +9,7 @@
 // slower with it: a transpose of 4680 x 1536 behind another one 5.1 and 6.3.)
 // 4680 x 5120 takes 16.9 us from fp32 (6.4 TB/s) and 11.5 from bf16 (5.3 TB/s; 2.9 instructions a
 // cycle and SM, so that both count), its values 10.7 to bf16 and 21.7 to fp32; 4680 x 1536 bf16 takes 4.6 us, its transpose 5.1.
+// Transposes to 20480 x 4680 take 41.4 us from bf16 (5.9 TB/s) and 63.7 from fp32 (6.8).
 // A row that is not whole vectors of 8 columns goes by way of shared memory, 16 neighbouring words of 4 bytes at once, from which
 // bf16 rows that begin on odd places are shifted (4680 x 5111 14.4 us, its values 13.2; number by number 22.5 and 19.5).
 #include <cuda_bf16.h>
@@ -399,6 +400,7 @@ cudaError_t launch_mx4_dequantize(const Mx4Params& p, cudaStream_t s)
 {
     // The same, us with one, two and four: 4680 x 5120 to fp32 21.7, 22.8 and 23.2, to bf16 15.1, 11.7 and 10.7; rows without vectors
     // 4680 x 5111 24.4, 23.2 and 22.4, and 18.7, 15.0 and 13.2; 1001 x 1050 (nine tiles) 2.3, 2.5 and 2.8, and 1.8, 1.7 and 1.9
+    // (fp32 without vectors: two for all sizes, within 4 and 9 % of the best of these)
     const int unroll = p.f32 ? (p.vectors ? 1 : 2) : fills_four(p) && blocks_of(p, 4) >= 152 ? 4 : 2;
     RowsKernel kernel;
     if (p.f32) kernel = p.vectors ? dequantize_kernel<true, true, 1> : dequantize_kernel<true, false, 2>;

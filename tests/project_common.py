@@ -6,8 +6,8 @@ Bounds:
 * a rounding is off by at most half a step, 2^-8 of the value for bf16 and 2^-24 for fp32;
 * products of 4-bit numbers are exact.  The tensor cores add 64 of them to a 32-bit sum at a time, each addend cut off at 2^-24
   of the largest at the latest, so that a step is off by at most 65 * 2^-24 < 2^-17.9 of the sum of the magnitudes so far, and a
-  sum of K by ceil(K/64) steps of that.  (The CUDA cores' sums of 32 are exact and their 32-bit additions off by 2^-24 each.)  Parts
-  of the depth add one rounding each, at most 76 in all, which 2^-17 covers beside a part's fewer steps;
+  sum of K by ceil(K/64) steps of that.  Parts of the depth add one rounding of 2^-24 each, at most eight (2^-21) in all; the 2^-17 of
+  the bound covers them many times over;
 * gelu's exponential and division add a few 2^-22 of the result, and as the argument of the exponential grows with y^3, an error of
   its argument of 2^-22 relative to the 2u <= 100 for which the result is not zero: 2^-15; its slope is at most 1.13;
 * a sine or cosine is off by at most 2^-22 (its own error of 2 steps and its angle's of 2^-27 of a turn), and the rotation rounds
