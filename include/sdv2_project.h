@@ -72,7 +72,8 @@ sdv2_status sdv2_mx4_dequantize(const sdv2_mx4_cfg* cfg, const void* codes, cons
 
 typedef enum {
     SDV2_NO_ACTIVATION = 0,
-    SDV2_GELU = 1              /* y/2 * (1 + tanh(sqrt(2/pi) * (y + 0.044715 y^3)))             */
+    SDV2_GELU = 1              /* y/2 * (1 + tanh(sqrt(2/pi) * (y + 0.044715 y^3))); y below     */
+                               /* -7.2 as -7.2, whose result is -2^-52                          */
 } sdv2_activation;
 
 typedef struct {

@@ -8,6 +8,8 @@ which stay for all chunks and steps until the prompt changes.  project_step() mu
 weights held in 4 bits (Mx4Matrix), and rope_step() turns queries and keys that do not go into the
 cache.  Nothing here computes: it allocates and calls the library.  Steps of one session share its
 buffers and error word: steps, or graphs of them, that run at the same time need sessions of their own.
+What a session allocates is the memory of the stream that the call names (the current one by default):
+before a session is dropped, any other stream that it was used on has to be waited for.
 """
 import contextlib
 
